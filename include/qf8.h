@@ -350,6 +350,105 @@ qf8_status dequantize_mxfp4(const uint8_t *q, const uint8_t *sb, int64_t rows, i
 qf8_status dequantize_nvfp4(const uint8_t *q, const uint8_t *s_blk, const float *tensor_scale, int64_t rows,
                             int64_t cols, void *out, qf8_out_dtype out_dtype, void *stream);
 
+/* ---- matrix products of FP8 codes under group scales ------------------------------------------
+ * With v = decode(code) / S, S the fp32 scale of the code's group as quantize_block writes it:
+ *   y[i][j] = sum_{l < k} a[i][l] * b(l, j),
+ * one group of 128 along k after the other, each group's sum of products times 1/Sa * 1/Sb (both
+ * reciprocals and their product rounded to fp32), the groups summed in fp32. y is rounded once to
+ * BF16 or stored as FP32. The same call gives the same bits.
+ * Precision inside a group: with QF8_OUT_FP32 the products are exact and summed in fp32. With
+ * QF8_OUT_BF16 the sums are those of the FP8 matrix instructions, which align each 8 neighbouring
+ * products to the largest of them and keep 14 bits: an error of at most 2^-10, about 2^-16 on normal
+ * data, of sum |a||b|, far below the rounding to BF16 unless the sum cancels.
+ * a: codes [m][k] of fmt_a in 1x128 groups, scales sa [m][ceil(k/128)]. b by kind:
+ *   QF8_WEIGHT_NK  codes [n][k], 128x128 blocks, sb [ceil(n/128)][ceil(k/128)]: y = a b^T, a layer's
+ *                  forward product
+ *   QF8_WEIGHT_KN  codes [k][n], 128x128 blocks, sb [ceil(k/128)][ceil(n/128)]: y = a b, the input
+ *                  gradient with the weight as the forward pass stores it
+ *   QF8_GROUPS_NK  codes [n][k], 1x128 groups, sb [n][ceil(k/128)]: y = a b^T, the weight gradient
+ *                  (both operands in groups along the tokens)
+ * flags: QF8_FLAG_POW2_SCALES says that every scale is a power of two; then the exponents of sa and
+ * sb alone may be read (the matrix core applies them). A factor 1/Sa * 1/Sb below
+ * 2^-126 is held as a subnormal. NaN and Inf codes give what fp32 arithmetic gives.
+ * k % 4 == 0, for QF8_WEIGHT_KN also n % 4 == 0; k, n <= 2^22; m < 2^31; k = 0 gives zeros. a, b, y and
+ * ws 16-byte aligned, scales 4-byte; y overlaps no input.
+ * ws: matmul_block_workspace_bytes() bytes (0: ws may be NULL): the partial sums of a product whose
+ * k is split over workgroups; it needs no initialisation. */
+typedef enum qf8_operand { QF8_WEIGHT_NK = 0, QF8_WEIGHT_KN = 1, QF8_GROUPS_NK = 2 } qf8_operand;
+
+size_t matmul_block_workspace_bytes(int64_t m, int64_t n, int64_t k, qf8_operand kind,
+                                    qf8_out_dtype out_dtype);
+qf8_status matmul_block(const uint8_t *a, const float *sa, const uint8_t *b, const float *sb, int64_t m, int64_t n,
+                        int64_t k, qf8_fmt fmt_a, qf8_fmt fmt_b, qf8_operand kind, int flags, void *y,
+                        qf8_out_dtype out_dtype, void *ws, size_t ws_bytes, void *stream);
+
+/* The same product with one b for each expert (b [experts] of the layouts above, sb likewise; kind
+ * QF8_WEIGHT_NK or QF8_WEIGHT_KN). Rows [offsets[e], offsets[e+1]) of y [nrows][n] belong to expert e
+ * (offsets: experts + 1 device int32, not decreasing); rows that belong to none are zeros. Row i
+ * reads row rows[i] of a [tokens][k] (an entry outside [0, tokens): a row of zeros); with rows NULL it
+ * reads row i and tokens must be nrows. experts <= 1024, tokens * k < 2^32 with rows. The row counts stay on the device: nothing
+ * synchronizes. */
+qf8_status matmul_block_experts(const uint8_t *a, const float *sa, int64_t tokens, const uint8_t *b, const float *sb,
+                                const int32_t *offsets, int experts, const int32_t *rows, int64_t nrows, int64_t n,
+                                int64_t k, qf8_fmt fmt_a, qf8_fmt fmt_b, qf8_operand kind, int flags, void *y,
+                                qf8_out_dtype out_dtype, void *stream);
+
+/* Weight gradients of the experts: y[e] = at[:, r_e] bt[:, r_e]^T with r_e = [offsets[e], offsets[e+1]).
+ * at: codes [m][nrows], bt: codes [n][nrows], both in 1x128 groups along the rows (scales
+ * [m or n][ceil(nrows/128)]), so every offset is a multiple of 128 (others are rounded down at the
+ * start of an expert). y [experts][m][n]; an expert without rows gets zeros. nrows % 4 == 0. */
+qf8_status matmul_block_experts_wgrad(const uint8_t *at, const float *sat, const uint8_t *bt, const float *sbt,
+                                      const int32_t *offsets, int experts, int64_t nrows, int64_t m, int64_t n,
+                                      qf8_fmt fmt_a, qf8_fmt fmt_b, int flags, void *y, qf8_out_dtype out_dtype,
+                                      void *stream);
+
+/* ---- the expert layer around its products -------------------------------------------------------
+ * Scores of the experts (softmax over the row or sigmoid, fp64 from the logits) and the choice of
+ * top_k of them per token: choice = score + bias[e] (bias nullable fp32, for balance); with groups > 1
+ * the experts are groups of experts/groups neighbours, a group is worth the sum of its two best
+ * choices, and only the experts of the best top_groups groups can be chosen. Equal values: the lower
+ * index first. ids [tokens][top_k] come in falling order of the choice, weights [tokens][top_k] are
+ * scale * score, with renorm divided by the sum of the chosen scores (0 if that sum is 0).
+ * A logit of -Inf or NaN has score 0 and comes after every number; +Inf reads as the largest finite
+ * value; a row without finite logits gets the lowest indices and, with softmax, weights 0.
+ * experts <= 1024, groups <= 64 and a divisor of experts, top_k <= 64 and <= top_groups * experts /
+ * groups. logits [tokens][experts] BF16 or FP32. */
+typedef enum qf8_score { QF8_SCORE_SOFTMAX = 0, QF8_SCORE_SIGMOID = 1 } qf8_score;
+
+qf8_status route_experts(const void *logits, qf8_dtype dtype, int64_t tokens, int experts, int top_k, qf8_score score,
+                         const float *bias, int groups, int top_groups, int renorm, float scale, int32_t *ids,
+                         float *weights, void *stream);
+
+/* Gradient of the logits from dweights [tokens][top_k], for the ids of route_experts (the choice
+ * itself has no gradient; an id outside [0, experts) contributes nothing). dlogits: the logits' type. */
+qf8_status route_experts_backward(const void *logits, qf8_dtype dtype, int64_t tokens, int experts, const int32_t *ids,
+                                  const float *dweights, int top_k, qf8_score score, int renorm, float scale,
+                                  void *dlogits, void *stream);
+
+/* Rows by expert: the tokens x top_k choices sorted by expert, in the order of the tokens, every
+ * expert's rows starting at a multiple of align. offsets [experts + 1]: first row of each expert and the
+ * end; rows [nrows]: token of each row, -1 where a row holds none (padding, and from offsets[experts]
+ * on); slots [tokens][top_k]: the row of each choice (-1 for an id outside [0, experts)).
+ * nrows >= order_experts_rows(): (n + min(experts, n) (align - 1)) rounded up to align for n = tokens *
+ * top_k choices, and below 2^31. ws: order_experts_workspace_bytes() bytes (0: ws may be NULL), 16-byte aligned,
+ * no initialisation. experts, align <= 1024. */
+int64_t order_experts_rows(int64_t tokens, int top_k, int experts, int align);
+size_t order_experts_workspace_bytes(int64_t tokens, int top_k, int experts);
+qf8_status order_experts(const int32_t *ids, int64_t tokens, int top_k, int experts, int align, int32_t *offsets,
+                         int32_t *rows, int64_t nrows, int32_t *slots, void *ws, size_t ws_bytes, void *stream);
+
+/* Weighted sum: y[t] = sum_j weights[t][j] * x[slots[t][j]], in fp32, rounded once to x's type. x
+ * [nrows][dim], y [tokens][dim]; a slot outside [0, nrows) adds nothing. */
+qf8_status combine_experts(const void *x, qf8_dtype dtype, int64_t nrows, int64_t dim, const float *weights,
+                           const int32_t *slots, int64_t tokens, int top_k, void *y, void *stream);
+
+/* Its gradients: dx[slots[t][j]] = weights[t][j] * dy[t] (x's type), dweights[t][j] = dy[t] . x[slots[t][j]]
+ * (fp32; 0 for a slot outside [0, nrows)). Rows of dx whose entry of rows [nrows] is no token are zeros;
+ * rows and slots are those of one order_experts call. */
+qf8_status combine_experts_backward(const void *dy, const void *x, qf8_dtype dtype, int64_t nrows, int64_t dim,
+                                    const float *weights, const int32_t *slots, const int32_t *rows, int64_t tokens,
+                                    int top_k, void *dx, float *dweights, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,9 @@ __all__ = [
     "EST_MAX", "EST_RECENT", "EST_MEAN", "DELAYED_SPLIT_AMAX",
     "quantize_block", "quantize_mx_dual", "quantize_mxfp4_dual", "quantize_nvfp4", "dequantize_mxfp4",
     "dequantize_nvfp4",
+    "WEIGHT_NK", "WEIGHT_KN", "GROUPS_NK", "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "matmul_block", "matmul_block_experts", "matmul_block_experts_wgrad",
+    "route_experts", "route_experts_backward", "order_experts", "combine_experts", "combine_experts_backward",
 ]
 
 E4M3, E5M2 = 0, 1
@@ -29,6 +32,8 @@ ROUND_DOWN, ROUND_UP = 0, 1
 FLAG_POW2_SCALES = 1
 EST_MAX, EST_RECENT, EST_MEAN = 0, 1, 2   # delayed-scaling estimators (qf8_estimator)
 DELAYED_SPLIT_AMAX = 1                    # qf8_delayed_flags
+WEIGHT_NK, WEIGHT_KN, GROUPS_NK = 0, 1, 2  # qf8_operand: layout of the second operand of a product
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1       # qf8_score
 _BF16, _FP32 = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -85,6 +90,18 @@ def _load():
         "dequantize_scaled": (i32, [vp, i64, i32, vp, vp, i32, vp, i32, vp, vp, sz, vp]),
         "dequantize_block": (i32, [vp, i64, i64, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, sz, vp]),
         "dequantize_mx": (i32, [vp, vp, i64, i64, i32, vp, i32, vp, i32, vp, vp, sz, vp]),
+        "matmul_block_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
+        "matmul_block": (i32, [vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, vp, i32, vp, sz, vp]),
+        "matmul_block_experts": (i32, [vp, vp, i64, vp, vp, vp, i32, vp, i64, i64, i64, i32, i32, i32, i32, vp, i32,
+                                       vp]),
+        "matmul_block_experts_wgrad": (i32, [vp, vp, vp, vp, vp, i32, i64, i64, i64, i32, i32, i32, vp, i32, vp]),
+        "route_experts": (i32, [vp, i32, i64, i32, i32, i32, vp, i32, i32, i32, ctypes.c_float, vp, vp, vp]),
+        "route_experts_backward": (i32, [vp, i32, i64, i32, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp]),
+        "order_experts_rows": (i64, [i64, i32, i32, i32]),
+        "order_experts_workspace_bytes": (sz, [i64, i32, i32]),
+        "order_experts": (i32, [vp, i64, i32, i32, i32, vp, vp, i64, vp, vp, sz, vp]),
+        "combine_experts": (i32, [vp, i32, i64, i64, vp, vp, i64, i32, vp, vp]),
+        "combine_experts_backward": (i32, [vp, vp, i32, i64, i64, vp, vp, vp, i64, i32, vp, vp, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -473,3 +490,182 @@ def dequantize_mx(q, s, fmt, out_dtype=torch.bfloat16, out=None, x=None, want_ou
     _check(_load().dequantize_mx(_ptr(q), _ptr(s), rows, cols, fmt, _ptr(out), oc, _ptr(x), xc, _ptr(stats),
                                  _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev)), "dequantize_mx")
     return out, stats
+
+
+# ---- matrix products under group scales --------------------------------------------------------
+
+def _input(t, name, dtype, shape):
+    """A contiguous device tensor of this type and shape (None in the shape: any size)."""
+    _dev_tensor(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have the shape {tuple('*' if w is None else w for w in shape)}, "
+                         f"got {tuple(t.shape)}")
+    return t
+
+
+def _out_code(out_dtype):
+    if out_dtype == torch.bfloat16:
+        return _BF16
+    if out_dtype == torch.float32:
+        return _FP32
+    raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+
+
+def _scale_shape(kind, n, k):
+    if kind == WEIGHT_NK:
+        return -(-n // 128), -(-k // 128)
+    if kind == WEIGHT_KN:
+        return -(-k // 128), -(-n // 128)
+    return n, -(-k // 128)
+
+
+def matmul_block(a, sa, b, sb, fmt_a, fmt_b, kind=WEIGHT_NK, pow2_scales=False, out_dtype=torch.bfloat16, out=None,
+                 ws=None, stream=None):
+    """y [m][n] = values(a) times values(b), where values are decode(codes) / scale. a: uint8 codes
+    [m][k] with 1x128 group scales sa; b and sb by kind: WEIGHT_NK [n][k] and WEIGHT_KN [k][n] in
+    128x128 blocks, GROUPS_NK [n][k] in 1x128 groups. pow2_scales: every scale is a power of two. A float32 result has fp32 sums; a
+    bfloat16 one those of the FP8 matrix instructions, which keep 14 bits of each 8 products."""
+    m, k = _input(a, "a", torch.uint8, (None, None)).shape
+    if kind == WEIGHT_KN:
+        n = _input(b, "b", torch.uint8, (k, None)).shape[1]
+    else:
+        n = _input(b, "b", torch.uint8, (None, k)).shape[0]
+    _input(sa, "sa", torch.float32, (m, -(-k // 128)))
+    _input(sb, "sb", torch.float32, _scale_shape(kind, n, k))
+    code = _out_code(out_dtype)
+    dev = a.device
+    out = _out(out, (m, n), out_dtype, dev, "out")
+    lib = _load()
+    need = lib.matmul_block_workspace_bytes(m, n, k, kind, code)
+    if need and ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib.matmul_block(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), m, n, k, fmt_a, fmt_b, kind,
+                            FLAG_POW2_SCALES if pow2_scales else 0, _ptr(out), code, _ptr(ws),
+                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream, dev)), "matmul_block")
+    return out
+
+
+def matmul_block_experts(a, sa, b, sb, offsets, fmt_a, fmt_b, kind=WEIGHT_NK, rows=None, pow2_scales=False,
+                         out_dtype=torch.bfloat16, out=None, stream=None):
+    """One weight per expert: b [experts][n][k] (WEIGHT_NK) or [experts][k][n] (WEIGHT_KN). Rows
+    offsets[e] .. offsets[e+1] of the result are those of expert e; row i reads row rows[i] of a (a
+    negative entry: zeros), or row i without rows. Rows of no expert are zeros."""
+    tokens, k = _input(a, "a", torch.uint8, (None, None)).shape
+    if kind == WEIGHT_KN:
+        experts, _, n = _input(b, "b", torch.uint8, (None, k, None)).shape
+    else:
+        experts, n, _ = _input(b, "b", torch.uint8, (None, None, k)).shape
+    _input(sa, "sa", torch.float32, (tokens, -(-k // 128)))
+    _input(sb, "sb", torch.float32, (experts,) + _scale_shape(kind, n, k))
+    _input(offsets, "offsets", torch.int32, (experts + 1,))
+    nrows = tokens if rows is None else _input(rows, "rows", torch.int32, (None,)).shape[0]
+    code = _out_code(out_dtype)
+    out = _out(out, (nrows, n), out_dtype, a.device, "out")
+    _check(_load().matmul_block_experts(_ptr(a), _ptr(sa), tokens, _ptr(b), _ptr(sb), _ptr(offsets), experts, _ptr(rows),
+                                        nrows, n, k, fmt_a, fmt_b, kind, FLAG_POW2_SCALES if pow2_scales else 0,
+                                        _ptr(out), code, _stream(stream, a.device)), "matmul_block_experts")
+    return out
+
+
+def matmul_block_experts_wgrad(at, sat, bt, sbt, offsets, fmt_a, fmt_b, pow2_scales=False, out_dtype=torch.float32,
+                               out=None, stream=None):
+    """Weight gradients [experts][m][n]: values(at)[:, rows of e] times values(bt)[:, rows of e]
+    transposed, for codes at [m][nrows] and bt [n][nrows] in 1x128 groups along the rows; offsets
+    are multiples of 128."""
+    m, nrows = _input(at, "at", torch.uint8, (None, None)).shape
+    n = _input(bt, "bt", torch.uint8, (None, nrows)).shape[0]
+    _input(sat, "sat", torch.float32, (m, -(-nrows // 128)))
+    _input(sbt, "sbt", torch.float32, (n, -(-nrows // 128)))
+    experts = _input(offsets, "offsets", torch.int32, (None,)).shape[0] - 1
+    code = _out_code(out_dtype)
+    out = _out(out, (experts, m, n), out_dtype, at.device, "out")
+    _check(_load().matmul_block_experts_wgrad(_ptr(at), _ptr(sat), _ptr(bt), _ptr(sbt), _ptr(offsets), experts, nrows, m,
+                                              n, fmt_a, fmt_b, FLAG_POW2_SCALES if pow2_scales else 0, _ptr(out), code,
+                                              _stream(stream, at.device)), "matmul_block_experts_wgrad")
+    return out
+
+
+# ---- the expert layer around its products --------------------------------------------------------
+
+def route_experts(logits, top_k, score=SCORE_SOFTMAX, bias=None, groups=1, top_groups=1, renorm=True, scale=1.0,
+                  ids=None, weights=None, stream=None):
+    """Choice of top_k experts for each token from logits [tokens][experts] (BF16 or FP32). bias:
+    float32 [experts], added to the scores for the choice only; groups > 1: only the experts of the
+    best top_groups groups (by the sum of their two best choices). Returns (ids int32, weights
+    float32), both [tokens][top_k], in falling order of the choice."""
+    tokens, experts = _input(logits, "logits", logits.dtype, (None, None)).shape
+    dtype = _dtype_code(logits)
+    if bias is not None:
+        _input(bias, "bias", torch.float32, (experts,))
+    dev = logits.device
+    ids = _out(ids, (tokens, top_k), torch.int32, dev, "ids")
+    weights = _out(weights, (tokens, top_k), torch.float32, dev, "weights")
+    _check(_load().route_experts(_ptr(logits), dtype, tokens, experts, top_k, score, _ptr(bias), groups, top_groups,
+                                 int(renorm), scale, _ptr(ids), _ptr(weights), _stream(stream, dev)), "route_experts")
+    return ids, weights
+
+
+def route_experts_backward(logits, ids, dweights, score=SCORE_SOFTMAX, renorm=True, scale=1.0, dlogits=None,
+                           stream=None):
+    """Gradient of the logits from that of the weights of route_experts (same score, renorm, scale)."""
+    tokens, experts = _input(logits, "logits", logits.dtype, (None, None)).shape
+    dtype = _dtype_code(logits)
+    top_k = _input(ids, "ids", torch.int32, (tokens, None)).shape[1]
+    _input(dweights, "dweights", torch.float32, (tokens, top_k))
+    dlogits = _out(dlogits, (tokens, experts), logits.dtype, logits.device, "dlogits")
+    _check(_load().route_experts_backward(_ptr(logits), dtype, tokens, experts, _ptr(ids), _ptr(dweights), top_k, score,
+                                          int(renorm), scale, _ptr(dlogits), _stream(stream, logits.device)),
+           "route_experts_backward")
+    return dlogits
+
+
+def order_experts(ids, experts, align=1, offsets=None, rows=None, slots=None, ws=None, stream=None):
+    """Rows by expert for the choices ids [tokens][top_k]: offsets [experts + 1], rows (the token of
+    each row, -1 for padding; every expert starts at a multiple of align), slots [tokens][top_k] (the
+    row of each choice). All int32; nothing is read back to the host."""
+    tokens, top_k = _input(ids, "ids", torch.int32, (None, None)).shape
+    lib = _load()
+    dev = ids.device
+    nrows = lib.order_experts_rows(tokens, top_k, experts, align) if rows is None else rows.numel()
+    offsets = _out(offsets, (experts + 1,), torch.int32, dev, "offsets")
+    rows = _out(rows, (nrows,), torch.int32, dev, "rows")
+    slots = _out(slots, (tokens, top_k), torch.int32, dev, "slots")
+    need = lib.order_experts_workspace_bytes(tokens, top_k, experts)
+    if need and ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib.order_experts(_ptr(ids), tokens, top_k, experts, align, _ptr(offsets), _ptr(rows), nrows, _ptr(slots),
+                             _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream, dev)),
+           "order_experts")
+    return offsets, rows, slots
+
+
+def combine_experts(x, weights, slots, y=None, stream=None):
+    """y[t] = sum_j weights[t][j] x[slots[t][j]] for x [rows][dim] (BF16 or FP32); a slot outside the
+    rows adds nothing."""
+    nrows, dim = _input(x, "x", x.dtype, (None, None)).shape
+    dtype = _dtype_code(x)
+    tokens, top_k = _input(slots, "slots", torch.int32, (None, None)).shape
+    _input(weights, "weights", torch.float32, (tokens, top_k))
+    y = _out(y, (tokens, dim), x.dtype, x.device, "y")
+    _check(_load().combine_experts(_ptr(x), dtype, nrows, dim, _ptr(weights), _ptr(slots), tokens, top_k, _ptr(y),
+                                   _stream(stream, x.device)), "combine_experts")
+    return y
+
+
+def combine_experts_backward(dy, x, weights, slots, rows, dx=None, dweights=None, stream=None):
+    """Gradients of combine_experts: (dx, dweights). rows and slots are those of one order_experts
+    call; rows of dx that hold no token are zeros."""
+    nrows, dim = _input(x, "x", x.dtype, (None, None)).shape
+    dtype = _dtype_code(x)
+    tokens, top_k = _input(slots, "slots", torch.int32, (None, None)).shape
+    _input(weights, "weights", torch.float32, (tokens, top_k))
+    _input(dy, "dy", x.dtype, (tokens, dim))
+    _input(rows, "rows", torch.int32, (nrows,))
+    dx = _out(dx, (nrows, dim), x.dtype, x.device, "dx")
+    dweights = _out(dweights, (tokens, top_k), torch.float32, x.device, "dweights")
+    _check(_load().combine_experts_backward(_ptr(dy), _ptr(x), dtype, nrows, dim, _ptr(weights), _ptr(slots), _ptr(rows),
+                                            tokens, top_k, _ptr(dx), _ptr(dweights), _stream(stream, x.device)),
+           "combine_experts_backward")
+    return dx, dweights

@@ -31,6 +31,16 @@ inline bool dims_ok(int64_t rows, int64_t cols) {
     return true;
 }
 
+inline bool kind_ok(int kind) { return kind >= QF8_WEIGHT_NK && kind <= QF8_GROUPS_NK; }
+inline bool out_ok(int out) { return out == QF8_OUT_BF16 || out == QF8_OUT_FP32; }
+constexpr int64_t kMaxMatmulDim = 1 << 22;   // keeps every buffer offset of a tile below 2^31
+
+// the sizes a product takes: rows of codes are read as whole dwords
+inline bool matmul_dims_ok(int64_t m, int64_t n, int64_t k, int kind) {
+    if (m < 0 || n < 0 || k < 0 || m >= (int64_t)1 << 31 || n > kMaxMatmulDim || k > kMaxMatmulDim) return false;
+    return k % 4 == 0 && (kind != QF8_WEIGHT_KN || n % 4 == 0);
+}
+
 int check_delayed(const qf8_delayed_state *st) {
     if (!st) return QF8_ERR_NULL;
     if (st->magic != kDelayedMagic) return QF8_ERR_STATE;
@@ -434,6 +444,180 @@ qf8_status dequantize_mx(const uint8_t *q, const uint8_t *s, int64_t rows, int64
     if (rows * cols == 0 && !stats) return QF8_OK;
     return status_of(qf8::launch_dequant(2, fmt, q, rows, cols, 1, nullptr, s, out, out_dtype, x, x_dtype, stats, ws,
                                          as_stream(stream)));
+}
+
+size_t matmul_block_workspace_bytes(int64_t m, int64_t n, int64_t k, qf8_operand kind, qf8_out_dtype out_dtype) {
+    if (!kind_ok(kind) || !out_ok(out_dtype) || !matmul_dims_ok(m, n, k, kind)) return 0;
+    return qf8::matmul_workspace(m, n, k, kind, out_dtype == QF8_OUT_BF16);
+}
+
+qf8_status matmul_block(const uint8_t *a, const float *sa, const uint8_t *b, const float *sb, int64_t m, int64_t n,
+                        int64_t k, qf8_fmt fmt_a, qf8_fmt fmt_b, qf8_operand kind, int flags, void *y,
+                        qf8_out_dtype out_dtype, void *ws, size_t ws_bytes, void *stream) {
+    if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b) || !kind_ok(kind) || !out_ok(out_dtype) || (flags & ~QF8_FLAG_POW2_SCALES))
+        return QF8_ERR_ENUM;
+    if (!matmul_dims_ok(m, n, k, kind)) return QF8_ERR_SHAPE;
+    if (m == 0 || n == 0) return QF8_OK;
+    if (!y || (k > 0 && (!a || !sa || !b || !sb))) return QF8_ERR_NULL;
+    const size_t need = qf8::matmul_workspace(m, n, k, kind, out_dtype == QF8_OUT_BF16);
+    if (need > 0 && (!ws || ws_bytes < need)) return QF8_ERR_WORKSPACE;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(ws, 16))
+        return QF8_ERR_ALIGN;
+    qf8::MatmulArgs p = {};
+    p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.y = y;
+    p.m = m; p.n = (int)n; p.k = k; p.a_rows = m;
+    p.mode = qf8::kMatmulDense;
+    p.out_bf16 = out_dtype == QF8_OUT_BF16;
+    return status_of(qf8::launch_matmul(p, fmt_a, fmt_b, kind, flags & QF8_FLAG_POW2_SCALES, (float *)ws, as_stream(stream)));
+}
+
+qf8_status matmul_block_experts(const uint8_t *a, const float *sa, int64_t tokens, const uint8_t *b, const float *sb,
+                                const int32_t *offsets, int experts, const int32_t *rows, int64_t nrows, int64_t n,
+                                int64_t k, qf8_fmt fmt_a, qf8_fmt fmt_b, qf8_operand kind, int flags, void *y,
+                                qf8_out_dtype out_dtype, void *stream) {
+    if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b) || (kind != QF8_WEIGHT_NK && kind != QF8_WEIGHT_KN) || !out_ok(out_dtype) ||
+        (flags & ~QF8_FLAG_POW2_SCALES))
+        return QF8_ERR_ENUM;
+    if (!matmul_dims_ok(nrows, n, k, kind) || tokens < 0 || experts < 1 || experts > qf8::kMaxExperts) return QF8_ERR_SHAPE;
+    if (rows ? tokens >= (int64_t)1 << 31 || (k > 0 && tokens > 0xFFFFFFFFll / k) : tokens != nrows) return QF8_ERR_SHAPE;
+    if (nrows == 0 || n == 0) return QF8_OK;
+    if (!y || !offsets || (k > 0 && (!b || !sb)) || (k > 0 && tokens > 0 && (!a || !sa))) return QF8_ERR_NULL;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(sa, 4) || !aligned(sb, 4) ||
+        !aligned(offsets, 4) || !aligned(rows, 4))
+        return QF8_ERR_ALIGN;
+    qf8::MatmulArgs p = {};
+    p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.offsets = offsets; p.rows = rows; p.y = y;
+    p.m = nrows; p.n = (int)n; p.k = tokens > 0 ? k : 0; p.a_rows = tokens;      // no tokens: every row is zeros
+    p.experts = experts;
+    p.mode = qf8::kMatmulExperts;
+    p.out_bf16 = out_dtype == QF8_OUT_BF16;
+    return status_of(qf8::launch_matmul(p, fmt_a, fmt_b, kind, flags & QF8_FLAG_POW2_SCALES, nullptr, as_stream(stream)));
+}
+
+qf8_status matmul_block_experts_wgrad(const uint8_t *at, const float *sat, const uint8_t *bt, const float *sbt,
+                                      const int32_t *offsets, int experts, int64_t nrows, int64_t m, int64_t n,
+                                      qf8_fmt fmt_a, qf8_fmt fmt_b, int flags, void *y, qf8_out_dtype out_dtype,
+                                      void *stream) {
+    if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b) || !out_ok(out_dtype) || (flags & ~QF8_FLAG_POW2_SCALES)) return QF8_ERR_ENUM;
+    if (!matmul_dims_ok(m, n, nrows, QF8_GROUPS_NK) || experts < 1 || experts > qf8::kMaxExperts) return QF8_ERR_SHAPE;
+    if (m == 0 || n == 0) return QF8_OK;
+    if (!y || !offsets || (nrows > 0 && (!at || !sat || !bt || !sbt))) return QF8_ERR_NULL;
+    if (!aligned(at, 16) || !aligned(bt, 16) || !aligned(y, 16) || !aligned(sat, 4) || !aligned(sbt, 4) ||
+        !aligned(offsets, 4))
+        return QF8_ERR_ALIGN;
+    qf8::MatmulArgs p = {};
+    p.a = at; p.sa = sat; p.b = bt; p.sb = sbt; p.offsets = offsets; p.y = y;
+    p.m = m; p.n = (int)n; p.k = nrows; p.a_rows = m;
+    p.experts = experts;
+    p.mode = qf8::kMatmulExpertsK;
+    p.out_bf16 = out_dtype == QF8_OUT_BF16;
+    return status_of(qf8::launch_matmul(p, fmt_a, fmt_b, QF8_GROUPS_NK, flags & QF8_FLAG_POW2_SCALES, nullptr,
+                                        as_stream(stream)));
+}
+
+qf8_status route_experts(const void *logits, qf8_dtype dtype, int64_t tokens, int experts, int top_k, qf8_score score,
+                         const float *bias, int groups, int top_groups, int renorm, float scale, int32_t *ids,
+                         float *weights, void *stream) {
+    if (!dtype_ok(dtype) || (score != QF8_SCORE_SOFTMAX && score != QF8_SCORE_SIGMOID)) return QF8_ERR_ENUM;
+    if (tokens < 0 || tokens >= (int64_t)1 << 31 || experts < 1 || experts > qf8::kMaxExperts || groups < 1 ||
+        groups > qf8::kMaxExpertGroups || experts % groups != 0 || top_groups < 1 || top_groups > groups || top_k < 1 ||
+        top_k > qf8::kMaxTopK || top_k > experts / groups * top_groups)
+        return QF8_ERR_SHAPE;
+    if (tokens == 0) return QF8_OK;
+    if (!logits || !ids || !weights) return QF8_ERR_NULL;
+    if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return QF8_ERR_ALIGN;
+    qf8::RouteArgs p = {};
+    p.logits = logits; p.bias = bias; p.ids = ids; p.weights = weights;
+    p.tokens = tokens; p.experts = experts; p.top_k = top_k; p.score = score;
+    p.groups = top_groups == groups ? 1 : groups;      // all groups open: the same as none
+    p.top_groups = p.groups == 1 ? 1 : top_groups;
+    p.renorm = renorm != 0; p.scale = scale;
+    return status_of(qf8::launch_route(p, dtype, 0, as_stream(stream)));
+}
+
+qf8_status route_experts_backward(const void *logits, qf8_dtype dtype, int64_t tokens, int experts, const int32_t *ids,
+                                  const float *dweights, int top_k, qf8_score score, int renorm, float scale,
+                                  void *dlogits, void *stream) {
+    if (!dtype_ok(dtype) || (score != QF8_SCORE_SOFTMAX && score != QF8_SCORE_SIGMOID)) return QF8_ERR_ENUM;
+    if (tokens < 0 || tokens >= (int64_t)1 << 31 || experts < 1 || experts > qf8::kMaxExperts || top_k < 1 ||
+        top_k > qf8::kMaxTopK || top_k > experts)
+        return QF8_ERR_SHAPE;
+    if (tokens == 0) return QF8_OK;
+    if (!logits || !ids || !dweights || !dlogits) return QF8_ERR_NULL;
+    if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(dweights, 4) || !aligned(dlogits, 4)) return QF8_ERR_ALIGN;
+    qf8::RouteArgs p = {};
+    p.logits = logits; p.ids = const_cast<int32_t *>(ids); p.dweights = dweights; p.dlogits = dlogits;
+    p.tokens = tokens; p.experts = experts; p.top_k = top_k; p.score = score; p.renorm = renorm != 0; p.scale = scale;
+    return status_of(qf8::launch_route(p, dtype, 1, as_stream(stream)));
+}
+
+int64_t order_experts_rows(int64_t tokens, int top_k, int experts, int align) {
+    if (tokens < 0 || tokens >= (int64_t)1 << 31 || top_k < 1 || top_k > qf8::kMaxTopK || experts < 1 ||
+        experts > qf8::kMaxExperts || align < 1 || align > 1024)
+        return 0;
+    const int64_t n = tokens * top_k;
+    return (n + (experts < n ? experts : n) * (align - 1) + align - 1) / align * align;
+}
+
+size_t order_experts_workspace_bytes(int64_t tokens, int top_k, int experts) {
+    return order_experts_rows(tokens, top_k, experts, 1) == 0 ? 0 : qf8::order_workspace(tokens * top_k, experts);
+}
+
+qf8_status order_experts(const int32_t *ids, int64_t tokens, int top_k, int experts, int align, int32_t *offsets,
+                         int32_t *rows, int64_t nrows, int32_t *slots, void *ws, size_t ws_bytes, void *stream) {
+    if (tokens < 0 || tokens >= (int64_t)1 << 31 || top_k < 1 || top_k > qf8::kMaxTopK || experts < 1 ||
+        experts > qf8::kMaxExperts || align < 1 || align > 1024)
+        return QF8_ERR_SHAPE;
+    if (nrows < order_experts_rows(tokens, top_k, experts, align) || nrows >= (int64_t)1 << 31) return QF8_ERR_SHAPE;
+    if (!offsets || (tokens > 0 && (!ids || !slots)) || (nrows > 0 && !rows)) return QF8_ERR_NULL;
+    const size_t need = qf8::order_workspace(tokens * top_k, experts);
+    if (need > 0 && (!ws || ws_bytes < need)) return QF8_ERR_WORKSPACE;
+    if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4) || !aligned(ws, 16))
+        return QF8_ERR_ALIGN;
+    qf8::OrderArgs p = {};
+    p.ids = ids; p.offsets = offsets; p.rows = rows; p.slots = slots; p.counts = (int32_t *)ws;
+    p.n = tokens * top_k; p.nrows = nrows; p.top_k = top_k; p.experts = experts; p.align = align;
+    return status_of(qf8::launch_order(p, as_stream(stream)));
+}
+
+namespace {
+int check_combine(qf8_dtype dtype, int64_t nrows, int64_t dim, int64_t tokens, int top_k) {
+    if (!dtype_ok(dtype)) return QF8_ERR_ENUM;
+    if (tokens < 0 || tokens >= (int64_t)1 << 30 || nrows < 0 || nrows >= (int64_t)1 << 31 || dim < 0 ||
+        dim >= (int64_t)1 << 31 || top_k < 1 || top_k > qf8::kMaxTopK)
+        return QF8_ERR_SHAPE;
+    return QF8_OK;
+}
+}  // namespace
+
+qf8_status combine_experts(const void *x, qf8_dtype dtype, int64_t nrows, int64_t dim, const float *weights,
+                           const int32_t *slots, int64_t tokens, int top_k, void *y, void *stream) {
+    const int c = check_combine(dtype, nrows, dim, tokens, top_k);
+    if (c != QF8_OK) return status_of(c);
+    if (tokens == 0 || dim == 0) return QF8_OK;
+    if ((nrows > 0 && !x) || !weights || !slots || !y) return QF8_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(weights, 4) || !aligned(slots, 4)) return QF8_ERR_ALIGN;
+    qf8::CombineArgs p = {};
+    p.x = x; p.weights = weights; p.slots = slots; p.y = y;
+    p.tokens = tokens; p.nrows = nrows; p.dim = dim; p.top_k = top_k;
+    return status_of(qf8::launch_combine(p, dtype, 0, as_stream(stream)));
+}
+
+qf8_status combine_experts_backward(const void *dy, const void *x, qf8_dtype dtype, int64_t nrows, int64_t dim,
+                                    const float *weights, const int32_t *slots, const int32_t *rows, int64_t tokens,
+                                    int top_k, void *dx, float *dweights, void *stream) {
+    const int c = check_combine(dtype, nrows, dim, tokens, top_k);
+    if (c != QF8_OK) return status_of(c);
+    if (tokens == 0 && (nrows == 0 || dim == 0)) return QF8_OK;
+    if ((tokens > 0 && (!weights || !slots || !dweights || (dim > 0 && !dy))) || (nrows > 0 && (!rows || (dim > 0 && (!x || !dx)))))
+        return QF8_ERR_NULL;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dx, 16) || !aligned(weights, 4) || !aligned(slots, 4) ||
+        !aligned(rows, 4) || !aligned(dweights, 4))
+        return QF8_ERR_ALIGN;
+    qf8::CombineArgs p = {};
+    p.x = x; p.dy = dy; p.weights = weights; p.slots = slots; p.rows = rows; p.dx = dx; p.dweights = dweights;
+    p.tokens = tokens; p.nrows = nrows; p.dim = dim; p.top_k = top_k;
+    return status_of(qf8::launch_combine(p, dtype, 1, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -93,4 +93,57 @@ int launch_dequant(int mode, int fmt, const uint8_t *q, int64_t rows, int64_t co
                    const float *scale, const uint8_t *sb, void *out, int out_dtype, const void *x, int x_dtype,
                    qf8_error_stats *stats, void *ws, hipStream_t s);
 
+// Products of FP8 codes under group scales. Dense: y [m][n] = a [m][k] b; experts: rows of y belong to
+// experts by offsets, each with its own b, and row i reads row rows[i] of a (all with rows NULL);
+// experts along k: one y [m][n] per expert over its own range of k.
+enum { kMatmulDense = 0, kMatmulExperts = 1, kMatmulExpertsK = 2 };
+struct MatmulArgs {
+    const uint8_t *a;
+    const float *sa;
+    const uint8_t *b;
+    const float *sb;
+    const int32_t *offsets;      // experts + 1
+    const int32_t *rows;         // m entries or NULL
+    void *y;                     // output, or with splits > 1 the fp32 partial sums [splits][m][n]
+    int64_t m, k, a_rows;
+    int n, experts, mode, splits;
+    int64_t split_k;             // k of one split, a multiple of 128
+    int out_bf16, vec;           // vec: 16-byte stores fit every row
+};
+int launch_matmul(const MatmulArgs &p, int fmt_a, int fmt_b, int kind, int pow2, float *ws, hipStream_t s);
+// Bytes of partial sums launch_matmul uses for a dense product (0: none).
+size_t matmul_workspace(int64_t m, int64_t n, int64_t k, int kind, int out_bf16);
+
+// The expert layer: choice of experts, order of the rows, weighted sum.
+constexpr int kMaxExperts = 1024, kMaxTopK = 64, kMaxExpertGroups = 64;
+struct RouteArgs {
+    const void *logits;
+    const float *bias, *dweights;
+    int32_t *ids;                // read by the backward pass
+    float *weights;
+    void *dlogits;
+    int64_t tokens;
+    int experts, top_k, score, groups, top_groups, renorm;
+    float scale;
+};
+int launch_route(const RouteArgs &p, int dtype, int backward, hipStream_t s);
+struct OrderArgs {
+    const int32_t *ids;
+    int32_t *offsets, *rows, *slots, *counts;
+    int64_t n, nrows;            // choices, rows
+    int top_k, experts, align;
+};
+size_t order_workspace(int64_t n, int experts);
+int launch_order(const OrderArgs &p, hipStream_t s);
+struct CombineArgs {
+    const void *x, *dy;
+    const float *weights;
+    const int32_t *slots, *rows;
+    void *y, *dx;
+    float *dweights;
+    int64_t tokens, nrows, dim;
+    int top_k, vec;
+};
+int launch_combine(const CombineArgs &p, int dtype, int backward, hipStream_t s);
+
 }  // namespace qf8

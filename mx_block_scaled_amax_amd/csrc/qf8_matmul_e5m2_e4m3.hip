@@ -1,0 +1,6 @@
+// qf8_matmul_e5m2_e4m3.hip -- the matrix products of E5M2 rows with E4M3 columns.
+#include "qf8_matmul.h"
+
+namespace qf8 {
+template int launch_matmul_formats<kE5M2, kE4M3>(const MatmulArgs &, int, int, int, int64_t, hipStream_t);
+}
