@@ -41,6 +41,12 @@ constexpr int kBK = 128;                                  // bytes of k per step
 
 // ---- pieces ------------------------------------------------------------------------------------
 
+// Position of chunk 0 of a 128-byte row in LDS. A 16-byte read serves 16 lanes a cycle (0-3, 12-15,
+// 20-23 and 24-27 of each half wave): two rows fill the 64 banks, so the 8 even and the 8 odd rows
+// among those lanes need 8 positions each, for fragments of 16 rows x 4 chunks and of 32 rows x 2
+// alike. Measured 233 bytes a cycle; with r & 7 the 32-row form took twice as long.
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
+
 // A buffer descriptor whose base moves along k: `left` is the number of bytes from the base to the
 // end of the tensor, so every lane past it reads zeros.
 struct MovingBuffer {
@@ -73,6 +79,16 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
 __device__ __forceinline__ void lds_dma16(v4i32 rsrc, uint32_t voff, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :: "s"(lds), "v"(voff), "s"(rsrc) : "memory");
+}
+__device__ __forceinline__ void lds_dma4(v4i32 rsrc, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :: "s"(lds), "v"(voff), "s"(rsrc) : "memory");
+}
+template <int N> __device__ __forceinline__ void wait_vmem_but() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory"); }
+// End of a phase: this wave's LDS traffic is done; then the workgroup meets.
+__device__ __forceinline__ void phase_end() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 __device__ __forceinline__ void wait_vmem() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
@@ -256,6 +272,148 @@ __device__ __forceinline__ void store_run(const MatmulArgs &p, const TilePlace &
     }
 }
 
+// The tile of this workgroup; false: there is none.
+__device__ __forceinline__ bool place_tile(const MatmulArgs &p, int bm, int bn, TilePlace &pl) {
+    pl.split = 0;
+    pl.expert = 0;
+    const int tn = (p.n + bn - 1) / bn;
+    if (p.mode == kMatmulExperts) {
+        pl.rows = 0;
+        const int tiles_m = find_row_tile(p.offsets, p.experts, p.m, bm, -1, pl);
+        const int64_t id = xcd_order(blockIdx.x, (int64_t)tiles_m * tn);
+        if (id < 0) return false;
+        // all columns of up to 4 row tiles, then the next ones: the row tiles of one expert run together
+        int im, in;
+        constexpr int kPanel = 4;
+        const int64_t per = (int64_t)kPanel * tn;
+        const int pn = (int)(id / per), rr = (int)(id - pn * per);
+        const int h = tiles_m - pn * kPanel < kPanel ? tiles_m - pn * kPanel : kPanel;
+        im = pn * kPanel + rr % h;
+        in = rr / h;
+        find_row_tile(p.offsets, p.experts, p.m, bm, im, pl);
+        pl.n0 = in * bn;
+        pl.k0 = 0;
+        pl.k1 = p.k;
+    } else {
+        const int tm = (int)((p.m + bm - 1) / bm);
+        const int64_t per = (int64_t)tm * tn;
+        const int64_t total = per * (p.mode == kMatmulExpertsK ? p.experts : p.splits);
+        const int64_t id = xcd_order(blockIdx.x, total);
+        if (id < 0) return false;
+        const int part = (int)(id / per);
+        int im, in;
+        panel_order(id - part * per, tm, tn, im, in);
+        pl.row0 = (int64_t)im * bm;
+        pl.rows = (int)(p.m - pl.row0 < bm ? p.m - pl.row0 : bm);
+        pl.n0 = in * bn;
+        if (p.mode == kMatmulExpertsK) {
+            pl.expert = part;
+            int64_t lo = p.offsets[part], hi = p.offsets[part + 1];
+            lo = lo < 0 ? 0 : lo > p.k ? p.k : lo & ~(int64_t)(kBK - 1);
+            hi = hi < lo ? lo : hi > p.k ? p.k : hi;
+            pl.k0 = lo;
+            pl.k1 = hi;
+        } else {
+            pl.split = part;
+            pl.k0 = (int64_t)part * p.split_k;
+            pl.k1 = pl.k0 + p.split_k < p.k ? pl.k0 + p.split_k : p.k;
+        }
+    }
+    return true;
+}
+
+// The row of a that row r of the tile reads; rows past the end repeat the last one, and a row that
+// names no row of a reads row 0 (its result is not stored).
+__device__ __forceinline__ int64_t source_row(const MatmulArgs &p, const TilePlace &pl, int r) {
+    r = r < pl.rows ? r : pl.rows - 1;
+    if (!p.rows) return pl.row0 + r;
+    const int64_t v = p.rows[pl.row0 + r];
+    return v < 0 || v >= p.a_rows ? 0 : v;
+}
+
+// Addresses of a tile's operand loads: piece i of a thread is 16 bytes; the buffers move along k.
+template <int KIND, bool EXACT, int BM, int BN, int TN, int NT>
+struct TileLoads {
+    static constexpr int LA = BM * kBK / 16 / NT, LB = BN * kBK / 16 / NT;
+    MovingBuffer ba, bb;
+    uint32_t va[LA], vb[LB], stepb;
+
+    __device__ __forceinline__ void init(const MatmulArgs &p, const TilePlace &pl, int steps, int t) {
+        const bool gather = p.rows != nullptr;
+        if (gather) {
+            ba.base = uniform64((uint64_t)(uintptr_t)p.a);
+            ba.left = (uint32_t)(p.a_rows * p.k);
+        } else {
+            ba.base = uniform64((uint64_t)(uintptr_t)p.a + (uint64_t)(pl.row0 * p.k + pl.k0));
+            ba.left = cap31((p.m - pl.row0) * p.k - pl.k0);
+        }
+        ba.left = __builtin_amdgcn_readfirstlane((int)ba.left);
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            const int id = i * NT + t, row = id >> 3, ch = (id & 7) ^ swizzle(row);
+            va[i] = steps ? (uint32_t)((source_row(p, pl, row) - (gather ? 0 : pl.row0)) * p.k) + 16u * ch : 0u;
+        }
+        const uint64_t bmat = (uint64_t)(p.mode == kMatmulExperts && pl.expert > 0 ? pl.expert : 0) * (uint64_t)p.n * (uint64_t)p.k;
+        if constexpr (KIND == kKN) {
+            bb.base = uniform64((uint64_t)(uintptr_t)p.b + bmat + (uint64_t)(pl.k0 * p.n + pl.n0));
+            bb.left = cap31((p.k - pl.k0) * p.n - pl.n0);
+            constexpr int C = BN / 16;
+#pragma unroll
+            for (int i = 0; i < LB; ++i) {
+                const int id = i * NT + t, kr = id / C, ch = (id % C) ^ (kr & 7);
+                vb[i] = (uint32_t)kr * (uint32_t)p.n + 16u * ch;
+            }
+        } else {
+            bb.base = uniform64((uint64_t)(uintptr_t)p.b + bmat + (uint64_t)((int64_t)pl.n0 * p.k + pl.k0));
+            bb.left = cap31((int64_t)(p.n - pl.n0) * p.k - pl.k0);
+#pragma unroll
+            for (int i = 0; i < LB; ++i) {
+                const int id = i * NT + t, row = id >> 3, ch = (id & 7) ^ swizzle(row);
+                int n = (row / TN) * TN + column_of<TN, EXACT>(row % TN);
+                n = n < p.n - pl.n0 ? n : p.n - pl.n0 - 1;
+                vb[i] = (uint32_t)n * (uint32_t)p.k + 16u * ch;
+            }
+        }
+        bb.left = __builtin_amdgcn_readfirstlane((int)bb.left);
+        stepb = KIND == kKN ? (uint32_t)kBK * (uint32_t)p.n : (uint32_t)kBK;
+    }
+};
+
+// Stores a wave's TM x TN values.
+template <int KIND, bool EXACT, int TM, int TN, typename V, int FM, int FN>
+__device__ __forceinline__ void store_tile(const MatmulArgs &p, const TilePlace &pl, int wm, int wn, int lane,
+                                           const V (&acc)[FM][FN]) {
+    constexpr int FR = EXACT ? 32 : 16, FV = FR * FR / 64;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int r = wm * TM + FR * i + (lane % FR);
+        if (r >= pl.rows) continue;
+        const int64_t row = pl.row0 + r;
+        bool zero = false;
+        if (p.rows) {
+            const int64_t src = p.rows[row];
+            zero = src < 0 || src >= p.a_rows;
+        }
+        // runs of neighbouring columns: all a lane holds, or 4 with KN, whose columns keep their order
+        constexpr int PER = TN * FR / 64, RUN = KIND == kKN ? 4 : PER;
+        const int q = lane / FR;
+#pragma unroll
+        for (int u = 0; u < PER / RUN; ++u) {
+            int n = pl.n0 + wn * TN;
+            if constexpr (KIND != kKN) n += q * PER;
+            else if constexpr (EXACT) n += 32 * (u >> 2) + 8 * (u & 3) + 4 * q;
+            else n += 16 * u + 4 * q;
+            float v[RUN];
+#pragma unroll
+            for (int e = 0; e < RUN; ++e) {
+                const int at = u * RUN + e;
+                v[e] = zero ? 0.0f : acc[i][at / FV][at % FV];
+            }
+            store_run<RUN>(p, pl, row, n, v);
+        }
+    }
+}
+
 // ---- the tiled kernel ---------------------------------------------------------------------------
 
 // BM x BN outputs per workgroup, WM x WN waves. Operand tiles of 128 bytes of k go straight from
@@ -263,8 +421,8 @@ __device__ __forceinline__ void store_run(const MatmulArgs &p, const TilePlace &
 // barrier a step.
 //
 // LDS tiles of rows along k (a, and b unless KN): 128-byte rows of eight 16-byte chunks, chunk c of
-// row r at position c ^ (r & 7), so the rows of a fragment read spread over all banks. The lanes of
-// the load fetch the permuted chunk, which stays inside the same 128 bytes of memory.
+// row r at position c ^ swizzle(r). The lanes of the load fetch the permuted chunk, which stays
+// inside the same 128 bytes of memory.
 // KN: b's tile keeps k as rows of BN bytes (chunk c of row k at c ^ (k & 7)) and the transposing
 // LDS read hands each lane 8 codes along k of one column.
 template <int FA, int FB, int KIND, int MATH, int BM, int BN, int WM, int WN>
@@ -283,103 +441,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, g = lane >> 4;
 
-    // ---- the tile of this workgroup
     TilePlace pl;
-    pl.split = 0;
-    pl.expert = 0;
-    const int tn = (p.n + BN - 1) / BN;
-    if (p.mode == kMatmulExperts) {
-        pl.rows = 0;
-        const int tiles_m = find_row_tile(p.offsets, p.experts, p.m, BM, -1, pl);
-        const int64_t id = xcd_order(blockIdx.x, (int64_t)tiles_m * tn);
-        if (id < 0) return;
-        // all columns of up to 4 row tiles, then the next ones: the row tiles of one expert run together
-        int im, in;
-        constexpr int kPanel = 4;
-        const int64_t per = (int64_t)kPanel * tn;
-        const int pn = (int)(id / per), rr = (int)(id - pn * per);
-        const int h = tiles_m - pn * kPanel < kPanel ? tiles_m - pn * kPanel : kPanel;
-        im = pn * kPanel + rr % h;
-        in = rr / h;
-        find_row_tile(p.offsets, p.experts, p.m, BM, im, pl);
-        pl.n0 = in * BN;
-        pl.k0 = 0;
-        pl.k1 = p.k;
-    } else {
-        const int tm = (int)((p.m + BM - 1) / BM);
-        const int64_t per = (int64_t)tm * tn;
-        const int64_t total = per * (p.mode == kMatmulExpertsK ? p.experts : p.splits);
-        const int64_t id = xcd_order(blockIdx.x, total);
-        if (id < 0) return;
-        const int part = (int)(id / per);
-        int im, in;
-        panel_order(id - part * per, tm, tn, im, in);
-        pl.row0 = (int64_t)im * BM;
-        pl.rows = (int)(p.m - pl.row0 < BM ? p.m - pl.row0 : BM);
-        pl.n0 = in * BN;
-        if (p.mode == kMatmulExpertsK) {
-            pl.expert = part;
-            int64_t lo = p.offsets[part], hi = p.offsets[part + 1];
-            lo = lo < 0 ? 0 : lo > p.k ? p.k : lo & ~(int64_t)(kBK - 1);
-            hi = hi < lo ? lo : hi > p.k ? p.k : hi;
-            pl.k0 = lo;
-            pl.k1 = hi;
-        } else {
-            pl.split = part;
-            pl.k0 = (int64_t)part * p.split_k;
-            pl.k1 = pl.k0 + p.split_k < p.k ? pl.k0 + p.split_k : p.k;
-        }
-    }
+    if (!place_tile(p, BM, BN, pl)) return;
     const int steps = pl.expert < 0 || pl.k1 <= pl.k0 ? 0 : (int)((pl.k1 - pl.k0 + kBK - 1) / kBK);
     const int kend = (int)(pl.k1 - pl.k0);
     const int gk = (int)((p.k + kBK - 1) / kBK), g0 = (int)(pl.k0 / kBK);
-    const bool gather = p.rows != nullptr;
 
-    // ---- operand addresses
-    MovingBuffer ba, bb;
-    uint32_t va[LA], vb[LB];
-    if (gather) {
-        ba.base = uniform64((uint64_t)(uintptr_t)p.a);
-        ba.left = (uint32_t)(p.a_rows * p.k);
-    } else {
-        ba.base = uniform64((uint64_t)(uintptr_t)p.a + (uint64_t)(pl.row0 * p.k + pl.k0));
-        ba.left = cap31((p.m - pl.row0) * p.k - pl.k0);
-    }
-    ba.left = __builtin_amdgcn_readfirstlane((int)ba.left);
-    auto a_row = [&](int r) -> int64_t {               // row of a for tile row r; rows past the end repeat the last
-        r = r < pl.rows ? r : pl.rows - 1;
-        if (!gather) return r;
-        const int64_t v = p.rows[pl.row0 + r];
-        return v < 0 || v >= p.a_rows ? 0 : v;         // no such row: any values, the result is not stored
-    };
-#pragma unroll
-    for (int i = 0; i < LA; ++i) {
-        const int id = i * NT + t, row = id >> 3, ch = (id & 7) ^ (row & 7);
-        va[i] = steps ? (uint32_t)(a_row(row) * p.k) + 16u * ch : 0u;
-    }
-    const uint64_t bmat = (uint64_t)(p.mode == kMatmulExperts && pl.expert > 0 ? pl.expert : 0) * (uint64_t)p.n * (uint64_t)p.k;
-    if constexpr (KIND == kKN) {
-        bb.base = uniform64((uint64_t)(uintptr_t)p.b + bmat + (uint64_t)(pl.k0 * p.n + pl.n0));
-        bb.left = cap31((p.k - pl.k0) * p.n - pl.n0);
-        constexpr int C = BN / 16;
-#pragma unroll
-        for (int i = 0; i < LB; ++i) {
-            const int id = i * NT + t, kr = id / C, ch = (id % C) ^ (kr & 7);
-            vb[i] = (uint32_t)kr * (uint32_t)p.n + 16u * ch;
-        }
-    } else {
-        bb.base = uniform64((uint64_t)(uintptr_t)p.b + bmat + (uint64_t)((int64_t)pl.n0 * p.k + pl.k0));
-        bb.left = cap31((int64_t)(p.n - pl.n0) * p.k - pl.k0);
-#pragma unroll
-        for (int i = 0; i < LB; ++i) {
-            const int id = i * NT + t, row = id >> 3, ch = (id & 7) ^ (row & 7);
-            int n = (row / TN) * TN + column_of<TN, EXACT>(row % TN);
-            n = n < p.n - pl.n0 ? n : p.n - pl.n0 - 1;
-            vb[i] = (uint32_t)n * (uint32_t)p.k + 16u * ch;
-        }
-    }
-    bb.left = __builtin_amdgcn_readfirstlane((int)bb.left);
-    const uint32_t stepb = KIND == kKN ? (uint32_t)kBK * (uint32_t)p.n : (uint32_t)kBK;
+    TileLoads<KIND, EXACT, BM, BN, TN, NT> ld;
+    ld.init(p, pl, steps, t);
+    MovingBuffer &ba = ld.ba, &bb = ld.bb;
+    const auto &va = ld.va;
+    const auto &vb = ld.vb;
+    const uint32_t stepb = ld.stepb;
 
     // ---- scale addresses: thread u < BM loads a row's scale, BM <= u < BM + SB one of b
     constexpr int LS = (BM + SB + NT - 1) / NT;
@@ -388,7 +461,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     for (int i = 0; i < LS; ++i) {
         const int u = i * NT + t;
         if (u < BM) {
-            const int64_t r = gather ? a_row(u) : pl.row0 + a_row(u);
+            const int64_t r = source_row(p, pl, u);
             sp[i] = p.sa + (steps ? r : 0) * gk + g0;
         } else if (u < BM + SB) {
             const int v = u - BM;
@@ -414,35 +487,46 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     const int sstep_b = KIND == kKN ? (p.n + 127) / 128 : 1;
 
     constexpr int FV = FR * FR / 64;                     // values of a fragment in a lane
-    float acc[FM][FN][FV];
+    typedef float frag __attribute__((ext_vector_type(FV)));
+    frag acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int e = 0; e < FV; ++e) acc[i][j][e] = 0.0f;
+        for (int j = 0; j < FN; ++j) acc[i][j] = (frag)0.0f;
 
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)lds_address(&tiles[0][0])) + (uint32_t)wave * 1024u;
+    // The loads of a step: piece u of LA + LB, then advance. Past the last step the descriptors have
+    // length 0: the loads still run, read nothing and leave zeros in a buffer nobody reads.
+    constexpr int LT = LA + LB;
+    v4i32 ra = ba.rsrc(), rb = bb.rsrc();
+    auto load_piece = [&](int stage, int u) {
+        const uint32_t at = lds0 + (uint32_t)stage * kStage + (u < LA ? 0u : (uint32_t)kA) + (uint32_t)(u < LA ? u : u - LA) * NT * 16;
+        if (u < LA) lds_dma16(ra, va[u < LA ? u : 0], at);
+        else lds_dma16(rb, vb[u < LA ? 0 : u - LA], at);
+    };
     float sreg[LS];
-    auto load_step = [&](int s) {
-        const uint32_t at = lds0 + (uint32_t)(s & 1) * kStage;
-        const v4i32 ra = ba.rsrc(), rb = bb.rsrc();
-#pragma unroll
-        for (int i = 0; i < LA; ++i) lds_dma16(ra, va[i], at + (uint32_t)i * NT * 16);
-#pragma unroll
-        for (int i = 0; i < LB; ++i) lds_dma16(rb, vb[i], at + kA + (uint32_t)i * NT * 16);
-        ba.advance(kBK);
-        bb.advance(stepb);
+    auto load_scales = [&](bool more) {
 #pragma unroll
         for (int i = 0; i < LS; ++i) {
             if (sp[i]) {
                 sreg[i] = *sp[i];
-                sp[i] += i * NT + t < BM ? 1 : sstep_b;
+                sp[i] += more ? (i * NT + t < BM ? 1 : sstep_b) : 0;
             }
         }
     };
+    auto advance = [&](bool more) {
+        ba.advance(kBK);
+        bb.advance(stepb);
+        if (!more) ba.left = bb.left = 0;
+        ra = ba.rsrc();
+        rb = bb.rsrc();
+    };
 
-    if (steps) load_step(0);
+    if (steps) {
+#pragma unroll
+        for (int u = 0; u < LT; ++u) load_piece(0, u);
+        load_scales(steps > 1);
+    }
     for (int s = 0; s < steps; ++s) {
         wait_vmem();
         float *sc = scales[s & 1];
@@ -455,7 +539,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
         if (krem < kBK) {                               // the last step of a k that is no multiple of 128
 #pragma unroll
             for (int i = 0; i < LA; ++i) {
-                const int id = i * NT + t, row = id >> 3, ch = (id & 7) ^ (row & 7);
+                const int id = i * NT + t, row = id >> 3, ch = (id & 7) ^ swizzle(row);
                 uint4 *at = (uint4 *)(ta + 16 * id);
                 if (16 * ch + 16 > krem) *at = keep_bytes(*at, krem - 16 * ch);
             }
@@ -466,18 +550,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                 if constexpr (KIND == kKN) {
                     if (id / (BN / 16) >= krem) *at = make_uint4(0, 0, 0, 0);
                 } else {
-                    const int row = id >> 3, ch = (id & 7) ^ (row & 7);
+                    const int row = id >> 3, ch = (id & 7) ^ swizzle(row);
                     if (16 * ch + 16 > krem) *at = keep_bytes(*at, krem - 16 * ch);
                 }
             }
             __syncthreads();
         }
-        if (s + 1 < steps) load_step(s + 1);
+        advance(s + 1 < steps);
+        load_scales(s + 2 < steps);
+        const int stage = (s + 1) & 1;
 
         if constexpr (EXACT) {
             // lane (r32, h): row r32 of a fragment; slice u of 16 k holds, for half h, the 8 codes at
             // k = 16 (2 (u / 2) + h) + 8 (u % 2)
             const int r32 = lane & 31, h = lane >> 5;
+#pragma unroll
+            for (int u = 0; u < LT; ++u) load_piece(stage, u);
             v8bf16 fb[FN][8];
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
@@ -493,7 +581,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                     const int row = wn * TN + 32 * j + r32;
 #pragma unroll
                     for (int u = 0; u < 8; u += 2) {
-                        const uint4 q = *(const uint4 *)(tb + row * kBK + (((u + h) ^ (row & 7)) << 4));
+                        const uint4 q = *(const uint4 *)(tb + row * kBK + (((u + h) ^ swizzle(row)) << 4));
                         fb[j][u] = codes_to_bf16<FB>(q.x, q.y);
                         fb[j][u + 1] = codes_to_bf16<FB>(q.z, q.w);
                     }
@@ -509,7 +597,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                     for (int e = 0; e < 16; ++e) part[j][e] = 0.0f;
 #pragma unroll
                 for (int u = 0; u < 8; u += 2) {
-                    const uint4 q = *(const uint4 *)(ta + row * kBK + (((u + h) ^ (row & 7)) << 4));
+                    const uint4 q = *(const uint4 *)(ta + row * kBK + (((u + h) ^ swizzle(row)) << 4));
                     const v8bf16 f0 = codes_to_bf16<FA>(q.x, q.y), f1 = codes_to_bf16<FA>(q.z, q.w);
 #pragma unroll
                     for (int j = 0; j < FN; ++j) part[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j][u], f0, part[j], 0, 0, 0);
@@ -535,8 +623,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                 }
             }
         } else {
-            // fragments of b: lane (r16, g) holds row r16 and k = 16 g + [0, 16) and 64 + 16 g + [0, 16)
+            // lane (r16, g) holds row r16 of a fragment and k = 16 g + [0, 16) and 64 + 16 g + [0, 16).
+            // Products of fragment i run while the fragments of i + 1 are read and the sums of i - 1
+            // are scaled; the next step's loads are issued in between, a few at a time, so that no
+            // wave stands in a full load queue while the matrix core idles.
+            const uint32_t swz = (uint32_t)((g ^ swizzle(r16)) << 4);
+            const uint8_t *const pa = ta + (wm * TM + r16) * kBK;
+            auto frag_a = [&](int i) {
+                return join16(*(const uint4 *)(pa + i * 16 * kBK + swz), *(const uint4 *)(pa + i * 16 * kBK + (swz ^ 64u)));
+            };
             v8i32 fb[FN];
+            v8i32 fa = frag_a(0);
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 if constexpr (KIND == kKN) {
@@ -546,20 +643,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                         // 16 lanes read 8 rows of k x 16 columns; two neighbouring lanes cover a row
                         const int kr = (h >> 1) * 64 + 16 * g + 8 * (h & 1) + (r16 >> 1);
                         const int ch = (wn * TN + 16 * j) / 16;
-                        const uint8_t *src = tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1);
-                            q[h] = read_transposed(src);
+                        q[h] = read_transposed(tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1));
                     }
                     fb[j] = v8i32{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
                 } else {
-                    const int row = wn * TN + 16 * j + r16;
-                    const uint8_t *src = tb + row * kBK;
-                    fb[j] = join16(*(const uint4 *)(src + ((g ^ (row & 7)) << 4)),
-                                   *(const uint4 *)(src + (((g + 4) ^ (row & 7)) << 4)));
+                    const uint8_t *src = tb + (wn * TN + r16) * kBK + j * 16 * kBK;
+                    fb[j] = join16(*(const uint4 *)(src + swz), *(const uint4 *)(src + (swz ^ 64u)));
                 }
             }
-            float sbu = 0.0f;
             v4f32 sbg[FN];
             int ebg[FN];
+            float sa[FM];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa[i] = sc[wm * TM + 16 * i + r16];
             if constexpr (KIND == kGroups) {
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
@@ -567,74 +663,292 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                     else sbg[j] = *(const v4f32 *)(sc + BM + wn * TN + 16 * j + 4 * g);
                 }
             } else {
-                sbu = sc[BM + wn * TN / 128];
+                const float sbu = sc[BM + wn * TN / 128];
+                if constexpr (POW2) {
 #pragma unroll
-                for (int j = 0; j < FN; ++j) ebg[j] = __float_as_int(sbu);
+                    for (int j = 0; j < FN; ++j) ebg[j] = __float_as_int(sbu);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) sa[i] *= sbu;
+                }
             }
+            v4f32 part[2][FN];
+            auto scale = [&](int i) {                   // acc += part * (1/Sa 1/Sb)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (KIND == kGroups) acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e] * sa[i], sbg[j][e], acc[i][j][e]);
+                        else acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], sa[i], acc[i][j][e]);
+                    }
+            };
+            constexpr int PI = (LT + FM - 1) / FM;      // load pieces issued per fragment
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
-                const int row = wm * TM + 16 * i + r16;
-                const uint8_t *src = ta + row * kBK;
-                const v8i32 fa = join16(*(const uint4 *)(src + ((g ^ (row & 7)) << 4)),
-                                        *(const uint4 *)(src + (((g + 4) ^ (row & 7)) << 4)));
-                const float sa = sc[row];
+                v8i32 next;
+                if (i + 1 < FM) next = frag_a(i + 1);
+#pragma unroll
+                for (int u = i * PI; u < (i + 1) * PI && u < LT; ++u) load_piece(stage, u);
                 if constexpr (POW2) {
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
-                        const v4f32 c = mfma_e8m0<FA, FB>(fb[j], fa, v4f32{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]},
-                                                          ebg[j], __float_as_int(sa));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = c[e];
+                        acc[i][j] = mfma_e8m0<FA, FB>(fb[j], fa, acc[i][j], ebg[j], __float_as_int(sa[i]));
                     }
                 } else {
-                    v4f32 part[FN];
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) part[j] = mfma_raw<FA, FB>(fb[j], fa, v4f32{0.0f, 0.0f, 0.0f, 0.0f});
+                    for (int j = 0; j < FN; ++j) part[i & 1][j] = mfma_raw<FA, FB>(fb[j], fa, v4f32{0.0f, 0.0f, 0.0f, 0.0f});
+                    if (i > 0) scale(i - 1);
+                }
+                if (i + 1 < FM) fa = next;
+            }
+            if constexpr (!POW2) scale(FM - 1);
+        }
+    }
+    wait_vmem();                                        // no load may still write LDS when the workgroup ends
+
+    store_tile<KIND, EXACT, TM, TN>(p, pl, wm, wn, lane, acc);
+}
+
+// ---- the large tile in two alternating groups of waves --------------------------------------------
+//
+// 256 x 256 outputs, 8 waves of 128 x 64, two on each SIMD: wave w and w + 4. A step of k is four
+// phases with a barrier after each, and the second four waves run one phase behind the first:
+//
+//   P0  read b's fragments and a's first half from LDS      P1  16 MFMAs a wave and their scaling
+//   P2  read a's second half                                 P3  16 MFMAs a wave and their scaling
+//
+// so on every SIMD one wave feeds the matrix core while the other reads. In the plain form of the
+// tile both waves of a SIMD wait for the same barrier and the same reads: the matrix core was busy
+// 40% of the time on 8192 x 7168 x 18432 (1143 us).
+// Loads go to LDS as soon as a region is free in both groups: P2 of step s loads b, a's first halves
+// and a column of scales for step s + 2 (7 loads a wave), P0 loads a's second halves for step
+// s + 1 (2 loads); each has five to six phases to arrive and is waited for by count (9 newer loads may be in
+// flight). Scales arrive one step earlier than their codes; P0 of the step before inverts them, one
+// per thread.
+template <int FA, int FB, int KIND, int MATH>
+__global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
+    static_assert(KIND != kGroups && MATH != kMathExact, "one scale of b for each wave and step");
+    constexpr int BM = 256, BN = 256, WN = 4, NT = 512, TM = 128, TN = 64, FM = 8, FN = 4;
+    constexpr bool POW2 = MATH == kMathE8m0;
+    constexpr int kA = BM * kBK, kB = BN * kBK, kStage = kA + kB;
+    __shared__ __attribute__((aligned(1024))) uint8_t tiles[2][kStage];
+    __shared__ __attribute__((aligned(256))) float raw[2][BM + BN];
+    __shared__ __attribute__((aligned(16))) float inv[2][BM + BN];
+
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, g = lane >> 4;
+    TilePlace pl;
+    if (!place_tile(p, BM, BN, pl)) return;
+    const int steps = pl.expert < 0 || pl.k1 <= pl.k0 ? 0 : (int)((pl.k1 - pl.k0 + kBK - 1) / kBK);
+    const int kend = (int)(pl.k1 - pl.k0);
+    const int gk = (int)((p.k + kBK - 1) / kBK), g0 = (int)(pl.k0 / kBK);
+
+    v4f32 acc[FM][FN];
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) {
-                        if constexpr (KIND == kGroups) {
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[j][e] * sa, sbg[j][e], acc[i][j][e]);
-                        } else {
-                            const float f = sa * sbu;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[j][e], f, acc[i][j][e]);
-                        }
-                    }
+        for (int j = 0; j < FN; ++j) acc[i][j] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+
+    if (steps > 0) {
+        TileLoads<KIND, false, BM, BN, TN, NT> ld;
+        ld.init(p, pl, steps, t);
+        // thread u < 256 loads the scale of a's row u, u >= 256 that of b's block u % 2; waves 0-3 and
+        // 4-7 each use one buffer.
+        MovingBuffer bs;
+        uint32_t vs, step_s = 4;
+        {
+            const int gn = (p.n + 127) / 128, e = pl.expert > 0 ? pl.expert : 0;
+            if (wave < 4) {
+                const int64_t first = p.rows ? 0 : pl.row0;
+                bs.base = uniform64((uint64_t)(uintptr_t)(p.sa + first * gk + g0));
+                const int64_t left = ((p.rows ? p.a_rows : p.m) - first) * gk - g0;
+                bs.left = left > 0x3FFFFFFF ? 0xFFFFFFFCu : (uint32_t)left * 4u;
+                vs = (uint32_t)((source_row(p, pl, t) - first) * gk * 4);
+            } else {
+                int nb = (t & 1) < gn - pl.n0 / 128 ? t & 1 : 0;
+                if constexpr (KIND == kNK) {
+                    bs.base = uniform64((uint64_t)(uintptr_t)(p.sb + ((int64_t)e * gn + pl.n0 / 128) * gk + g0));
+                    bs.left = cap31(((int64_t)(gn - pl.n0 / 128) * gk - g0) * 4);
+                    vs = (uint32_t)(nb * gk * 4);
+                } else {
+                    bs.base = uniform64((uint64_t)(uintptr_t)(p.sb + ((int64_t)e * gk + g0) * gn + pl.n0 / 128));
+                    bs.left = cap31(((int64_t)(gk - g0) * gn - pl.n0 / 128) * 4);
+                    vs = (uint32_t)(nb * 4);
+                    step_s = (uint32_t)gn * 4u;
                 }
             }
+            bs.left = __builtin_amdgcn_readfirstlane((int)bs.left);
         }
-    }
+        const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)lds_address(&tiles[0][0])) + (uint32_t)wave * 1024u;
+        const uint32_t lds_raw = __builtin_amdgcn_readfirstlane((int)lds_address(&raw[0][0])) + (uint32_t)wave * 256u;
 
-    // ---- store
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int r = wm * TM + FR * i + (EXACT ? lane & 31 : r16);
-        if (r >= pl.rows) continue;
-        const int64_t row = pl.row0 + r;
-        bool zero = false;
-        if (gather) {
-            const int64_t src = p.rows[row];
-            zero = src < 0 || src >= p.a_rows;
-        }
-        // runs of neighbouring columns: all a lane holds, or 4 with KN, whose columns keep their order
-        constexpr int PER = TN * FR / 64, RUN = KIND == kKN ? 4 : PER;
-        const int q = lane / FR;
-#pragma unroll
-        for (int u = 0; u < PER / RUN; ++u) {
-            int n = pl.n0 + wn * TN;
-            if constexpr (KIND != kKN) n += q * PER;
-            else if constexpr (EXACT) n += 32 * (u >> 2) + 8 * (u & 3) + 4 * q;
-            else n += 16 * u + 4 * q;
-            float v[RUN];
-#pragma unroll
-            for (int e = 0; e < RUN; ++e) {
-                const int at = u * RUN + e;
-                v[e] = zero ? 0.0f : acc[i][at / FV][at % FV];
+        // Each stream of loads has its own position along k; past the last step its buffer has length 0
+        // and the loads leave zeros nobody uses.
+        MovingBuffer first = ld.ba, second = ld.ba, cols = ld.bb;
+        int n_first = 0, n_second = 0, n_scale = 0;
+        auto load_first = [&](int u) {                  // piece u of 6: b and a's first halves of step n_first
+            const uint32_t at = lds0 + (uint32_t)(n_first & 1) * kStage;
+            if (u == 0 && n_first >= steps) first.left = cols.left = 0;
+            if (u < 4) lds_dma16(cols.rsrc(), ld.vb[u], at + kA + (uint32_t)u * 8192u);
+            else lds_dma16(first.rsrc(), ld.va[2 * (u - 4)], at + (uint32_t)(u - 4) * 2u * 8192u);
+            if (u == 5) {
+                first.advance(kBK);
+                cols.advance(ld.stepb);
+                ++n_first;
             }
-            store_run<RUN>(p, pl, row, n, v);
+        };
+        auto load_second = [&](int u) {                 // piece u of 2: a's second halves of step n_second
+            const uint32_t at = lds0 + (uint32_t)(n_second & 1) * kStage;
+            if (u == 0 && n_second >= steps) second.left = 0;
+            lds_dma16(second.rsrc(), ld.va[2 * u + 1], at + (2u * u + 1u) * 8192u);
+            if (u == 1) {
+                second.advance(kBK);
+                ++n_second;
+            }
+        };
+        auto load_scale = [&]() {
+            if (n_scale >= steps) bs.left = 0;
+            lds_dma4(bs.rsrc(), vs, lds_raw + (uint32_t)(n_scale & 1) * (BM + BN) * 4u);
+            bs.advance(step_s);
+            ++n_scale;
+        };
+
+        load_scale();
+#pragma unroll
+        for (int u = 0; u < 6; ++u) load_first(u);
+        load_scale();
+        load_second(0);
+        load_second(1);
+#pragma unroll
+        for (int u = 0; u < 6; ++u) load_first(u);
+        wait_vmem_but<6>();
+        phase_end();
+        inv[0][t] = inverse_scale<POW2>(raw[0][t]);
+        phase_end();
+        load_scale();                                   // into the place of the scales just read
+        if (wave >= 4) phase_end();                     // one phase behind
+
+        const uint32_t swz = (uint32_t)((g ^ swizzle(r16)) << 4);
+        v8i32 fa[4], fb[FN];
+        // Product m of a phase goes to part[m % 4] and is scaled three products later (the last three
+        // in the next phase), when it is complete without a wait.
+        v4f32 part[4] = {};
+        float sa[4] = {}, late = 0.0f;
+        int eb = 0;
+        auto scale_one = [&](int i, int j, float f) {   // acc += part * (1/Sa 1/Sb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[j][e], f, acc[i][j][e]);
+            asm volatile("" : "+v"(acc[i][j]));         // here, not after a later branch: part is used again
+        };
+        // codes past k in the last step: chunk g holds k = 16 g + [0, 16) of a fragment, chunk g + 4 64 more
+        auto trim = [&](v8i32 f, int krem) {
+            asm volatile("" : "+s"(krem));              // keeps the masks inside the branch
+            const uint4 lo = keep_bytes(make_uint4(f[0], f[1], f[2], f[3]), krem - 16 * g);
+            const uint4 hi = keep_bytes(make_uint4(f[4], f[5], f[6], f[7]), krem - 64 - 16 * g);
+            return join16(lo, hi);
+        };
+        auto read_a = [&](const uint8_t *ta, const float *sc, int half) {
+            const uint8_t *src = ta + (wm * TM + half * 64 + r16) * kBK;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                fa[i] = join16(*(const uint4 *)(src + i * 16 * kBK + swz), *(const uint4 *)(src + i * 16 * kBK + (swz ^ 64u)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sa[i] = sc[wm * TM + half * 64 + 16 * i + r16];
+            const float sbu = sc[BM + wn / 2];
+            eb = __float_as_int(sbu);
+            if constexpr (!POW2) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sa[i] *= sbu;
+                    asm volatile("" : "+v"(sa[i]));     // before the phase ends
+                }
+            }
+        };
+        // 16 products. Between them go the loads (a load of 1 KiB takes the path to LDS for 16 cycles:
+        // issued in a row they would hold up the wave) and, in the first half, the next step's scales.
+        auto products = [&](int half, int s) {
+            __builtin_amdgcn_s_setprio(1);
+            float next = 1.0f;
+            if (half == 0) next = raw[(s + 1) & 1][t];
+#pragma unroll
+            for (int m = 0; m < 4 * FN; ++m) {
+                const int i = m / FN, j = m % FN, at = half * 4 + i;
+                if constexpr (POW2) {
+                    acc[at][j] = mfma_e8m0<FA, FB>(fb[j], fa[i], acc[at][j], eb, __float_as_int(sa[i]));
+                    asm volatile("" : "+v"(acc[at][j]));
+                } else {
+                    part[j] = mfma_raw<FA, FB>(fb[j], fa[i], v4f32{0.0f, 0.0f, 0.0f, 0.0f});
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (m < 3) scale_one((half * 4 + 7) % 8, m + 1, late);
+                    else scale_one(half * 4 + (m - 3) / FN, (m - 3) % FN, sa[(m - 3) / FN]);
+                }
+                if (half == 0) {
+                    if (m == 4 || m == 8) load_second(m / 4 - 1);
+                    if (m == 5) asm volatile("" : "+v"(next));
+                    if (m == 11) inv[(s + 1) & 1][t] = inverse_scale<POW2>(next);
+                } else {
+                    if (m % 2 == 0 && m / 2 < 6) load_first(m / 2);
+                    if (m == 12) load_scale();
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            late = sa[3];
+            __builtin_amdgcn_s_setprio(0);
+        };
+
+        for (int s = 0; s < steps; ++s) {
+            const uint8_t *const ta = tiles[s & 1], *const tb = ta + kA;
+            const float *const sc = inv[s & 1];
+            const int krem = kend - s * kBK;
+            // P0
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                if constexpr (KIND == kKN) {
+                    v2i32 q[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const int kr = (h >> 1) * 64 + 16 * g + 8 * (h & 1) + (r16 >> 1);
+                        const int ch = (wn * TN + 16 * j) / 16;
+                        q[h] = read_transposed(tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1));
+                    }
+                    fb[j] = v8i32{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
+                } else {
+                    const uint8_t *src = tb + (wn * TN + r16) * kBK + j * 16 * kBK;
+                    fb[j] = join16(*(const uint4 *)(src + swz), *(const uint4 *)(src + (swz ^ 64u)));
+                }
+            }
+            read_a(ta, sc, 0);
+            if (krem < kBK) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) fb[j] = trim(fb[j], krem);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fa[i] = trim(fa[i], krem);
+            }
+            wait_vmem_but<7>();                         // a's second halves of this step
+            phase_end();
+            // P1
+            products(0, s);
+            phase_end();
+            // P2
+            read_a(ta, sc, 1);
+            if (krem < kBK) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fa[i] = trim(fa[i], krem);
+            }
+            wait_vmem_but<2>();                         // b and a's first halves of the next
+            phase_end();
+            // P3
+            products(1, s);
+            phase_end();
         }
+        if constexpr (!POW2) {
+#pragma unroll
+            for (int j = 1; j < FN; ++j) scale_one(FM - 1, j, late);
+        }
+        if (wave < 4) phase_end();                      // the others are one phase behind
+        wait_vmem();                                    // no load may still write LDS when the workgroup ends
     }
+    store_tile<KIND, false, TM, TN>(p, pl, wm, wn, lane, acc);
 }
 
 // ---- launch ----------------------------------------------------------------------------------------
@@ -648,7 +962,8 @@ int launch_matmul_tile(const MatmulArgs &p, int size, int64_t groups, hipStream_
     const dim3 grid((unsigned)groups);
     if (size == 0) {
         if constexpr (MATH == kMathExact) hipLaunchKernelGGL((matmul_tile_kernel<FA, FB, KIND, MATH, 256, 128, 4, 2>), grid, dim3(512), 0, s, p);
-        else hipLaunchKernelGGL((matmul_tile_kernel<FA, FB, KIND, MATH, 256, 256, 2, 4>), grid, dim3(512), 0, s, p);
+        else if constexpr (KIND == kGroups) hipLaunchKernelGGL((matmul_tile_kernel<FA, FB, KIND, MATH, 256, 256, 2, 4>), grid, dim3(512), 0, s, p);
+        else hipLaunchKernelGGL((matmul_large_kernel<FA, FB, KIND, MATH>), grid, dim3(512), 0, s, p);
     } else if (size == 1) {
         hipLaunchKernelGGL((matmul_tile_kernel<FA, FB, KIND, MATH, 128, 128, 2, 2>), grid, dim3(256), 0, s, p);
     } else {

@@ -20,7 +20,7 @@ struct Plan { int size, splits; int64_t split_k; };
 // that fit on one), a round costs its steps of k.
 Plan plan_matmul(int64_t m, int64_t n, int64_t k, int parts, bool may_split, bool exact) {
     constexpr int kFit[] = {1, 2, 3};                                                  // workgroups per CU (LDS)
-    constexpr double kStep[2][3] = {{2600.0, 1500.0, 1400.0}, {3000.0, 3200.0, 2600.0}};   // cycles of one step of a full CU
+    constexpr double kStep[2][3] = {{4300.0, 2900.0, 2550.0}, {5100.0, 4600.0, 4400.0}};   // cycles of one step of a full CU
     const TileSize *sizes = kTileSizes[exact];
     const int64_t steps = (k + kBK - 1) / kBK;
     Plan best = {2, 1, steps * kBK};
