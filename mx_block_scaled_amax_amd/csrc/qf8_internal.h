@@ -108,7 +108,7 @@ struct MatmulArgs {
     int64_t m, k, a_rows;
     int n, experts, mode, splits;
     int64_t split_k;             // k of one split, a multiple of 128
-    int out_bf16, vec;           // vec: 16-byte stores fit every row
+    int out_bf16;
 };
 int launch_matmul(const MatmulArgs &p, int fmt_a, int fmt_b, int kind, int pow2, float *ws, hipStream_t s);
 // Bytes of partial sums launch_matmul uses for a dense product (0: none).

@@ -12,6 +12,8 @@
 //               accumulates in place, without VALU work.
 //   kMathExact  the codes become BF16 (exactly) and go through 32x32x16 BF16 MFMAs, the group's sum
 //               then scaled by an FMA.
+//   kMathExactPow2  the same with power-of-two scales: the conversion to BF16 multiplies by 1/S,
+//               which is still exact, and the sums need no scaling.
 // Why two precisions: the FP8 MFMAs of gfx950 align the products of each 8 neighbours along k to the
 // largest of them and keep 14 bits (measured: beside a product of 2^16 one of 2^3 counts and one of
 // 2^2 is lost; 1.4e-5 relative error on normal data, for the 16x16x32 form too), while the BF16
@@ -36,7 +38,7 @@ typedef float v16f32 __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
 
 enum { kNK = 0, kKN = 1, kGroups = 2 };
-enum { kMathFp8 = 0, kMathE8m0 = 1, kMathExact = 2 };
+enum { kMathFp8 = 0, kMathE8m0 = 1, kMathExact = 2, kMathExactPow2 = 3 };
 constexpr int kBK = 128;                                  // bytes of k per step: one scale group
 
 // ---- pieces ------------------------------------------------------------------------------------
@@ -105,9 +107,9 @@ __device__ __forceinline__ v2i32 read_transposed(const uint8_t *p) {
 }
 
 // 1/S, or for power-of-two scales the E8M0 byte of 1/S from S's exponent field.
-template <bool POW2>
+template <int MATH>
 __device__ __forceinline__ float inverse_scale(float s) {
-    if constexpr (POW2) return __uint_as_float(umax(254u - umin((__float_as_uint(s) >> 23) & 0xFFu, 254u), 0u));
+    if constexpr (MATH == kMathE8m0) return __uint_as_float(umax(254u - umin((__float_as_uint(s) >> 23) & 0xFFu, 254u), 0u));
     else return 1.0f / s;
 }
 
@@ -125,31 +127,32 @@ __device__ __forceinline__ v8i32 join16(uint4 lo, uint4 hi) {
     return r;
 }
 
-// 8 codes -> 8 BF16 values (exact for both formats).
+// 8 codes times a power of two -> 8 BF16 values (exact for both formats, down to BF16's subnormals).
 template <int F>
-__device__ __forceinline__ v8bf16 codes_to_bf16(uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ v8bf16 codes_to_bf16(uint32_t lo, uint32_t hi, float f = 1.0f) {
     v2bf16 p[4];
     if constexpr (F == kE4M3) {
-        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, false);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, true);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, false);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, true);
     } else {
-        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false);
-        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true);
-        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false);
-        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true);
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, f, false);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, f, true);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, f, false);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, f, true);
     }
     return v8bf16{p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y};
 }
 
-// Where LDS row rho of a wave's TN rows of b lies among its TN columns of y. The result of an MFMA
-// gives a lane rows 4 q + i of every 16 (FP8) or 8 q + 4 h + i of every 32 (BF16); with this order
-// they are TN/4 (TN/2) neighbouring columns, stored 16 bytes at a time.
-template <int TN, bool EXACT>
+// Where LDS row rho of a wave's TN rows of b lies among its TN columns of y. An FP8 MFMA's result
+// gives a lane rows 4 q + i of every 16; in this order two fragments make 8 neighbouring columns, so
+// a lane stores 16 bytes at a time and four lanes 64. (BF16 MFMAs run with a first: a lane has one
+// column, and the natural order stores whole lines.)
+template <bool EXACT>
 __device__ __forceinline__ int column_of(int rho) {
-    if constexpr (EXACT) return ((rho >> 2) & 1) * (TN / 2) + 16 * (rho >> 5) + 4 * ((rho >> 3) & 3) + (rho & 3);
-    else return ((rho >> 2) & 3) * (TN / 4) + 4 * (rho >> 4) + (rho & 3);
+    if constexpr (EXACT) return rho;
+    else return (rho & ~31) + 8 * ((rho >> 2) & 3) + 4 * ((rho >> 4) & 1) + (rho & 3);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -238,32 +241,28 @@ __device__ __forceinline__ int find_row_tile(const int32_t *offsets, int experts
     return total;
 }
 
-// RUN neighbouring columns of one row, rounded once to BF16 or stored as FP32.
+// RUN neighbouring columns of one row, rounded once to BF16 or stored as FP32. Rows need no alignment:
+// 16-byte stores may start at any element.
 template <int RUN>
 __device__ __forceinline__ void store_run(const MatmulArgs &p, const TilePlace &pl, int64_t row, int n, const float *v) {
     const int64_t plane = p.mode == kMatmulExpertsK ? pl.expert : pl.split;
     const int64_t at = (plane * p.m + row) * p.n + n;
     if (p.out_bf16) {
         uint16_t *y = (uint16_t *)p.y + at;
-        if (p.vec && n + RUN <= p.n) {
-            if constexpr (RUN % 8 == 0) {
+        uint32_t w[RUN / 2];
 #pragma unroll
-                for (int e = 0; e < RUN; e += 8)
-                    *(uint4 *)(y + e) = make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]),
-                                                   pack_bf16(v[e + 4], v[e + 5]), pack_bf16(v[e + 6], v[e + 7]));
-            } else {
-                *(uint2 *)y = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-            }
+        for (int e = 0; e < RUN; e += 2) w[e / 2] = pack_bf16(v[e], v[e + 1]);
+        if (n + RUN <= p.n) {
+            __builtin_memcpy(y, w, sizeof(w));
         } else {
 #pragma unroll
             for (int e = 0; e < RUN; ++e)
-                if (n + e < p.n) y[e] = (uint16_t)pack_bf16(v[e], 0.0f);
+                if (n + e < p.n) y[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
         }
     } else {
         float *y = (float *)p.y + at;
-        if (p.vec && n + RUN <= p.n) {
-#pragma unroll
-            for (int e = 0; e < RUN; e += 4) *(float4 *)(y + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        if (n + RUN <= p.n) {
+            __builtin_memcpy(y, v, RUN * sizeof(float));
         } else {
 #pragma unroll
             for (int e = 0; e < RUN; ++e)
@@ -369,7 +368,7 @@ struct TileLoads {
 #pragma unroll
             for (int i = 0; i < LB; ++i) {
                 const int id = i * NT + t, row = id >> 3, ch = (id & 7) ^ swizzle(row);
-                int n = (row / TN) * TN + column_of<TN, EXACT>(row % TN);
+                int n = column_of<EXACT>(row);
                 n = n < p.n - pl.n0 ? n : p.n - pl.n0 - 1;
                 vb[i] = (uint32_t)n * (uint32_t)p.k + 16u * ch;
             }
@@ -379,64 +378,122 @@ struct TileLoads {
     }
 };
 
+// Row `row` of the output takes no values: its entry in rows names no row of a.
+__device__ __forceinline__ bool no_source(const MatmulArgs &p, int64_t row) {
+    if (!p.rows) return false;
+    const int64_t src = p.rows[row];
+    return src < 0 || src >= p.a_rows;
+}
+
 // Stores a wave's TM x TN values.
 template <int KIND, bool EXACT, int TM, int TN, typename V, int FM, int FN>
 __device__ __forceinline__ void store_tile(const MatmulArgs &p, const TilePlace &pl, int wm, int wn, int lane,
                                            const V (&acc)[FM][FN]) {
-    constexpr int FR = EXACT ? 32 : 16, FV = FR * FR / 64;
+    if constexpr (EXACT) {                               // lane: column lane % 32, rows 8 q + 4 (lane / 32) + e
+        const int64_t plane = p.mode == kMatmulExpertsK ? pl.expert : pl.split;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int r = wm * TM + FR * i + (lane % FR);
-        if (r >= pl.rows) continue;
-        const int64_t row = pl.row0 + r;
-        bool zero = false;
-        if (p.rows) {
-            const int64_t src = p.rows[row];
-            zero = src < 0 || src >= p.a_rows;
-        }
-        // runs of neighbouring columns: all a lane holds, or 4 with KN, whose columns keep their order
-        constexpr int PER = TN * FR / 64, RUN = KIND == kKN ? 4 : PER;
-        const int q = lane / FR;
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int u = 0; u < PER / RUN; ++u) {
-            int n = pl.n0 + wn * TN;
-            if constexpr (KIND != kKN) n += q * PER;
-            else if constexpr (EXACT) n += 32 * (u >> 2) + 8 * (u & 3) + 4 * q;
-            else n += 16 * u + 4 * q;
-            float v[RUN];
+            for (int e = 0; e < 16; ++e) {
+                const int r = wm * TM + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+                if (r >= pl.rows) continue;
+                const int64_t row = pl.row0 + r;
+                const bool zero = no_source(p, row);
+                float *y = (float *)p.y + (plane * p.m + row) * p.n;
 #pragma unroll
-            for (int e = 0; e < RUN; ++e) {
-                const int at = u * RUN + e;
-                v[e] = zero ? 0.0f : acc[i][at / FV][at % FV];
+                for (int j = 0; j < FN; ++j) {
+                    const int n = pl.n0 + wn * TN + 32 * j + (lane & 31);
+                    if (n < p.n) y[n] = zero ? 0.0f : acc[i][j][e];
+                }
             }
-            store_run<RUN>(p, pl, row, n, v);
+    } else {                                             // lane: row lane % 16
+        const int g = lane >> 4;
+        constexpr int RUN = KIND == kKN || FN == 1 ? 4 : 8;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int r = wm * TM + 16 * i + (lane & 15);
+            if (r >= pl.rows) continue;
+            const int64_t row = pl.row0 + r;
+            const bool zero = no_source(p, row);
+#pragma unroll
+            for (int u = 0; u < 4 * FN / RUN; ++u) {
+                float v[RUN];
+#pragma unroll
+                for (int e = 0; e < RUN; ++e) v[e] = zero ? 0.0f : acc[i][u * (RUN / 4) + e / 4][e % 4];
+                store_run<RUN>(p, pl, row, pl.n0 + wn * TN + 4 * RUN * u + RUN * g, v);
+            }
         }
     }
 }
 
+// Scales of a tile for one group of k: thread u < BA loads that of a's row u, u >= BA one of b's, of its
+// LDS row u - BA (groups) or of block (u - BA) % BLOCKS. A wave uses one buffer.
+template <int KIND, bool EXACT, int BM, int BN, int NT>
+struct ScaleLoads {
+    static constexpr int BA = BM < 64 ? 64 : BM, BLOCKS = (BN + 127) / 128;
+    static_assert(KIND == kGroups ? BA + BN <= NT : BA < NT, "one scale per thread");
+    MovingBuffer buf;
+    uint32_t off, step;
+
+    __device__ __forceinline__ void init(const MatmulArgs &p, const TilePlace &pl, int t, int wave, int gk, int g0) {
+        const int gn = (p.n + 127) / 128, e = pl.expert > 0 ? pl.expert : 0;
+        step = 4;
+        if (wave < BA / 64) {
+            const int64_t first = p.rows ? 0 : pl.row0;
+            buf.base = uniform64((uint64_t)(uintptr_t)(p.sa + first * gk + g0));
+            const int64_t left = ((p.rows ? p.a_rows : p.m) - first) * gk - g0;
+            buf.left = left > 0x3FFFFFFF ? 0xFFFFFFFCu : (uint32_t)left * 4u;
+            off = (uint32_t)((source_row(p, pl, t) - first) * gk * 4);
+        } else if constexpr (KIND == kGroups) {
+            buf.base = uniform64((uint64_t)(uintptr_t)(p.sb + (int64_t)pl.n0 * gk + g0));
+            buf.left = cap31(((int64_t)(p.n - pl.n0) * gk - g0) * 4);
+            int n = column_of<EXACT>(t - BA);
+            n = n < p.n - pl.n0 ? n : p.n - pl.n0 - 1;
+            off = (uint32_t)n * (uint32_t)gk * 4u;
+        } else {
+            const int v = (t - BA) % BLOCKS, nb = v < gn - pl.n0 / 128 ? v : 0;
+            if constexpr (KIND == kNK) {
+                buf.base = uniform64((uint64_t)(uintptr_t)(p.sb + ((int64_t)e * gn + pl.n0 / 128) * gk + g0));
+                buf.left = cap31(((int64_t)(gn - pl.n0 / 128) * gk - g0) * 4);
+                off = (uint32_t)nb * (uint32_t)gk * 4u;
+            } else {                                     // scales [k/128][n/128]
+                buf.base = uniform64((uint64_t)(uintptr_t)(p.sb + ((int64_t)e * gk + g0) * gn + pl.n0 / 128));
+                buf.left = cap31(((int64_t)(gk - g0) * gn - pl.n0 / 128) * 4);
+                off = (uint32_t)nb * 4u;
+                step = (uint32_t)gn * 4u;
+            }
+        }
+        buf.left = __builtin_amdgcn_readfirstlane((int)buf.left);
+    }
+};
+
 // ---- the tiled kernel ---------------------------------------------------------------------------
 
 // BM x BN outputs per workgroup, WM x WN waves. Operand tiles of 128 bytes of k go straight from
-// memory to LDS, double-buffered: the loads of step s+1 run under the products of step s, with one
-// barrier a step.
+// memory to LDS into a ring of D stages: the loads of step s + D - 1 are issued under the products of
+// step s and waited for by count, with one barrier a step. Many workgroups hide each other's
+// latency with D = 2; a grid of about one workgroup per CU needs a deep ring (64 x 128 with D = 6 keeps
+// 120 KB in flight).
 //
 // LDS tiles of rows along k (a, and b unless KN): 128-byte rows of eight 16-byte chunks, chunk c of
 // row r at position c ^ swizzle(r). The lanes of the load fetch the permuted chunk, which stays
 // inside the same 128 bytes of memory.
 // KN: b's tile keeps k as rows of BN bytes (chunk c of row k at c ^ (k & 7)) and the transposing
 // LDS read hands each lane 8 codes along k of one column.
-template <int FA, int FB, int KIND, int MATH, int BM, int BN, int WM, int WN>
+// Scales come one step ahead of their codes, as they are; each thread inverts one of them.
+template <int FA, int FB, int KIND, int MATH, int BM, int BN, int WM, int WN, int D>
 __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs p) {
     constexpr int NT = 64 * WM * WN, TM = BM / WM, TN = BN / WN;
-    constexpr bool POW2 = MATH == kMathE8m0, EXACT = MATH == kMathExact;
+    constexpr bool POW2 = MATH == kMathE8m0 || MATH == kMathExactPow2, EXACT = MATH >= kMathExact;
     constexpr int FR = EXACT ? 32 : 16, FM = TM / FR, FN = TN / FR;      // fragments
     constexpr int kA = BM * kBK, kB = BN * kBK, kStage = kA + kB;
-    constexpr int LA = kA / 16 / NT, LB = kB / 16 / NT;   // loads per thread and step
-    constexpr int SB = KIND == kGroups ? BN : (BN + 127) / 128;
+    typedef TileLoads<KIND, EXACT, BM, BN, TN, NT> Loads;
+    typedef ScaleLoads<KIND, EXACT, BM, BN, NT> Scales;
+    constexpr int LA = Loads::LA, LB = Loads::LB, LT = LA + LB, BA = Scales::BA;
     static_assert(LA * NT * 16 == kA && LB * NT * 16 == kB, "tile and workgroup do not match");
-    static_assert(BM + SB <= NT * 2, "scales");
-    __shared__ __attribute__((aligned(1024))) uint8_t tiles[2][kStage];
-    __shared__ float scales[2][BM + SB];
+    __shared__ __attribute__((aligned(1024))) uint8_t tiles[D][kStage];
+    __shared__ __attribute__((aligned(256))) float raw[D][NT];
+    __shared__ __attribute__((aligned(16))) float inv[2][NT];
 
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave / WN, wn = wave % WN, r16 = lane & 15, g = lane >> 4;
@@ -447,44 +504,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     const int kend = (int)(pl.k1 - pl.k0);
     const int gk = (int)((p.k + kBK - 1) / kBK), g0 = (int)(pl.k0 / kBK);
 
-    TileLoads<KIND, EXACT, BM, BN, TN, NT> ld;
+    Loads ld;
     ld.init(p, pl, steps, t);
-    MovingBuffer &ba = ld.ba, &bb = ld.bb;
-    const auto &va = ld.va;
-    const auto &vb = ld.vb;
-    const uint32_t stepb = ld.stepb;
-
-    // ---- scale addresses: thread u < BM loads a row's scale, BM <= u < BM + SB one of b
-    constexpr int LS = (BM + SB + NT - 1) / NT;
-    const float *sp[LS];
-#pragma unroll
-    for (int i = 0; i < LS; ++i) {
-        const int u = i * NT + t;
-        if (u < BM) {
-            const int64_t r = source_row(p, pl, u);
-            sp[i] = p.sa + (steps ? r : 0) * gk + g0;
-        } else if (u < BM + SB) {
-            const int v = u - BM;
-            if constexpr (KIND == kGroups) {
-                int n = pl.n0 + (v / TN) * TN + column_of<TN, EXACT>(v % TN);
-                n = n < p.n ? n : p.n - 1;
-                sp[i] = p.sb + (int64_t)n * gk + g0;
-            } else if constexpr (KIND == kNK) {
-                const int gn = (p.n + 127) / 128;
-                int nb = pl.n0 / 128 + v;
-                nb = nb < gn ? nb : gn - 1;
-                sp[i] = p.sb + ((int64_t)(pl.expert > 0 ? pl.expert : 0) * gn + nb) * gk + g0;
-            } else {                                    // scales [k/128][n/128]: one row of them per step
-                const int gn = (p.n + 127) / 128;
-                int nb = pl.n0 / 128 + v;
-                nb = nb < gn ? nb : gn - 1;
-                sp[i] = p.sb + ((int64_t)(pl.expert > 0 ? pl.expert : 0) * gk + g0) * gn + nb;
-            }
-        } else {
-            sp[i] = nullptr;
-        }
-    }
-    const int sstep_b = KIND == kKN ? (p.n + 127) / 128 : 1;
+    Scales ls;
+    if (steps) ls.init(p, pl, t, wave, gk, g0);
 
     constexpr int FV = FR * FR / 64;                     // values of a fragment in a lane
     typedef float frag __attribute__((ext_vector_type(FV)));
@@ -494,47 +517,49 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = (frag)0.0f;
 
+    // The loads of step n_load: piece u of LA + LB, then the scales of step n_load + 1. Past the last
+    // step the buffers have length 0: the loads still run, so that counts hold, and leave zeros nobody uses.
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)lds_address(&tiles[0][0])) + (uint32_t)wave * 1024u;
-    // The loads of a step: piece u of LA + LB, then advance. Past the last step the descriptors have
-    // length 0: the loads still run, read nothing and leave zeros in a buffer nobody reads.
-    constexpr int LT = LA + LB;
-    v4i32 ra = ba.rsrc(), rb = bb.rsrc();
-    auto load_piece = [&](int stage, int u) {
-        const uint32_t at = lds0 + (uint32_t)stage * kStage + (u < LA ? 0u : (uint32_t)kA) + (uint32_t)(u < LA ? u : u - LA) * NT * 16;
-        if (u < LA) lds_dma16(ra, va[u < LA ? u : 0], at);
-        else lds_dma16(rb, vb[u < LA ? 0 : u - LA], at);
+    const uint32_t lds_raw = __builtin_amdgcn_readfirstlane((int)lds_address(&raw[0][0])) + (uint32_t)wave * 256u;
+    int n_load = 0, n_scale = 0, at_load = 0, at_scale = 0;              // steps, and their places in the rings
+    auto load_scale = [&]() {
+        if (n_scale >= steps) ls.buf.left = 0;
+        lds_dma4(ls.buf.rsrc(), ls.off, lds_raw + (uint32_t)at_scale * NT * 4u);
+        ls.buf.advance(ls.step);
+        ++n_scale;
+        at_scale = at_scale + 1 == D ? 0 : at_scale + 1;
     };
-    float sreg[LS];
-    auto load_scales = [&](bool more) {
-#pragma unroll
-        for (int i = 0; i < LS; ++i) {
-            if (sp[i]) {
-                sreg[i] = *sp[i];
-                sp[i] += more ? (i * NT + t < BM ? 1 : sstep_b) : 0;
-            }
+    auto load_piece = [&](int u) {
+        const uint32_t at = lds0 + (uint32_t)at_load * kStage;
+        if (u == 0 && n_load >= steps) ld.ba.left = ld.bb.left = 0;
+        if (u < LA) lds_dma16(ld.ba.rsrc(), ld.va[u < LA ? u : 0], at + (uint32_t)u * NT * 16u);
+        else if (u < LT) lds_dma16(ld.bb.rsrc(), ld.vb[u < LA ? 0 : u - LA], at + kA + (uint32_t)(u - LA) * NT * 16u);
+        if (u == LT) {
+            ld.ba.advance(kBK);
+            ld.bb.advance(ld.stepb);
+            load_scale();
+            ++n_load;
+            at_load = at_load + 1 == D ? 0 : at_load + 1;
         }
-    };
-    auto advance = [&](bool more) {
-        ba.advance(kBK);
-        bb.advance(stepb);
-        if (!more) ba.left = bb.left = 0;
-        ra = ba.rsrc();
-        rb = bb.rsrc();
     };
 
     if (steps) {
+        load_scale();
 #pragma unroll
-        for (int u = 0; u < LT; ++u) load_piece(0, u);
-        load_scales(steps > 1);
+        for (int d = 0; d < D - 1; ++d)
+#pragma unroll
+            for (int u = 0; u <= LT; ++u) load_piece(u);
+        wait_vmem_but<(D - 1) * (LT + 1)>();
+        phase_end();
+        inv[0][t] = inverse_scale<MATH>(raw[0][t]);
     }
+    int at = 0;                                          // stage of step s
     for (int s = 0; s < steps; ++s) {
-        wait_vmem();
-        float *sc = scales[s & 1];
-#pragma unroll
-        for (int i = 0; i < LS; ++i)
-            if (i * NT + t < BM + SB) sc[i * NT + t] = inverse_scale<POW2>(sreg[i]);
-        __syncthreads();
-        uint8_t *const ta = tiles[s & 1], *const tb = ta + kA;
+        wait_vmem_but<(D - 2) * (LT + 1)>();
+        phase_end();
+        uint8_t *const ta = tiles[at], *const tb = ta + kA;
+        const float *const sc = inv[s & 1];
+        at = at + 1 == D ? 0 : at + 1;
         const int krem = kend - s * kBK;
         if (krem < kBK) {                               // the last step of a k that is no multiple of 128
 #pragma unroll
@@ -554,18 +579,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                     if (16 * ch + 16 > krem) *at = keep_bytes(*at, krem - 16 * ch);
                 }
             }
-            __syncthreads();
+            phase_end();
         }
-        advance(s + 1 < steps);
-        load_scales(s + 2 < steps);
-        const int stage = (s + 1) & 1;
-
+        float next;                                      // scale of the next step, inverted after the products
         if constexpr (EXACT) {
             // lane (r32, h): row r32 of a fragment; slice u of 16 k holds, for half h, the 8 codes at
-            // k = 16 (2 (u / 2) + h) + 8 (u % 2)
+            // k = 16 (2 (u / 2) + h) + 8 (u % 2). a comes first, so that a lane ends with one column.
             const int r32 = lane & 31, h = lane >> 5;
+            // With power-of-two scales a lane's row of each operand carries its own factor.
+            float ea[FM], eb[FN];
 #pragma unroll
-            for (int u = 0; u < LT; ++u) load_piece(stage, u);
+            for (int i = 0; i < FM; ++i) ea[i] = POW2 ? sc[wm * TM + 32 * i + r32] : 1.0f;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) eb[j] = POW2 ? sc[BA + (KIND == kGroups ? wn * TN + 32 * j + r32 : wn * TN / 128)] : 1.0f;
             v8bf16 fb[FN][8];
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
@@ -575,52 +601,60 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                         const int kr = 16 * (2 * (u >> 1) + h) + 8 * (u & 1) + (r16 >> 1);
                         const int ch = (wn * TN + 32 * j) / 16 + ((lane >> 4) & 1);
                         const v2i32 q = read_transposed(tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1));
-                        fb[j][u] = codes_to_bf16<FB>((uint32_t)q.x, (uint32_t)q.y);
+                        fb[j][u] = codes_to_bf16<FB>((uint32_t)q.x, (uint32_t)q.y, eb[j]);
                     }
                 } else {
                     const int row = wn * TN + 32 * j + r32;
 #pragma unroll
                     for (int u = 0; u < 8; u += 2) {
                         const uint4 q = *(const uint4 *)(tb + row * kBK + (((u + h) ^ swizzle(row)) << 4));
-                        fb[j][u] = codes_to_bf16<FB>(q.x, q.y);
-                        fb[j][u + 1] = codes_to_bf16<FB>(q.z, q.w);
+                        fb[j][u] = codes_to_bf16<FB>(q.x, q.y, eb[j]);
+                        fb[j][u + 1] = codes_to_bf16<FB>(q.z, q.w, eb[j]);
                     }
                 }
             }
+            next = raw[at][t];
+#pragma unroll
+            for (int u = 0; u <= LT; ++u) load_piece(u);
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 const int row = wm * TM + 32 * i + r32;
                 v16f32 part[FN];
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) part[j][e] = 0.0f;
+                for (int j = 0; j < FN; ++j) part[j] = POW2 ? (v16f32)acc[i][j] : (v16f32)0.0f;
 #pragma unroll
                 for (int u = 0; u < 8; u += 2) {
                     const uint4 q = *(const uint4 *)(ta + row * kBK + (((u + h) ^ swizzle(row)) << 4));
-                    const v8bf16 f0 = codes_to_bf16<FA>(q.x, q.y), f1 = codes_to_bf16<FA>(q.z, q.w);
+                    const v8bf16 f0 = codes_to_bf16<FA>(q.x, q.y, ea[i]), f1 = codes_to_bf16<FA>(q.z, q.w, ea[i]);
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) part[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j][u], f0, part[j], 0, 0, 0);
+                    for (int j = 0; j < FN; ++j) part[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f0, fb[j][u], part[j], 0, 0, 0);
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) part[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j][u + 1], f1, part[j], 0, 0, 0);
+                    for (int j = 0; j < FN; ++j) part[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1, fb[j][u + 1], part[j], 0, 0, 0);
                 }
-                const float sa = sc[row];
+                if constexpr (POW2) {
 #pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    if constexpr (KIND == kGroups) {
+                    for (int j = 0; j < FN; ++j) acc[i][j] = part[j];
+                } else {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const v4f32 sb = *(const v4f32 *)(sc + BM + wn * TN + 32 * j + 8 * q + 4 * h);
+                    for (int q = 0; q < 4; ++q) {
+                        v4f32 sa = *(const v4f32 *)(sc + wm * TM + 32 * i + 8 * q + 4 * h);
+                        if constexpr (KIND != kGroups) sa *= sc[BA + wn * TN / 128];
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) {
+                            v4f32 f = sa;
+                            if constexpr (KIND == kGroups) f *= sc[BA + wn * TN + 32 * j + r32];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                acc[i][j][4 * q + e] = __builtin_fmaf(part[j][4 * q + e] * sa, sb[e], acc[i][j][4 * q + e]);
+                                acc[i][j][4 * q + e] = __builtin_fmaf(part[j][4 * q + e], f[e], acc[i][j][4 * q + e]);
                         }
-                    } else {
-                        const float f = sa * sc[BM + wn * TN / 128];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(part[j][e], f, acc[i][j][e]);
                     }
                 }
+            }
+            // conversions and scaling run in the shadow of the products: 8 vector instructions a product
+#pragma unroll
+            for (int m = 0; m < FM * FN * 8; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, POW2 ? 5 : 9, 0);
             }
         } else {
             // lane (r16, g) holds row r16 of a fragment and k = 16 g + [0, 16) and 64 + 16 g + [0, 16).
@@ -659,11 +693,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
             if constexpr (KIND == kGroups) {
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
-                    if constexpr (POW2) ebg[j] = __float_as_int(sc[BM + wn * TN + 16 * j + r16]);
-                    else sbg[j] = *(const v4f32 *)(sc + BM + wn * TN + 16 * j + 4 * g);
+                    if constexpr (POW2) ebg[j] = __float_as_int(sc[BA + wn * TN + 16 * j + r16]);
+                    else sbg[j] = *(const v4f32 *)(sc + BA + wn * TN + 16 * j + 4 * g);
                 }
             } else {
-                const float sbu = sc[BM + wn * TN / 128];
+                const float sbu = sc[BA + wn * TN / 128];
                 if constexpr (POW2) {
 #pragma unroll
                     for (int j = 0; j < FN; ++j) ebg[j] = __float_as_int(sbu);
@@ -672,6 +706,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                     for (int i = 0; i < FM; ++i) sa[i] *= sbu;
                 }
             }
+            next = raw[at][t];
             v4f32 part[2][FN];
             auto scale = [&](int i) {                   // acc += part * (1/Sa 1/Sb)
 #pragma unroll
@@ -682,13 +717,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                         else acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], sa[i], acc[i][j][e]);
                     }
             };
-            constexpr int PI = (LT + FM - 1) / FM;      // load pieces issued per fragment
+            constexpr int PI = (LT + FM) / FM;          // load pieces issued per fragment
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 v8i32 next;
                 if (i + 1 < FM) next = frag_a(i + 1);
 #pragma unroll
-                for (int u = i * PI; u < (i + 1) * PI && u < LT; ++u) load_piece(stage, u);
+                for (int u = i * PI; u < (i + 1) * PI && u <= LT; ++u) load_piece(u);
                 if constexpr (POW2) {
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
@@ -703,6 +738,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
             }
             if constexpr (!POW2) scale(FM - 1);
         }
+        asm volatile("" : "+v"(next));
+        inv[(s + 1) & 1][t] = inverse_scale<MATH>(next);
     }
     wait_vmem();                                        // no load may still write LDS when the workgroup ends
 
@@ -727,7 +764,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 // per thread.
 template <int FA, int FB, int KIND, int MATH>
 __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
-    static_assert(KIND != kGroups && MATH != kMathExact, "one scale of b for each wave and step");
+    static_assert(KIND != kGroups && MATH < kMathExact, "one scale of b for each wave and step");
     constexpr int BM = 256, BN = 256, WN = 4, NT = 512, TM = 128, TN = 64, FM = 8, FN = 4;
     constexpr bool POW2 = MATH == kMathE8m0;
     constexpr int kA = BM * kBK, kB = BN * kBK, kStage = kA + kB;
@@ -752,33 +789,8 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
     if (steps > 0) {
         TileLoads<KIND, false, BM, BN, TN, NT> ld;
         ld.init(p, pl, steps, t);
-        // thread u < 256 loads the scale of a's row u, u >= 256 that of b's block u % 2; waves 0-3 and
-        // 4-7 each use one buffer.
-        MovingBuffer bs;
-        uint32_t vs, step_s = 4;
-        {
-            const int gn = (p.n + 127) / 128, e = pl.expert > 0 ? pl.expert : 0;
-            if (wave < 4) {
-                const int64_t first = p.rows ? 0 : pl.row0;
-                bs.base = uniform64((uint64_t)(uintptr_t)(p.sa + first * gk + g0));
-                const int64_t left = ((p.rows ? p.a_rows : p.m) - first) * gk - g0;
-                bs.left = left > 0x3FFFFFFF ? 0xFFFFFFFCu : (uint32_t)left * 4u;
-                vs = (uint32_t)((source_row(p, pl, t) - first) * gk * 4);
-            } else {
-                int nb = (t & 1) < gn - pl.n0 / 128 ? t & 1 : 0;
-                if constexpr (KIND == kNK) {
-                    bs.base = uniform64((uint64_t)(uintptr_t)(p.sb + ((int64_t)e * gn + pl.n0 / 128) * gk + g0));
-                    bs.left = cap31(((int64_t)(gn - pl.n0 / 128) * gk - g0) * 4);
-                    vs = (uint32_t)(nb * gk * 4);
-                } else {
-                    bs.base = uniform64((uint64_t)(uintptr_t)(p.sb + ((int64_t)e * gk + g0) * gn + pl.n0 / 128));
-                    bs.left = cap31(((int64_t)(gk - g0) * gn - pl.n0 / 128) * 4);
-                    vs = (uint32_t)(nb * 4);
-                    step_s = (uint32_t)gn * 4u;
-                }
-            }
-            bs.left = __builtin_amdgcn_readfirstlane((int)bs.left);
-        }
+        ScaleLoads<KIND, false, BM, BN, NT> ls;
+        ls.init(p, pl, t, wave, gk, g0);
         const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)lds_address(&tiles[0][0])) + (uint32_t)wave * 1024u;
         const uint32_t lds_raw = __builtin_amdgcn_readfirstlane((int)lds_address(&raw[0][0])) + (uint32_t)wave * 256u;
 
@@ -807,9 +819,9 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
             }
         };
         auto load_scale = [&]() {
-            if (n_scale >= steps) bs.left = 0;
-            lds_dma4(bs.rsrc(), vs, lds_raw + (uint32_t)(n_scale & 1) * (BM + BN) * 4u);
-            bs.advance(step_s);
+            if (n_scale >= steps) ls.buf.left = 0;
+            lds_dma4(ls.buf.rsrc(), ls.off, lds_raw + (uint32_t)(n_scale & 1) * (BM + BN) * 4u);
+            ls.buf.advance(ls.step);
             ++n_scale;
         };
 
@@ -823,7 +835,7 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
         for (int u = 0; u < 6; ++u) load_first(u);
         wait_vmem_but<6>();
         phase_end();
-        inv[0][t] = inverse_scale<POW2>(raw[0][t]);
+        inv[0][t] = inverse_scale<MATH>(raw[0][t]);
         phase_end();
         load_scale();                                   // into the place of the scales just read
         if (wave >= 4) phase_end();                     // one phase behind
@@ -885,7 +897,7 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
                 if (half == 0) {
                     if (m == 4 || m == 8) load_second(m / 4 - 1);
                     if (m == 5) asm volatile("" : "+v"(next));
-                    if (m == 11) inv[(s + 1) & 1][t] = inverse_scale<POW2>(next);
+                    if (m == 11) inv[(s + 1) & 1][t] = inverse_scale<MATH>(next);
                 } else {
                     if (m % 2 == 0 && m / 2 < 6) load_first(m / 2);
                     if (m == 12) load_scale();
@@ -953,22 +965,27 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
 
 // ---- launch ----------------------------------------------------------------------------------------
 
-struct TileSize { int bm, bn; };
-constexpr TileSize kTileSizes[2][3] = {{{256, 256}, {128, 128}, {64, 128}},      // FP8 MFMAs
-                                       {{256, 128}, {128, 128}, {64, 128}}};     // BF16 MFMAs
+// Tile sizes. fit: workgroups that share a CU.
+struct TileSize { int bm, bn, fit; };
+constexpr int kTileCount = 4;
+constexpr TileSize kTileSizes[kTileCount] = {{256, 256, 1}, {128, 128, 2}, {64, 128, 2}, {32, 128, 2}};
 
 template <int FA, int FB, int KIND, int MATH>
 int launch_matmul_tile(const MatmulArgs &p, int size, int64_t groups, hipStream_t s) {
     const dim3 grid((unsigned)groups);
-    if (size == 0) {
-        if constexpr (MATH == kMathExact) hipLaunchKernelGGL((matmul_tile_kernel<FA, FB, KIND, MATH, 256, 128, 4, 2>), grid, dim3(512), 0, s, p);
-        else if constexpr (KIND == kGroups) hipLaunchKernelGGL((matmul_tile_kernel<FA, FB, KIND, MATH, 256, 256, 2, 4>), grid, dim3(512), 0, s, p);
-        else hipLaunchKernelGGL((matmul_large_kernel<FA, FB, KIND, MATH>), grid, dim3(512), 0, s, p);
-    } else if (size == 1) {
-        hipLaunchKernelGGL((matmul_tile_kernel<FA, FB, KIND, MATH, 128, 128, 2, 2>), grid, dim3(256), 0, s, p);
-    } else {
-        hipLaunchKernelGGL((matmul_tile_kernel<FA, FB, KIND, MATH, 64, 128, 1, 4>), grid, dim3(256), 0, s, p);
+#define QF8_TILE(BM, BN, WM, WN, D) \
+    hipLaunchKernelGGL((matmul_tile_kernel<FA, FB, KIND, MATH, BM, BN, WM, WN, D>), grid, dim3(64 * WM * WN), 0, s, p)
+    switch (size) {
+        case 0:
+            if constexpr (MATH >= kMathExact) return QF8_ERR_HIP;        // never planned
+            else if constexpr (KIND == kGroups) QF8_TILE(256, 256, 2, 4, 2);
+            else hipLaunchKernelGGL((matmul_large_kernel<FA, FB, KIND, MATH>), grid, dim3(512), 0, s, p);
+            break;
+        case 1: QF8_TILE(128, 128, 2, 2, 2); break;
+        case 2: QF8_TILE(64, 128, 1, 4, 3); break;
+        default: QF8_TILE(32, 128, 1, 4, 3); break;
     }
+#undef QF8_TILE
     return hipGetLastError() == hipSuccess ? QF8_OK : QF8_ERR_HIP;
 }
 
@@ -976,7 +993,8 @@ template <int FA, int FB, int KIND>
 int launch_matmul_kind(const MatmulArgs &p, int math, int size, int64_t groups, hipStream_t s) {
     if (math == kMathFp8) return launch_matmul_tile<FA, FB, KIND, kMathFp8>(p, size, groups, s);
     if (math == kMathE8m0) return launch_matmul_tile<FA, FB, KIND, kMathE8m0>(p, size, groups, s);
-    return launch_matmul_tile<FA, FB, KIND, kMathExact>(p, size, groups, s);
+    if (math == kMathExact) return launch_matmul_tile<FA, FB, KIND, kMathExact>(p, size, groups, s);
+    return launch_matmul_tile<FA, FB, KIND, kMathExactPow2>(p, size, groups, s);
 }
 
 template <int FA, int FB>

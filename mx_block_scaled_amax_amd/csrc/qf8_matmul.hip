@@ -19,19 +19,20 @@ struct Plan { int size, splits; int64_t split_k; };
 // Tile size and split of k from a model of the time: workgroups run in rounds of CUs x (workgroups
 // that fit on one), a round costs its steps of k.
 Plan plan_matmul(int64_t m, int64_t n, int64_t k, int parts, bool may_split, bool exact) {
-    constexpr int kFit[] = {1, 2, 3};                                                  // workgroups per CU (LDS)
-    constexpr double kStep[2][3] = {{4300.0, 2900.0, 2550.0}, {5100.0, 4600.0, 4400.0}};   // cycles of one step of a full CU
-    const TileSize *sizes = kTileSizes[exact];
+    // cycles of one step of k of a full CU: FP8, BF16 products
+    constexpr double kStep[2][kTileCount] = {{4300.0, 2900.0, 2250.0, 1900.0},
+                                             {1e9, 4600.0, 3900.0, 3400.0}};
+    const TileSize *sizes = kTileSizes;
     const int64_t steps = (k + kBK - 1) / kBK;
     Plan best = {2, 1, steps * kBK};
     double best_t = 1e300;
-    for (int size = 0; size < 3; ++size) {
+    for (int size = 0; size < kTileCount; ++size) {
         const int64_t tiles = ((m + sizes[size].bm - 1) / sizes[size].bm) *
                               ((n + sizes[size].bn - 1) / sizes[size].bn) * parts;
         for (int splits = 1; splits <= (may_split ? 16 : 1); splits *= 2) {
             const int64_t per = (steps + splits - 1) / splits;
             if (splits > 1 && (per < 4 || (int64_t)splits * m * n * 4 > (int64_t)256 << 20)) break;
-            const int64_t slots = (int64_t)kCUs * kFit[size];
+            const int64_t slots = (int64_t)kCUs * sizes[size].fit;
             const int64_t rounds = (tiles * splits + slots - 1) / slots;
             double t = (double)rounds * (double)(per + 3) * kStep[exact][size];
             if (splits > 1) t += 6000.0 + (double)splits * (double)m * (double)n * 8.0 / 2000.0;
@@ -91,10 +92,9 @@ int launch_matmul(const MatmulArgs &args, int fmt_a, int fmt_b, int kind, int po
     if (p.m == 0 || p.n == 0) return QF8_OK;
     p.splits = 1;
     p.split_k = p.k;
-    p.vec = p.n % 8 == 0;
     const bool exact = !args.out_bf16;
-    const int math = exact ? kMathExact : pow2 ? kMathE8m0 : kMathFp8;
-    const TileSize *sizes = kTileSizes[exact];
+    const int math = exact ? (pow2 ? kMathExactPow2 : kMathExact) : pow2 ? kMathE8m0 : kMathFp8;
+    const TileSize *sizes = kTileSizes;
     if (p.mode == kMatmulDense) {
         const Plan pl = plan_matmul(p.m, p.n, p.k, 1, true, exact);
         const int64_t tiles = ((p.m + sizes[pl.size].bm - 1) / sizes[pl.size].bm) *
