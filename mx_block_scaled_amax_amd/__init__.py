@@ -493,16 +493,47 @@ def dequantize_mx(q, s, fmt, out_dtype=torch.bfloat16, out=None, x=None, want_ou
 
 
 # ---- matrix products under group scales --------------------------------------------------------
+#
+# The calls below are made once per layer and token batch, so their checks are kept short: pointers go to
+# the library as plain integers and the current stream is read as one.
 
-def _input(t, name, dtype, shape):
-    """A contiguous device tensor of this type and shape (None in the shape: any size)."""
-    _dev_tensor(t, name)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _need(t, name, dtype, shape=None):
+    """A contiguous device tensor of this type; shape: a tuple, or a number of dimensions."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor; the library has no CPU path")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have the shape {tuple('*' if w is None else w for w in shape)}, "
-                         f"got {tuple(t.shape)}")
+    if type(shape) is int:
+        if t.dim() != shape:
+            raise ValueError(f"{name} must have {shape} dimensions, got shape {tuple(t.shape)}")
+    elif t.shape != shape:
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape
+
+
+def _place(t, shape, dtype, like, name):
+    """The given output, checked, or a new one beside `like`."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(t, name, dtype, shape)
     return t
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _out_code(out_dtype):
@@ -511,6 +542,15 @@ def _out_code(out_dtype):
     if out_dtype == torch.float32:
         return _FP32
     raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+
+
+def _in_code(t, name):
+    if isinstance(t, torch.Tensor):
+        if t.dtype == torch.bfloat16:
+            return _BF16
+        if t.dtype == torch.float32:
+            return _FP32
+    raise TypeError(f"{name} must be a torch.bfloat16 or torch.float32 tensor")
 
 
 def _scale_shape(kind, n, k):
@@ -525,25 +565,25 @@ def matmul_block(a, sa, b, sb, fmt_a, fmt_b, kind=WEIGHT_NK, pow2_scales=False, 
                  ws=None, stream=None):
     """y [m][n] = values(a) times values(b), where values are decode(codes) / scale. a: uint8 codes
     [m][k] with 1x128 group scales sa; b and sb by kind: WEIGHT_NK [n][k] and WEIGHT_KN [k][n] in
-    128x128 blocks, GROUPS_NK [n][k] in 1x128 groups. pow2_scales: every scale is a power of two. A float32 result has fp32 sums; a
-    bfloat16 one those of the FP8 matrix instructions, which keep 14 bits of each 8 products."""
-    m, k = _input(a, "a", torch.uint8, (None, None)).shape
-    if kind == WEIGHT_KN:
-        n = _input(b, "b", torch.uint8, (k, None)).shape[1]
-    else:
-        n = _input(b, "b", torch.uint8, (None, k)).shape[0]
-    _input(sa, "sa", torch.float32, (m, -(-k // 128)))
-    _input(sb, "sb", torch.float32, _scale_shape(kind, n, k))
+    128x128 blocks, GROUPS_NK [n][k] in 1x128 groups. pow2_scales: every scale is a power of two. A
+    float32 result has fp32 sums; a bfloat16 one those of the FP8 matrix instructions, which keep 14
+    bits of each 8 products."""
+    m, k = _need(a, "a", torch.uint8, 2)
+    bs = _need(b, "b", torch.uint8, 2)
+    n, kb = (bs[1], bs[0]) if kind == WEIGHT_KN else bs
+    if kb != k:
+        raise ValueError(f"b must have {k} values along the sum, got {kb}")
+    _need(sa, "sa", torch.float32, (m, -(-k // 128)))
+    _need(sb, "sb", torch.float32, _scale_shape(kind, n, k))
     code = _out_code(out_dtype)
-    dev = a.device
-    out = _out(out, (m, n), out_dtype, dev, "out")
+    out = _place(out, (m, n), out_dtype, a, "out")
     lib = _load()
-    need = lib.matmul_block_workspace_bytes(m, n, k, kind, code)
-    if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(lib.matmul_block(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), m, n, k, fmt_a, fmt_b, kind,
-                            FLAG_POW2_SCALES if pow2_scales else 0, _ptr(out), code, _ptr(ws),
-                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream, dev)), "matmul_block")
+    if ws is None:
+        need = lib.matmul_block_workspace_bytes(m, n, k, kind, code)
+        ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
+    _check(lib.matmul_block(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), m, n, k, fmt_a, fmt_b, kind,
+                            FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code, _address(ws),
+                            0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, a)), "matmul_block")
     return out
 
 
@@ -552,20 +592,22 @@ def matmul_block_experts(a, sa, b, sb, offsets, fmt_a, fmt_b, kind=WEIGHT_NK, ro
     """One weight per expert: b [experts][n][k] (WEIGHT_NK) or [experts][k][n] (WEIGHT_KN). Rows
     offsets[e] .. offsets[e+1] of the result are those of expert e; row i reads row rows[i] of a (a
     negative entry: zeros), or row i without rows. Rows of no expert are zeros."""
-    tokens, k = _input(a, "a", torch.uint8, (None, None)).shape
+    tokens, k = _need(a, "a", torch.uint8, 2)
+    experts, n, kb = _need(b, "b", torch.uint8, 3)
     if kind == WEIGHT_KN:
-        experts, _, n = _input(b, "b", torch.uint8, (None, k, None)).shape
-    else:
-        experts, n, _ = _input(b, "b", torch.uint8, (None, None, k)).shape
-    _input(sa, "sa", torch.float32, (tokens, -(-k // 128)))
-    _input(sb, "sb", torch.float32, (experts,) + _scale_shape(kind, n, k))
-    _input(offsets, "offsets", torch.int32, (experts + 1,))
-    nrows = tokens if rows is None else _input(rows, "rows", torch.int32, (None,)).shape[0]
+        n, kb = kb, n
+    if kb != k:
+        raise ValueError(f"b must have {k} values along the sum, got {kb}")
+    _need(sa, "sa", torch.float32, (tokens, -(-k // 128)))
+    _need(sb, "sb", torch.float32, (experts,) + _scale_shape(kind, n, k))
+    _need(offsets, "offsets", torch.int32, (experts + 1,))
+    nrows = tokens if rows is None else _need(rows, "rows", torch.int32, 1)[0]
     code = _out_code(out_dtype)
-    out = _out(out, (nrows, n), out_dtype, a.device, "out")
-    _check(_load().matmul_block_experts(_ptr(a), _ptr(sa), tokens, _ptr(b), _ptr(sb), _ptr(offsets), experts, _ptr(rows),
-                                        nrows, n, k, fmt_a, fmt_b, kind, FLAG_POW2_SCALES if pow2_scales else 0,
-                                        _ptr(out), code, _stream(stream, a.device)), "matmul_block_experts")
+    out = _place(out, (nrows, n), out_dtype, a, "out")
+    _check(_load().matmul_block_experts(a.data_ptr(), sa.data_ptr(), tokens, b.data_ptr(), sb.data_ptr(),
+                                        offsets.data_ptr(), experts, _address(rows), nrows, n, k, fmt_a, fmt_b, kind,
+                                        FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code,
+                                        _stream_of(stream, a)), "matmul_block_experts")
     return out
 
 
@@ -574,16 +616,19 @@ def matmul_block_experts_wgrad(at, sat, bt, sbt, offsets, fmt_a, fmt_b, pow2_sca
     """Weight gradients [experts][m][n]: values(at)[:, rows of e] times values(bt)[:, rows of e]
     transposed, for codes at [m][nrows] and bt [n][nrows] in 1x128 groups along the rows; offsets
     are multiples of 128."""
-    m, nrows = _input(at, "at", torch.uint8, (None, None)).shape
-    n = _input(bt, "bt", torch.uint8, (None, nrows)).shape[0]
-    _input(sat, "sat", torch.float32, (m, -(-nrows // 128)))
-    _input(sbt, "sbt", torch.float32, (n, -(-nrows // 128)))
-    experts = _input(offsets, "offsets", torch.int32, (None,)).shape[0] - 1
+    m, nrows = _need(at, "at", torch.uint8, 2)
+    n, nb = _need(bt, "bt", torch.uint8, 2)
+    if nb != nrows:
+        raise ValueError(f"bt must have {nrows} columns, got {nb}")
+    _need(sat, "sat", torch.float32, (m, -(-nrows // 128)))
+    _need(sbt, "sbt", torch.float32, (n, -(-nrows // 128)))
+    experts = _need(offsets, "offsets", torch.int32, 1)[0] - 1
     code = _out_code(out_dtype)
-    out = _out(out, (experts, m, n), out_dtype, at.device, "out")
-    _check(_load().matmul_block_experts_wgrad(_ptr(at), _ptr(sat), _ptr(bt), _ptr(sbt), _ptr(offsets), experts, nrows, m,
-                                              n, fmt_a, fmt_b, FLAG_POW2_SCALES if pow2_scales else 0, _ptr(out), code,
-                                              _stream(stream, at.device)), "matmul_block_experts_wgrad")
+    out = _place(out, (experts, m, n), out_dtype, at, "out")
+    _check(_load().matmul_block_experts_wgrad(at.data_ptr(), sat.data_ptr(), bt.data_ptr(), sbt.data_ptr(),
+                                              offsets.data_ptr(), experts, nrows, m, n, fmt_a, fmt_b,
+                                              FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code,
+                                              _stream_of(stream, at)), "matmul_block_experts_wgrad")
     return out
 
 
@@ -595,29 +640,31 @@ def route_experts(logits, top_k, score=SCORE_SOFTMAX, bias=None, groups=1, top_g
     float32 [experts], added to the scores for the choice only; groups > 1: only the experts of the
     best top_groups groups (by the sum of their two best choices). Returns (ids int32, weights
     float32), both [tokens][top_k], in falling order of the choice."""
-    tokens, experts = _input(logits, "logits", logits.dtype, (None, None)).shape
-    dtype = _dtype_code(logits)
+    dtype = _in_code(logits, "logits")
+    tokens, experts = _need(logits, "logits", logits.dtype, 2)
     if bias is not None:
-        _input(bias, "bias", torch.float32, (experts,))
-    dev = logits.device
-    ids = _out(ids, (tokens, top_k), torch.int32, dev, "ids")
-    weights = _out(weights, (tokens, top_k), torch.float32, dev, "weights")
-    _check(_load().route_experts(_ptr(logits), dtype, tokens, experts, top_k, score, _ptr(bias), groups, top_groups,
-                                 int(renorm), scale, _ptr(ids), _ptr(weights), _stream(stream, dev)), "route_experts")
+        _need(bias, "bias", torch.float32, (experts,))
+    ids = _place(ids, (tokens, top_k), torch.int32, logits, "ids")
+    weights = _place(weights, (tokens, top_k), torch.float32, logits, "weights")
+    _check(_load().route_experts(logits.data_ptr(), dtype, tokens, experts, top_k, score, _address(bias), groups,
+                                 top_groups, int(renorm), scale, ids.data_ptr(), weights.data_ptr(),
+                                 _stream_of(stream, logits)), "route_experts")
     return ids, weights
 
 
 def route_experts_backward(logits, ids, dweights, score=SCORE_SOFTMAX, renorm=True, scale=1.0, dlogits=None,
                            stream=None):
     """Gradient of the logits from that of the weights of route_experts (same score, renorm, scale)."""
-    tokens, experts = _input(logits, "logits", logits.dtype, (None, None)).shape
-    dtype = _dtype_code(logits)
-    top_k = _input(ids, "ids", torch.int32, (tokens, None)).shape[1]
-    _input(dweights, "dweights", torch.float32, (tokens, top_k))
-    dlogits = _out(dlogits, (tokens, experts), logits.dtype, logits.device, "dlogits")
-    _check(_load().route_experts_backward(_ptr(logits), dtype, tokens, experts, _ptr(ids), _ptr(dweights), top_k, score,
-                                          int(renorm), scale, _ptr(dlogits), _stream(stream, logits.device)),
-           "route_experts_backward")
+    dtype = _in_code(logits, "logits")
+    tokens, experts = _need(logits, "logits", logits.dtype, 2)
+    t, top_k = _need(ids, "ids", torch.int32, 2)
+    if t != tokens:
+        raise ValueError(f"ids must have {tokens} rows, got {t}")
+    _need(dweights, "dweights", torch.float32, (tokens, top_k))
+    dlogits = _place(dlogits, (tokens, experts), logits.dtype, logits, "dlogits")
+    _check(_load().route_experts_backward(logits.data_ptr(), dtype, tokens, experts, ids.data_ptr(), dweights.data_ptr(),
+                                          top_k, score, int(renorm), scale, dlogits.data_ptr(),
+                                          _stream_of(stream, logits)), "route_experts_backward")
     return dlogits
 
 
@@ -625,47 +672,46 @@ def order_experts(ids, experts, align=1, offsets=None, rows=None, slots=None, ws
     """Rows by expert for the choices ids [tokens][top_k]: offsets [experts + 1], rows (the token of
     each row, -1 for padding; every expert starts at a multiple of align), slots [tokens][top_k] (the
     row of each choice). All int32; nothing is read back to the host."""
-    tokens, top_k = _input(ids, "ids", torch.int32, (None, None)).shape
+    tokens, top_k = _need(ids, "ids", torch.int32, 2)
     lib = _load()
-    dev = ids.device
     nrows = lib.order_experts_rows(tokens, top_k, experts, align) if rows is None else rows.numel()
-    offsets = _out(offsets, (experts + 1,), torch.int32, dev, "offsets")
-    rows = _out(rows, (nrows,), torch.int32, dev, "rows")
-    slots = _out(slots, (tokens, top_k), torch.int32, dev, "slots")
-    need = lib.order_experts_workspace_bytes(tokens, top_k, experts)
-    if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(lib.order_experts(_ptr(ids), tokens, top_k, experts, align, _ptr(offsets), _ptr(rows), nrows, _ptr(slots),
-                             _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream, dev)),
-           "order_experts")
+    offsets = _place(offsets, (experts + 1,), torch.int32, ids, "offsets")
+    rows = _place(rows, (nrows,), torch.int32, ids, "rows")
+    slots = _place(slots, (tokens, top_k), torch.int32, ids, "slots")
+    if ws is None:
+        need = lib.order_experts_workspace_bytes(tokens, top_k, experts)
+        ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+    _check(lib.order_experts(ids.data_ptr(), tokens, top_k, experts, align, offsets.data_ptr(), rows.data_ptr(), nrows,
+                             slots.data_ptr(), _address(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                             _stream_of(stream, ids)), "order_experts")
     return offsets, rows, slots
 
 
 def combine_experts(x, weights, slots, y=None, stream=None):
     """y[t] = sum_j weights[t][j] x[slots[t][j]] for x [rows][dim] (BF16 or FP32); a slot outside the
     rows adds nothing."""
-    nrows, dim = _input(x, "x", x.dtype, (None, None)).shape
-    dtype = _dtype_code(x)
-    tokens, top_k = _input(slots, "slots", torch.int32, (None, None)).shape
-    _input(weights, "weights", torch.float32, (tokens, top_k))
-    y = _out(y, (tokens, dim), x.dtype, x.device, "y")
-    _check(_load().combine_experts(_ptr(x), dtype, nrows, dim, _ptr(weights), _ptr(slots), tokens, top_k, _ptr(y),
-                                   _stream(stream, x.device)), "combine_experts")
+    dtype = _in_code(x, "x")
+    nrows, dim = _need(x, "x", x.dtype, 2)
+    tokens, top_k = _need(slots, "slots", torch.int32, 2)
+    _need(weights, "weights", torch.float32, (tokens, top_k))
+    y = _place(y, (tokens, dim), x.dtype, x, "y")
+    _check(_load().combine_experts(x.data_ptr(), dtype, nrows, dim, weights.data_ptr(), slots.data_ptr(), tokens, top_k,
+                                   y.data_ptr(), _stream_of(stream, x)), "combine_experts")
     return y
 
 
 def combine_experts_backward(dy, x, weights, slots, rows, dx=None, dweights=None, stream=None):
     """Gradients of combine_experts: (dx, dweights). rows and slots are those of one order_experts
     call; rows of dx that hold no token are zeros."""
-    nrows, dim = _input(x, "x", x.dtype, (None, None)).shape
-    dtype = _dtype_code(x)
-    tokens, top_k = _input(slots, "slots", torch.int32, (None, None)).shape
-    _input(weights, "weights", torch.float32, (tokens, top_k))
-    _input(dy, "dy", x.dtype, (tokens, dim))
-    _input(rows, "rows", torch.int32, (nrows,))
-    dx = _out(dx, (nrows, dim), x.dtype, x.device, "dx")
-    dweights = _out(dweights, (tokens, top_k), torch.float32, x.device, "dweights")
-    _check(_load().combine_experts_backward(_ptr(dy), _ptr(x), dtype, nrows, dim, _ptr(weights), _ptr(slots), _ptr(rows),
-                                            tokens, top_k, _ptr(dx), _ptr(dweights), _stream(stream, x.device)),
-           "combine_experts_backward")
+    dtype = _in_code(x, "x")
+    nrows, dim = _need(x, "x", x.dtype, 2)
+    tokens, top_k = _need(slots, "slots", torch.int32, 2)
+    _need(weights, "weights", torch.float32, (tokens, top_k))
+    _need(dy, "dy", x.dtype, (tokens, dim))
+    _need(rows, "rows", torch.int32, (nrows,))
+    dx = _place(dx, (nrows, dim), x.dtype, x, "dx")
+    dweights = _place(dweights, (tokens, top_k), torch.float32, x, "dweights")
+    _check(_load().combine_experts_backward(dy.data_ptr(), x.data_ptr(), dtype, nrows, dim, weights.data_ptr(),
+                                            slots.data_ptr(), rows.data_ptr(), tokens, top_k, dx.data_ptr(),
+                                            dweights.data_ptr(), _stream_of(stream, x)), "combine_experts_backward")
     return dx, dweights

@@ -7,25 +7,58 @@ namespace qf8 {
 namespace {
 
 // ---- wave-wide pieces ---------------------------------------------------------------------------
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+// Reductions by DPP moves, without the LDS round trips of a shuffle. Sums add in a fixed order.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_rows(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+// Maximum over the wave, the same in every lane (a scalar): row_shr 1, 2, 4, 8, then the last lane of a
+// row to the next row and of the lower half to the upper; lane 63 has seen all.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = umax(v, dpp_rows<0x111, 0xF>(v));
+    v = umax(v, dpp_rows<0x112, 0xF>(v));
+    v = umax(v, dpp_rows<0x114, 0xF>(v));
+    v = umax(v, dpp_rows<0x118, 0xF>(v));
+    v = umax(v, dpp_rows<0x142, 0xA>(v));                // row_bcast:15
+    v = umax(v, dpp_rows<0x143, 0xC>(v));                // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_double(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = dpp_mov<CTRL>((uint32_t)b), hi = dpp_mov<CTRL>((uint32_t)(b >> 32));
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ double lane_double(double v, int lane) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+// Sum over the first `lanes` lanes (the others hold 0): within rows of 16, then the rows.
+__device__ __forceinline__ double wave_sum(double v, int lanes = 64) {
+    v += dpp_double<0xB1>(v);
+    v += dpp_double<0x4E>(v);
+    v += dpp_double<0x141>(v);
+    v += dpp_double<0x140>(v);
+    double s = lane_double(v, 0);
+    if (lanes > 16) s += lane_double(v, 16);
+    if (lanes > 32) s += lane_double(v, 32) + lane_double(v, 48);
+    return s;
 }
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
     return v;
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+// Order-preserving integers of floats; 0 is below every value.
+__device__ __forceinline__ uint32_t float_key(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return b >> 31 ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ int wave_min(int v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = min(v, __shfl_xor(v, d));
-    return v;
+__device__ __forceinline__ float wave_max(float v) {
+    const uint32_t k = wave_max_u32(float_key(v));
+    return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k);
 }
 
 // Logits as the choice sees them: NaN reads as -Inf (never chosen before a number), +Inf as the
@@ -44,16 +77,10 @@ __device__ __forceinline__ void store_logit(uint16_t *p, int64_t i, float v) {
 }
 __device__ __forceinline__ void store_logit(float *p, int64_t i, float v) { p[i] = v; }
 
-// Order-preserving integers; 0 is below every value and marks what cannot be chosen.
 __device__ __forceinline__ uint64_t order_key(double v) {
     const uint64_t b = (uint64_t)__double_as_longlong(v);
     return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
-__device__ __forceinline__ uint64_t order_key(float v) {
-    const uint32_t b = __float_as_uint(v);
-    return (uint64_t)(b >> 31 ? ~b : b | 0x80000000u) << 32;
-}
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) { return max_wave(v); }
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
@@ -63,10 +90,25 @@ __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(
 // the logits themselves (scores rise with them, so without bias and groups the order is exact) or
 // the scores plus bias in fp64: fp32 scores would tie or swap experts whose scores differ by less
 // than 2^-24, and the chosen indices have to be those of the definition. What is read is 2-4 bytes
-// an expert; the time is that of the top_k rounds of a wave-wide maximum.
+// an expert; the time is that of the top_k rounds of a wave-wide maximum, so a round's key is as small
+// as it can be: BF16 logits and the index in one 32-bit word (no two alike, so the maximum is the
+// choice), FP32 logits in one with ties looked up afterwards, scores in two.
 constexpr int kRouteWaves = 4;
+enum { kByBf16 = 0, kByFp32 = 1, kByScore = 2 };
 
-template <typename T, int NE, bool SCORES>
+// The lowest expert e = 64 i + lane whose flag is set (flags: NE per lane); some flag is set.
+template <int NE>
+__device__ __forceinline__ int first_expert(const bool (&flag)[NE]) {
+    int e = 0;
+#pragma unroll
+    for (int i = NE - 1; i >= 0; --i) {
+        const uint64_t m = __ballot(flag[i]);
+        e = m ? 64 * i + __ffsll((unsigned long long)m) - 1 : e;
+    }
+    return __builtin_amdgcn_readfirstlane(e);
+}
+
+template <typename T, int NE, int BY>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t route_lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -89,8 +131,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
         if (top == -INFINITY) top = 0.0f;              // nothing left by the mask: every score is 0
     }
 
-    uint64_t key[NE];
-    if constexpr (SCORES) {
+    uint32_t key[NE], low[NE];                         // low: the other half of a score's key; 0, 0: not to choose
+    if constexpr (BY == kByScore) {
         double s[NE];
         double part = 0.0;
 #pragma unroll
@@ -149,7 +191,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             const int e = 64 * i + lane;
-            key[i] = e < p.experts && ((open >> (e / size)) & 1ull) ? order_key(s[i] + 0.0) : 0ull;
+            const uint64_t k = e < p.experts && ((open >> (e / size)) & 1ull) ? order_key(s[i] + 0.0) : 0ull;
+            key[i] = (uint32_t)(k >> 32);
+            low[i] = (uint32_t)k;
         }
     } else {
         if (softmax && !p.renorm) {
@@ -159,34 +203,44 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
             total = wave_sum(part);
         }
 #pragma unroll
-        for (int i = 0; i < NE; ++i) key[i] = 64 * i + lane < p.experts ? order_key(l[i]) : 0ull;
+        for (int i = 0; i < NE; ++i) {
+            const int e = 64 * i + lane;
+            key[i] = e >= p.experts ? 0u : BY == kByBf16 ? (float_key(l[i]) & 0xFFFF0000u) | (uint32_t)(0xFFFF - e) : float_key(l[i]);
+        }
     }
 
-    // top_k times: every lane's best (the lowest index among equals), then the wave's
     int mine = 0;                                      // lane j keeps the j-th choice
     for (int j = 0; j < p.top_k; ++j) {
-        uint64_t best = key[0];
-        int at = 0;
+        uint32_t best = key[0];
 #pragma unroll
-        for (int i = 1; i < NE; ++i)
-            if (key[i] > best) { best = key[i]; at = i; }
-        uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
-        const uint32_t mhi = wave_max_u32(hi);
-        uint64_t who = __ballot(hi == mhi);
-        int e = 64 * at + lane;
-        if (__popcll(who) > 1) {
-            const uint32_t mlo = wave_max_u32(hi == mhi ? lo : 0u);
-            who = __ballot(hi == mhi && lo == mlo);
-            if (__popcll(who) > 1) {
-                const int first = wave_min(hi == mhi && lo == mlo ? e : 0x7FFFFFFF);
-                who = __ballot(hi == mhi && lo == mlo && e == first);
+        for (int i = 1; i < NE; ++i) best = umax(best, key[i]);
+        best = wave_max_u32(best);
+        int e;
+        if constexpr (BY == kByBf16) {
+            e = 0xFFFF - (int)(best & 0xFFFFu);
+        } else {
+            bool hit[NE];
+#pragma unroll
+            for (int i = 0; i < NE; ++i) hit[i] = key[i] == best;
+            if constexpr (BY == kByScore) {
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < NE; ++i) n += __popcll(__ballot(hit[i]));
+                if (n > 1) {                           // the same upper half: by the lower one
+                    uint32_t second = 0;
+#pragma unroll
+                    for (int i = 0; i < NE; ++i) second = hit[i] ? umax(second, low[i]) : second;
+                    second = wave_max_u32(second);
+#pragma unroll
+                    for (int i = 0; i < NE; ++i) hit[i] = hit[i] && low[i] == second;
+                }
             }
+            e = first_expert(hit);
         }
-        e = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)who) - 1);
         if (lane == j) mine = e;
 #pragma unroll
         for (int i = 0; i < NE; ++i)
-            if (64 * i + lane == e) key[i] = 0ull;
+            if (64 * i + lane == e) key[i] = low[i] = 0u;
     }
 
     // weights of the chosen, in fp64, rounded once
@@ -201,7 +255,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
         }
     }
     if (p.renorm) {
-        const double sum = wave_sum(w);
+        const double sum = wave_sum(w, p.top_k);
         w = sum > 0.0 ? w / sum : 0.0;                 // scores that are all 0: weights 0
     }
     if (lane < p.top_k) {
@@ -253,13 +307,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteA
     if (all) s = total > 0.0 ? s / total : 0.0;
     double d, rest = 0.0;                              // gradients of the chosen logits; rest: -p_e rest for the others
     if (p.renorm) {
-        const double sum = wave_sum(s);
+        const double sum = wave_sum(s, p.top_k);
         const double w = sum > 0.0 ? s / sum : 0.0;
-        const double mean = wave_sum(g * w);
+        const double mean = wave_sum(g * w, p.top_k);
         if (softmax) d = w * (g - mean);
         else d = sum > 0.0 ? (g - mean) / sum * (s / (1.0 + exp(x))) : 0.0;
     } else if (softmax) {
-        rest = wave_sum(g * s);
+        rest = wave_sum(g * s, p.top_k);
         d = s * (g - rest);
     } else {
         d = g * (s / (1.0 + exp(x)));
@@ -270,7 +324,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteA
         v[i] = all && total > 0.0 ? (float)(-(exp((double)l[i] - top) / total) * rest) : 0.0f;
     for (int j = 0; j < p.top_k; ++j) {
         const int e = __builtin_amdgcn_readlane(have ? id : -1, j);
-        const float dj = __shfl((float)d, j);
+        const float dj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint((float)d), j));
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             if (64 * i + lane == e) v[i] = dj;
@@ -290,14 +344,18 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteA
 // choice among equal ones of its wave is a population count of the lanes that ballots of the
 // expert's bits leave; nothing depends on the order of atomics (they only count).
 constexpr int kOrderThreads = 1024, kOrderWaves = kOrderThreads / 64;
-constexpr int kOrderChunk = 2048;                      // choices per workgroup of the two-kernel form
-constexpr int kOrderOne = 4096;                        // up to here one workgroup does all
+constexpr int kOrderOne = 4096;                        // choices up to which one workgroup does all
+constexpr int kOrderGroups = 256;                      // workgroups at most: each reads the counts of all
+inline int64_t order_chunk(int64_t n) {                // choices of a workgroup
+    const int64_t c = (n + kOrderGroups - 1) / kOrderGroups;
+    return (c + kOrderThreads - 1) / kOrderThreads * kOrderThreads;
+}
 
 __global__ __launch_bounds__(kOrderThreads) void order_count_kernel(OrderArgs p) {
     __shared__ int count[kMaxExperts];
     for (int e = threadIdx.x; e < p.experts; e += kOrderThreads) count[e] = 0;
     __syncthreads();
-    const int64_t lo = (int64_t)blockIdx.x * kOrderChunk, hi = lo + kOrderChunk < p.n ? lo + kOrderChunk : p.n;
+    const int64_t lo = (int64_t)blockIdx.x * p.chunk, hi = lo + p.chunk < p.n ? lo + p.chunk : p.n;
     for (int64_t i = lo + threadIdx.x; i < hi; i += kOrderThreads) {
         const int e = p.ids[i];
         if (e >= 0 && e < p.experts) atomicAdd(&count[e], 1);
@@ -313,35 +371,43 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs p)
     __shared__ int scan[kOrderWaves];
     __shared__ int16_t rank[kOrderWaves * kMaxExperts];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int64_t chunk = ONE ? p.n : kOrderChunk;
-    const int64_t lo = (int64_t)blockIdx.x * chunk, hi = lo + chunk < p.n ? lo + chunk : p.n;
+    const int64_t lo = ONE ? 0 : (int64_t)blockIdx.x * p.chunk;
+    const int64_t hi = ONE ? p.n : lo + p.chunk < p.n ? lo + p.chunk : p.n;
 
+    int first_id = -1;                                 // asked for early: used after the counts
+    if (lo + t < hi) first_id = p.ids[lo + t];
     // counts of all choices, and of those before this workgroup's
     int before = 0, mine = 0;                          // thread e: expert e
+    if (t < p.experts) count[t] = next[t] = 0;
+    __syncthreads();
     if constexpr (ONE) {
-        if (t < p.experts) count[t] = 0;
-        __syncthreads();
         for (int64_t i = t; i < p.n; i += kOrderThreads) {
             const int e = p.ids[i];
             if (e >= 0 && e < p.experts) atomicAdd(&count[e], 1);
         }
-        __syncthreads();
-        if (t < p.experts) mine = count[t];
     } else {
-        if (t < p.experts) {
-            const int nb = gridDim.x, me = blockIdx.x;
-            for (int b = 0; b < nb; b += 8) {
+        // 1024 / experts threads share an expert, 8 loads of each in flight
+        const int nb = gridDim.x, me = blockIdx.x, parts = kOrderThreads / p.experts;
+        const int part = t / p.experts, e = t - part * p.experts;
+        if (part < parts) {
+            for (int b = part; b < nb; b += 8 * parts) {
                 int v[8];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] = b + u < nb ? p.counts[(int64_t)(b + u) * p.experts + t] : 0;
+                for (int u = 0; u < 8; ++u) v[u] = b + u * parts < nb ? p.counts[(int64_t)(b + u * parts) * p.experts + e] : 0;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    before += b + u < me ? v[u] : 0;
+                    before += b + u * parts < me ? v[u] : 0;
                     mine += v[u];
                 }
             }
-            count[t] = mine;
+            atomicAdd(&count[e], mine);
+            atomicAdd(&next[e], before);
         }
+    }
+    __syncthreads();
+    if (t < p.experts) {
+        mine = count[t];
+        before = next[t];
     }
     // first row of every expert: exclusive scan of the counts rounded up to align
     const int padded = t < p.experts ? (mine + p.align - 1) / p.align * p.align : 0;
@@ -377,7 +443,7 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs p)
         for (int i = t; i < kOrderWaves * p.experts; i += kOrderThreads) rank[i] = 0;
         __syncthreads();
         const int64_t i = c + t;
-        const int e = i < hi ? p.ids[i] : -1;
+        const int e = c == lo ? first_id : i < hi ? p.ids[i] : -1;
         const bool ok = e >= 0 && e < p.experts;
         uint64_t same = __ballot(ok);
         for (int b = 0; b < bits; ++b) {
@@ -421,7 +487,7 @@ template <> struct Piece<uint16_t> {
     static constexpr int N = 8;
     static __device__ __forceinline__ void load(const uint16_t *p, bool vec, int left, float *v) {
         if (vec) {
-            const uint4 w = *(const uint4 *)p;
+            const uint4 w = ld_stream((const uint4 *)p);
             v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
             v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
         } else {
@@ -435,7 +501,7 @@ template <> struct Piece<uint16_t> {
     }
     static __device__ __forceinline__ void store(uint16_t *p, bool vec, int left, const float *v) {
         if (vec) {
-            *(uint4 *)p = make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7]));
+            st_stream((uint4 *)p, make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7])));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -447,8 +513,8 @@ template <> struct Piece<float> {
     static constexpr int N = 4;
     static __device__ __forceinline__ void load(const float *p, bool vec, int left, float *v) {
         if (vec) {
-            const float4 w = *(const float4 *)p;
-            v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+            const uint4 w = ld_stream((const uint4 *)p);
+            v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y); v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0.0f;
@@ -456,7 +522,7 @@ template <> struct Piece<float> {
     }
     static __device__ __forceinline__ void store(float *p, bool vec, int left, const float *v) {
         if (vec) {
-            *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]);
+            st_stream((uint4 *)p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -586,9 +652,9 @@ int launch_route_ne(const RouteArgs &p, bool backward, hipStream_t s) {
         hipLaunchKernelGGL((route_backward_kernel<T, NE>), grid, block, 0, s, p);
     } else if (p.bias || p.groups > 1) {
         const size_t lds = p.groups > 1 ? (size_t)waves * p.experts * sizeof(double) : 0;
-        hipLaunchKernelGGL((route_kernel<T, NE, true>), grid, block, lds, s, p);
+        hipLaunchKernelGGL((route_kernel<T, NE, kByScore>), grid, block, lds, s, p);
     } else {
-        hipLaunchKernelGGL((route_kernel<T, NE, false>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((route_kernel<T, NE, sizeof(T) == 2 ? kByBf16 : kByFp32>), grid, block, 0, s, p);
     }
     return launched();
 }
@@ -610,15 +676,19 @@ int launch_route(const RouteArgs &p, int dtype, int backward, hipStream_t s) {
 }
 
 size_t order_workspace(int64_t n, int experts) {
-    return n <= kOrderOne ? 0 : (size_t)((n + kOrderChunk - 1) / kOrderChunk) * experts * sizeof(int32_t);
+    if (n <= kOrderOne) return 0;
+    const int64_t chunk = order_chunk(n);
+    return (size_t)((n + chunk - 1) / chunk) * experts * sizeof(int32_t);
 }
 
-int launch_order(const OrderArgs &p, hipStream_t s) {
+int launch_order(const OrderArgs &args, hipStream_t s) {
+    OrderArgs p = args;
+    p.chunk = order_chunk(p.n);
     if (p.n <= kOrderOne) {
         hipLaunchKernelGGL((order_place_kernel<true>), dim3(1), dim3(kOrderThreads), 0, s, p);
         return launched();
     }
-    const dim3 grid((unsigned)((p.n + kOrderChunk - 1) / kOrderChunk));
+    const dim3 grid((unsigned)((p.n + p.chunk - 1) / p.chunk));
     hipLaunchKernelGGL(order_count_kernel, grid, dim3(kOrderThreads), 0, s, p);
     if (launched() != QF8_OK) return QF8_ERR_HIP;
     hipLaunchKernelGGL((order_place_kernel<false>), grid, dim3(kOrderThreads), 0, s, p);

@@ -130,7 +130,7 @@ int launch_route(const RouteArgs &p, int dtype, int backward, hipStream_t s);
 struct OrderArgs {
     const int32_t *ids;
     int32_t *offsets, *rows, *slots, *counts;
-    int64_t n, nrows;            // choices, rows
+    int64_t n, nrows, chunk;     // choices, rows, choices of a workgroup
     int top_k, experts, align;
 };
 size_t order_workspace(int64_t n, int experts);

@@ -16,26 +16,31 @@ constexpr int kCUs = 256;
 
 struct Plan { int size, splits; int64_t split_k; };
 
-// Tile size and split of k from a model of the time: workgroups run in rounds of CUs x (workgroups
-// that fit on one), a round costs its steps of k.
-Plan plan_matmul(int64_t m, int64_t n, int64_t k, int parts, bool may_split, bool exact) {
-    // cycles of one step of k of a full CU: FP8, BF16 products
-    constexpr double kStep[2][kTileCount] = {{4300.0, 2900.0, 2250.0, 1900.0},
-                                             {1e9, 4600.0, 3900.0, 3400.0}};
-    const TileSize *sizes = kTileSizes;
+// Tile size and split of k by a model of the time, in us, fitted to sweeps over m 1-8192, n 512-7168,
+// k 512-16384 (its choice is within 10% of the best of all sizes and splits in most of them, 25% in
+// the worst). A workgroup takes a fixed time and one per step of k, longer where two share a CU;
+// workgroups run in rounds of what the CUs hold; parts of a split k are joined by a second kernel.
+// tiles: number of output tiles of a size, which for experts is an estimate.
+template <typename Tiles>
+Plan plan_matmul(int64_t k, double outputs, bool may_split, bool exact, Tiles tiles) {
+    struct Step { double alone, shared; };                  // us per step of k
+    constexpr Step kStep[2][kTileCount] = {{{1.50, 1.90}, {0.78, 1.30}, {0.47, 0.83}, {0.39, 0.63}},
+                                           {{1e9, 1e9}, {1.40, 2.40}, {1.04, 1.60}, {0.78, 1.09}}};
     const int64_t steps = (k + kBK - 1) / kBK;
     Plan best = {2, 1, steps * kBK};
     double best_t = 1e300;
     for (int size = 0; size < kTileCount; ++size) {
-        const int64_t tiles = ((m + sizes[size].bm - 1) / sizes[size].bm) *
-                              ((n + sizes[size].bn - 1) / sizes[size].bn) * parts;
+        const double count = tiles(kTileSizes[size]);
+        const Step c = kStep[exact][size];
         for (int splits = 1; splits <= (may_split ? 16 : 1); splits *= 2) {
             const int64_t per = (steps + splits - 1) / splits;
-            if (splits > 1 && (per < 4 || (int64_t)splits * m * n * 4 > (int64_t)256 << 20)) break;
-            const int64_t slots = (int64_t)kCUs * sizes[size].fit;
-            const int64_t rounds = (tiles * splits + slots - 1) / slots;
-            double t = (double)rounds * (double)(per + 3) * kStep[exact][size];
-            if (splits > 1) t += 6000.0 + (double)splits * (double)m * (double)n * 8.0 / 2000.0;
+            const double bytes = (double)splits * outputs * 4.0;
+            if (splits > 1 && (per < 2 || bytes > (double)((int64_t)256 << 20))) break;
+            const double groups = count * splits, slots = (double)kCUs * kTileSizes[size].fit;
+            const double full = groups > slots ? (double)(int64_t)((groups - 1.0) / slots) : 0.0;   // rounds before the last
+            const double last = groups - full * slots;
+            double t = 5.0 + (double)(per + 1) * (full * c.shared + (last > (size == 0 ? 0.75 * kCUs : kCUs) ? c.shared : c.alone));
+            if (splits > 1) t += 2.5 + 0.1 * splits + 2.0 * bytes / 4e6;
             if (t < best_t) {
                 best_t = t;
                 best.size = size;
@@ -46,6 +51,12 @@ Plan plan_matmul(int64_t m, int64_t n, int64_t k, int parts, bool may_split, boo
     }
     best.splits = best.splits > 1 ? (int)((steps * kBK + best.split_k - 1) / best.split_k) : 1;
     return best;
+}
+
+Plan plan_dense(int64_t m, int64_t n, int64_t k, bool exact) {
+    return plan_matmul(k, (double)m * (double)n, true, exact, [=](const TileSize &t) {
+        return (double)((m + t.bm - 1) / t.bm) * (double)((n + t.bn - 1) / t.bn);
+    });
 }
 
 // y = sum over the parts in their order, rounded once.
@@ -83,7 +94,7 @@ int launch_by_format(const MatmulArgs &p, int fa, int fb, int kind, int math, in
 size_t matmul_workspace(int64_t m, int64_t n, int64_t k, int kind, int out_bf16) {
     (void)kind;
     if (m == 0 || n == 0 || k == 0) return 0;
-    const Plan pl = plan_matmul(m, n, k, 1, true, !out_bf16);
+    const Plan pl = plan_dense(m, n, k, !out_bf16);
     return pl.splits > 1 ? (size_t)pl.splits * m * n * sizeof(float) : 0;
 }
 
@@ -96,7 +107,7 @@ int launch_matmul(const MatmulArgs &args, int fmt_a, int fmt_b, int kind, int po
     const int math = exact ? (pow2 ? kMathExactPow2 : kMathExact) : pow2 ? kMathE8m0 : kMathFp8;
     const TileSize *sizes = kTileSizes;
     if (p.mode == kMatmulDense) {
-        const Plan pl = plan_matmul(p.m, p.n, p.k, 1, true, exact);
+        const Plan pl = plan_dense(p.m, p.n, p.k, exact);
         const int64_t tiles = ((p.m + sizes[pl.size].bm - 1) / sizes[pl.size].bm) *
                               ((p.n + sizes[pl.size].bn - 1) / sizes[pl.size].bn);
         if (pl.splits == 1) return launch_by_format(p, fmt_a, fmt_b, kind, math, pl.size, tiles, s);
@@ -115,14 +126,20 @@ int launch_matmul(const MatmulArgs &args, int fmt_a, int fmt_b, int kind, int po
         return hipGetLastError() == hipSuccess ? QF8_OK : QF8_ERR_HIP;
     }
     if (p.mode == kMatmulExpertsK) {
-        const int64_t mean = p.k / (p.experts > 0 ? p.experts : 1) + 1;
-        const Plan pl = plan_matmul(p.m, p.n, mean, p.experts, false, exact);
+        const int64_t mean = p.k / p.experts + 1;
+        const Plan pl = plan_matmul(mean, 0.0, false, exact, [&](const TileSize &t) {
+            return (double)((p.m + t.bm - 1) / t.bm) * (double)((p.n + t.bn - 1) / t.bn) * p.experts;
+        });
         const int64_t tiles = ((p.m + sizes[pl.size].bm - 1) / sizes[pl.size].bm) *
                               ((p.n + sizes[pl.size].bn - 1) / sizes[pl.size].bn);
         return launch_by_format(p, fmt_a, fmt_b, kind, math, pl.size, tiles * p.experts, s);
     }
-    const int64_t mean = p.m / (p.experts > 0 ? p.experts : 1) + 1;
-    const Plan pl = plan_matmul(mean, p.n, p.k, p.experts, false, exact);
+    // the rows of an expert end inside a tile: half a tile more for each that has rows
+    const double used = (double)(p.m < p.experts ? p.m : p.experts);
+    const Plan pl = plan_matmul(p.k, 0.0, false, exact, [&](const TileSize &t) {
+        const double rows = (double)p.m / t.bm + 0.5 * used;
+        return (rows > used ? rows : used) * (double)((p.n + t.bn - 1) / t.bn);
+    });
     const int64_t tm = p.m / sizes[pl.size].bm + p.experts + 1, tn = (p.n + sizes[pl.size].bn - 1) / sizes[pl.size].bn;
     return launch_by_format(p, fmt_a, fmt_b, kind, math, pl.size, tm * tn, s);
 }
