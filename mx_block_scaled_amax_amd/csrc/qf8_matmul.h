@@ -24,6 +24,7 @@
 // Orientation: b's rows are the MFMA's first operand, so a lane of the result holds one row i of y
 // and neighbouring j: 1/Sa is one register per fragment and Sb's block is uniform.
 #pragma once
+#include <type_traits>
 #include "qf8_device.h"
 #include "qf8_internal.h"
 
@@ -50,15 +51,18 @@ constexpr int kBK = 128;                                  // bytes of k per step
 __device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
 
 // A buffer descriptor whose base moves along k: `left` is the number of bytes from the base to the
-// end of the tensor, so every lane past it reads zeros.
-struct MovingBuffer {
+// end of the tensor, so every lane past it reads zeros. LONG: the base may move over 4 GiB and more
+// (whole rows of k), where a count capped at its start would run out before the tensor does.
+template <bool LONG>
+struct MovingBufferOf {
+    typedef typename std::conditional<LONG, uint64_t, uint32_t>::type Count;
     uint64_t base;
-    uint32_t left;
+    Count left;
     __device__ __forceinline__ v4i32 rsrc() const {
         v4i32 r;
         r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
         r.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32) & 0xFFFF);
-        r.z = __builtin_amdgcn_readfirstlane((int)left);
+        r.z = __builtin_amdgcn_readfirstlane((int)(uint32_t)(LONG && left > 0xFFFFFFFFu ? 0xFFFFFFFFu : left));
         r.w = 0x00020000;
         return r;
     }
@@ -67,6 +71,7 @@ struct MovingBuffer {
         left = left > bytes ? left - bytes : 0u;
     }
 };
+typedef MovingBufferOf<false> MovingBuffer;
 __device__ __forceinline__ uint32_t cap31(int64_t bytes) {
     return bytes > 0x7FFFFFFFll ? 0x7FFFFFFFu : bytes < 0 ? 0u : (uint32_t)bytes;
 }
@@ -296,12 +301,23 @@ __device__ __forceinline__ bool place_tile(const MatmulArgs &p, int bm, int bn, 
     } else {
         const int tm = (int)((p.m + bm - 1) / bm);
         const int64_t per = (int64_t)tm * tn;
-        const int64_t total = per * (p.mode == kMatmulExpertsK ? p.experts : p.splits);
-        const int64_t id = xcd_order(blockIdx.x, total);
-        if (id < 0) return false;
-        const int part = (int)(id / per);
+        int part;
+        int64_t t;
+        if (p.mode == kMatmulExpertsK) {
+            // Experts have unequal ranges of k: each expert's tiles go to all 8 XCDs, in ranges of q (with
+            // whole experts for an XCD the CUs stood idle for 38% of the time at 32 experts).
+            const int64_t q = (per + 7) >> 3, i = blockIdx.x >> 3;
+            part = (int)(i / q);
+            t = ((blockIdx.x + part) & 7) * q + i - part * q;
+            if (t >= per) return false;
+        } else {
+            const int64_t id = xcd_order(blockIdx.x, per * p.splits);
+            if (id < 0) return false;
+            part = (int)(id / per);
+            t = id - part * per;
+        }
         int im, in;
-        panel_order(id - part * per, tm, tn, im, in);
+        panel_order(t, tm, tn, im, in);
         pl.row0 = (int64_t)im * bm;
         pl.rows = (int)(p.m - pl.row0 < bm ? p.m - pl.row0 : bm);
         pl.n0 = in * bn;
@@ -334,7 +350,8 @@ __device__ __forceinline__ int64_t source_row(const MatmulArgs &p, const TilePla
 template <int KIND, bool EXACT, int BM, int BN, int TN, int NT>
 struct TileLoads {
     static constexpr int LA = BM * kBK / 16 / NT, LB = BN * kBK / 16 / NT;
-    MovingBuffer ba, bb;
+    MovingBuffer ba;
+    MovingBufferOf<KIND == kKN> bb;
     uint32_t va[LA], vb[LB], stepb;
 
     __device__ __forceinline__ void init(const MatmulArgs &p, const TilePlace &pl, int steps, int t) {
@@ -355,7 +372,7 @@ struct TileLoads {
         const uint64_t bmat = (uint64_t)(p.mode == kMatmulExperts && pl.expert > 0 ? pl.expert : 0) * (uint64_t)p.n * (uint64_t)p.k;
         if constexpr (KIND == kKN) {
             bb.base = uniform64((uint64_t)(uintptr_t)p.b + bmat + (uint64_t)(pl.k0 * p.n + pl.n0));
-            bb.left = cap31((p.k - pl.k0) * p.n - pl.n0);
+            bb.left = uniform64((uint64_t)((p.k - pl.k0) * p.n - pl.n0));
             constexpr int C = BN / 16;
 #pragma unroll
             for (int i = 0; i < LB; ++i) {
@@ -372,8 +389,8 @@ struct TileLoads {
                 n = n < p.n - pl.n0 ? n : p.n - pl.n0 - 1;
                 vb[i] = (uint32_t)n * (uint32_t)p.k + 16u * ch;
             }
+            bb.left = __builtin_amdgcn_readfirstlane((int)bb.left);
         }
-        bb.left = __builtin_amdgcn_readfirstlane((int)bb.left);
         stepb = KIND == kKN ? (uint32_t)kBK * (uint32_t)p.n : (uint32_t)kBK;
     }
 };
@@ -403,7 +420,7 @@ __device__ __forceinline__ void store_tile(const MatmulArgs &p, const TilePlace 
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
                     const int n = pl.n0 + wn * TN + 32 * j + (lane & 31);
-                    if (n < p.n) y[n] = zero ? 0.0f : acc[i][j][e];
+                    if (n < p.n) __builtin_nontemporal_store(zero ? 0.0f : acc[i][j][e], y + n);
                 }
             }
     } else {                                             // lane: row lane % 16
@@ -796,7 +813,8 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
 
         // Each stream of loads has its own position along k; past the last step its buffer has length 0
         // and the loads leave zeros nobody uses.
-        MovingBuffer first = ld.ba, second = ld.ba, cols = ld.bb;
+        MovingBuffer first = ld.ba, second = ld.ba;
+        auto cols = ld.bb;
         int n_first = 0, n_second = 0, n_scale = 0;
         auto load_first = [&](int u) {                  // piece u of 6: b and a's first halves of step n_first
             const uint32_t at = lds0 + (uint32_t)(n_first & 1) * kStage;

@@ -132,7 +132,7 @@ int launch_matmul(const MatmulArgs &args, int fmt_a, int fmt_b, int kind, int po
         });
         const int64_t tiles = ((p.m + sizes[pl.size].bm - 1) / sizes[pl.size].bm) *
                               ((p.n + sizes[pl.size].bn - 1) / sizes[pl.size].bn);
-        return launch_by_format(p, fmt_a, fmt_b, kind, math, pl.size, tiles * p.experts, s);
+        return launch_by_format(p, fmt_a, fmt_b, kind, math, pl.size, (tiles + 7) / 8 * 8 * p.experts, s);
     }
     // the rows of an expert end inside a tile: half a tile more for each that has rows
     const double used = (double)(p.m < p.experts ? p.m : p.experts);

@@ -329,3 +329,21 @@ def test_graph_replays_the_product():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want), i
+
+
+@pytest.mark.parametrize("m", [3, 130])
+def test_weight_of_more_than_4_gib(m):
+    """[k][n] weights whose rows pass 2 and 4 GiB: the last rows of k count like the first."""
+    k, n = 33024, 131072
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(21)
+    a, sa = codes(gen, (m, k), "e4m3"), scales(gen, (m, k // 128), True)
+    b = torch.empty(k, n, dtype=torch.uint8, device="cuda")
+    for r in range(0, k, 1032):
+        b[r:r + 1032] = codes(gen, (1032, n), "e4m3")
+    sb = scales(gen, (k // 128, n // 128), True)
+    y = qf8.matmul_block(a, sa, b, sb, qf8.E4M3, qf8.E4M3, qf8.WEIGHT_KN, pow2_scales=True)
+    va = values(a, sa, "e4m3", 1)
+    for at in (0, n // 2 - 128, n - 256):
+        ref, mag = product(va, values(b[:, at:at + 256].contiguous(), sb[:, at // 128:at // 128 + 2].contiguous(), "e4m3", 128))
+        assert_close(y[:, at:at + 256], ref, mag, k, f"columns {at}")
