@@ -28,6 +28,9 @@
 #include "qf8_device.h"
 #include "qf8_internal.h"
 
+// Lambdas called from two loops: outlined, their variables would live in memory and no longer be uniform.
+#define QF8_INLINE __attribute__((always_inline))
+
 namespace qf8 {
 
 typedef int v8i32 __attribute__((ext_vector_type(8)));
@@ -816,7 +819,7 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
         MovingBuffer first = ld.ba, second = ld.ba;
         auto cols = ld.bb;
         int n_first = 0, n_second = 0, n_scale = 0;
-        auto load_first = [&](int u) {                  // piece u of 6: b and a's first halves of step n_first
+        auto load_first = [&](int u) QF8_INLINE {                  // piece u of 6: b and a's first halves of step n_first
             const uint32_t at = lds0 + (uint32_t)(n_first & 1) * kStage;
             if (u == 0 && n_first >= steps) first.left = cols.left = 0;
             if (u < 4) lds_dma16(cols.rsrc(), ld.vb[u], at + kA + (uint32_t)u * 8192u);
@@ -827,7 +830,7 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
                 ++n_first;
             }
         };
-        auto load_second = [&](int u) {                 // piece u of 2: a's second halves of step n_second
+        auto load_second = [&](int u) QF8_INLINE {                 // piece u of 2: a's second halves of step n_second
             const uint32_t at = lds0 + (uint32_t)(n_second & 1) * kStage;
             if (u == 0 && n_second >= steps) second.left = 0;
             lds_dma16(second.rsrc(), ld.va[2 * u + 1], at + (2u * u + 1u) * 8192u);
@@ -836,7 +839,7 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
                 ++n_second;
             }
         };
-        auto load_scale = [&]() {
+        auto load_scale = [&]() QF8_INLINE {
             if (n_scale >= steps) ls.buf.left = 0;
             lds_dma4(ls.buf.rsrc(), ls.off, lds_raw + (uint32_t)(n_scale & 1) * (BM + BN) * 4u);
             ls.buf.advance(ls.step);
@@ -865,19 +868,19 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
         v4f32 part[4] = {};
         float sa[4] = {}, late = 0.0f;
         int eb = 0;
-        auto scale_one = [&](int i, int j, float f) {   // acc += part * (1/Sa 1/Sb)
+        auto scale_one = [&](int i, int j, float f) QF8_INLINE {   // acc += part * (1/Sa 1/Sb)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[j][e], f, acc[i][j][e]);
             asm volatile("" : "+v"(acc[i][j]));         // here, not after a later branch: part is used again
         };
         // codes past k in the last step: chunk g holds k = 16 g + [0, 16) of a fragment, chunk g + 4 64 more
-        auto trim = [&](v8i32 f, int krem) {
+        auto trim = [&](v8i32 f, int krem) QF8_INLINE {
             asm volatile("" : "+s"(krem));              // keeps the masks inside the branch
             const uint4 lo = keep_bytes(make_uint4(f[0], f[1], f[2], f[3]), krem - 16 * g);
             const uint4 hi = keep_bytes(make_uint4(f[4], f[5], f[6], f[7]), krem - 64 - 16 * g);
             return join16(lo, hi);
         };
-        auto read_a = [&](const uint8_t *ta, const float *sc, int half) {
+        auto read_a = [&](const uint8_t *ta, const float *sc, int half) QF8_INLINE {
             const uint8_t *src = ta + (wm * TM + half * 64 + r16) * kBK;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -896,81 +899,109 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
         };
         // 16 products. Between them go the loads (a load of 1 KiB takes the path to LDS for 16 cycles:
         // issued in a row they would hold up the wave) and, in the first half, the next step's scales.
-        auto products = [&](int half, int s) {
+        auto between = [&](int half, int m, int s, float &next) QF8_INLINE {
+            if (half == 0) {
+                if (m == 4 || m == 8) load_second(m / 4 - 1);
+                if (m == 5) asm volatile("" : "+v"(next));
+                if (m == 11) inv[(s + 1) & 1][t] = inverse_scale<MATH>(next);
+            } else {
+                if (m % 2 == 0 && m / 2 < 6) load_first(m / 2);
+                if (m == 12) load_scale();
+            }
+        };
+        // TAIL, the last tile of some rows: halves of 64 rows past the last one take no products (half 1 then
+        // only finishes half 0's scaling). The experts' products on 4096 x 8 rows 1357 -> 1306 us; in one
+        // loop with the full tiles it cost those 1-2%.
+        const bool left[2] = {wm * TM < pl.rows, wm * TM + 64 < pl.rows};
+        auto products = [&](auto tail, int half, int s) QF8_INLINE {
+            constexpr bool TAIL = decltype(tail)::value;
             __builtin_amdgcn_s_setprio(1);
             float next = 1.0f;
             if (half == 0) next = raw[(s + 1) & 1][t];
+            if (!TAIL || left[half]) {
 #pragma unroll
-            for (int m = 0; m < 4 * FN; ++m) {
-                const int i = m / FN, j = m % FN, at = half * 4 + i;
-                if constexpr (POW2) {
-                    acc[at][j] = mfma_e8m0<FA, FB>(fb[j], fa[i], acc[at][j], eb, __float_as_int(sa[i]));
-                    asm volatile("" : "+v"(acc[at][j]));
-                } else {
-                    part[j] = mfma_raw<FA, FB>(fb[j], fa[i], v4f32{0.0f, 0.0f, 0.0f, 0.0f});
+                for (int m = 0; m < 4 * FN; ++m) {
+                    const int i = m / FN, j = m % FN, at = half * 4 + i;
+                    if constexpr (POW2) {
+                        acc[at][j] = mfma_e8m0<FA, FB>(fb[j], fa[i], acc[at][j], eb, __float_as_int(sa[i]));
+                        asm volatile("" : "+v"(acc[at][j]));
+                    } else {
+                        part[j] = mfma_raw<FA, FB>(fb[j], fa[i], v4f32{0.0f, 0.0f, 0.0f, 0.0f});
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (m < 3) scale_one((half * 4 + 7) % 8, m + 1, late);
+                        else scale_one(half * 4 + (m - 3) / FN, (m - 3) % FN, sa[(m - 3) / FN]);
+                    }
+                    between(half, m, s, next);
                     __builtin_amdgcn_sched_barrier(0);
-                    if (m < 3) scale_one((half * 4 + 7) % 8, m + 1, late);
-                    else scale_one(half * 4 + (m - 3) / FN, (m - 3) % FN, sa[(m - 3) / FN]);
                 }
-                if (half == 0) {
-                    if (m == 4 || m == 8) load_second(m / 4 - 1);
-                    if (m == 5) asm volatile("" : "+v"(next));
-                    if (m == 11) inv[(s + 1) & 1][t] = inverse_scale<MATH>(next);
-                } else {
-                    if (m % 2 == 0 && m / 2 < 6) load_first(m / 2);
-                    if (m == 12) load_scale();
+                late = sa[3];
+            } else {
+#pragma unroll
+                for (int m = 0; m < 4 * FN; ++m) between(half, m, s, next);
+                if constexpr (!POW2) {
+                    if (half == 1 && left[0]) {
+#pragma unroll
+                        for (int j = 1; j < FN; ++j) scale_one(3, j, late);
+                    }
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
-            late = sa[3];
             __builtin_amdgcn_s_setprio(0);
         };
 
-        for (int s = 0; s < steps; ++s) {
-            const uint8_t *const ta = tiles[s & 1], *const tb = ta + kA;
-            const float *const sc = inv[s & 1];
-            const int krem = kend - s * kBK;
-            // P0
+        auto all_steps = [&](auto tail) QF8_INLINE {
+            constexpr bool TAIL = decltype(tail)::value;
+            for (int s = 0; s < steps; ++s) {
+                const uint8_t *const ta = tiles[s & 1], *const tb = ta + kA;
+                const float *const sc = inv[s & 1];
+                const int krem = kend - s * kBK;
+                // P0
+                if (!TAIL || left[0]) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if constexpr (KIND == kKN) {
-                    v2i32 q[4];
+                    for (int j = 0; j < FN; ++j) {
+                        if constexpr (KIND == kKN) {
+                            v2i32 q[4];
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const int kr = (h >> 1) * 64 + 16 * g + 8 * (h & 1) + (r16 >> 1);
-                        const int ch = (wn * TN + 16 * j) / 16;
-                        q[h] = read_transposed(tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1));
+                            for (int h = 0; h < 4; ++h) {
+                                const int kr = (h >> 1) * 64 + 16 * g + 8 * (h & 1) + (r16 >> 1);
+                                const int ch = (wn * TN + 16 * j) / 16;
+                                q[h] = read_transposed(tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1));
+                            }
+                            fb[j] = v8i32{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
+                        } else {
+                            const uint8_t *src = tb + (wn * TN + r16) * kBK + j * 16 * kBK;
+                            fb[j] = join16(*(const uint4 *)(src + swz), *(const uint4 *)(src + (swz ^ 64u)));
+                        }
                     }
-                    fb[j] = v8i32{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
-                } else {
-                    const uint8_t *src = tb + (wn * TN + r16) * kBK + j * 16 * kBK;
-                    fb[j] = join16(*(const uint4 *)(src + swz), *(const uint4 *)(src + (swz ^ 64u)));
+                    read_a(ta, sc, 0);
+                    if (krem < kBK) {
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) fb[j] = trim(fb[j], krem);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) fa[i] = trim(fa[i], krem);
+                    }
                 }
-            }
-            read_a(ta, sc, 0);
-            if (krem < kBK) {
+                wait_vmem_but<7>();                         // a's second halves of this step
+                phase_end();
+                // P1
+                products(tail, 0, s);
+                phase_end();
+                // P2
+                if (!TAIL || left[1]) {
+                    read_a(ta, sc, 1);
+                    if (krem < kBK) {
 #pragma unroll
-                for (int j = 0; j < FN; ++j) fb[j] = trim(fb[j], krem);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) fa[i] = trim(fa[i], krem);
+                        for (int i = 0; i < 4; ++i) fa[i] = trim(fa[i], krem);
+                    }
+                }
+                wait_vmem_but<2>();                         // b and a's first halves of the next
+                phase_end();
+                // P3
+                products(tail, 1, s);
+                phase_end();
             }
-            wait_vmem_but<7>();                         // a's second halves of this step
-            phase_end();
-            // P1
-            products(0, s);
-            phase_end();
-            // P2
-            read_a(ta, sc, 1);
-            if (krem < kBK) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) fa[i] = trim(fa[i], krem);
-            }
-            wait_vmem_but<2>();                         // b and a's first halves of the next
-            phase_end();
-            // P3
-            products(1, s);
-            phase_end();
-        }
+        };
+        if (pl.rows > BM - 64) all_steps(std::false_type());
+        else all_steps(std::true_type());
         if constexpr (!POW2) {
 #pragma unroll
             for (int j = 1; j < FN; ++j) scale_one(FM - 1, j, late);

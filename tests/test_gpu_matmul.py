@@ -347,3 +347,28 @@ def test_weight_of_more_than_4_gib(m):
     for at in (0, n // 2 - 128, n - 256):
         ref, mag = product(va, values(b[:, at:at + 256].contiguous(), sb[:, at // 128:at // 128 + 2].contiguous(), "e4m3", 128))
         assert_close(y[:, at:at + 256], ref, mag, k, f"columns {at}")
+
+
+@pytest.mark.parametrize("rows", [1, 63, 64, 65, 128, 129, 191, 192, 193, 255])
+@pytest.mark.parametrize("kind", ["nk", "kn"])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_last_rows_of_the_large_tile(rows, kind, pow2):
+    """Halves of 64 rows past the last one take no products: every count of halves that exist."""
+    run_dense(3840 + rows, 4096, 388, kind, "e4m3", "e4m3", pow2, torch.bfloat16, seed=rows)
+
+
+@pytest.mark.parametrize("rows", [1, 64, 65, 130, 193])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_infinities_in_last_rows(rows, pow2):
+    """An infinite code in the last row reaches every column of that row (Inf, or NaN against a zero)
+    and no other row."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(rows)
+    m, n, k = 3840 + rows, 4096, 256
+    a, sa = codes(gen, (m, k), "e5m2"), scales(gen, (m, 2), pow2)
+    a[m - 1, 7] = 0x7C
+    b, sb, _ = operands(gen, "nk", n, k, "e4m3", pow2)
+    y = qf8.matmul_block(a, sa, b, sb, qf8.E5M2, qf8.E4M3, qf8.WEIGHT_NK, pow2_scales=pow2)
+    bad = ~torch.isfinite(y)
+    assert bool(bad[m - 1].all())
+    assert int(bad[:m - 1].sum()) == 0
