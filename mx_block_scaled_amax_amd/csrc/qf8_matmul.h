@@ -190,34 +190,42 @@ struct TilePlace {
     int split;
 };
 
+// Tiles are counted in 32 bits (a grid has no more): a 64-bit division costs a wave near a thousand cycles.
+//
 // Contiguous ranges of tiles for each of the 8 XCDs (workgroups are dealt to them in turn), so that
-// tiles that share operands share an L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
-    const int64_t x = id & 7, i = id >> 3, q = total >> 3, r = total & 7;
+// tiles that share operands share an L2. -1: no tile.
+__device__ __forceinline__ int xcd_order(uint32_t id, uint32_t total) {
+    const uint32_t x = id & 7, i = id >> 3, q = total >> 3, r = total & 7;
     if (i >= q + (x < r ? 1 : 0)) return -1;
-    return x * q + (x < r ? x : r) + i;
+    return (int)(x * q + (x < r ? x : r) + i);
 }
 
-// Tile number t of tm x tn tiles, in panels of 8 tile rows: neighbours share both operands.
-__device__ __forceinline__ void panel_order(int64_t t, int tm, int tn, int &im, int &in) {
-    constexpr int kPanel = 8;
-    const int64_t per = (int64_t)kPanel * tn;
-    const int p = (int)(t / per), r = (int)(t - p * per);
-    const int h = tm - p * kPanel < kPanel ? tm - p * kPanel : kPanel;
-    im = p * kPanel + r % h;
-    in = r / h;
+// Tile number t of tm x tn tiles, in panels of PANEL tile rows: neighbours share both operands.
+template <uint32_t PANEL>
+__device__ __forceinline__ void panel_order(uint32_t t, uint32_t tm, uint32_t tn, uint32_t &im, uint32_t &in) {
+    const uint32_t per = PANEL * tn, p = t / per, r = t - p * per;
+    const uint32_t left = tm - p * PANEL;
+    if (left >= PANEL) {
+        im = p * PANEL + r % PANEL;
+        in = r / PANEL;
+    } else {
+        in = r / left;
+        im = p * PANEL + r - in * left;
+    }
 }
 
 // Row tiles of every expert, found by each wave from the offsets: expert e owns rows
 // [offsets[e], offsets[e+1]) and ceil(rows / bm) tiles; the rows after the last expert are one more
-// stretch, of zeros. Returns the number of row tiles; with want >= 0 also the place of that one.
-__device__ __forceinline__ int find_row_tile(const int32_t *offsets, int experts, int64_t nrows, int bm, int want,
-                                             TilePlace &pl) {
+// stretch, of zeros. order(total) maps the number of row tiles to the one whose place is wanted, < 0: none.
+template <typename Order>
+__device__ __forceinline__ bool find_row_tile(const int32_t *offsets, int experts, int64_t nrows, int bm, Order order,
+                                              TilePlace &pl) {
     const int lane = threadIdx.x & 63;
-    int total = 0;
-    for (int e0 = 0; e0 <= experts; e0 += 64) {
+    int64_t lo = 0, hi = 0;
+    int c = 0, first = 0, total = 0;
+    auto stretch = [&](int e0) {                         // those of 64 experts, a lane each
         const int e = e0 + lane;
-        int64_t lo = 0, hi = 0;
+        lo = hi = 0;
         if (e < experts) {
             lo = offsets[e];
             hi = offsets[e + 1];
@@ -227,14 +235,23 @@ __device__ __forceinline__ int find_row_tile(const int32_t *offsets, int experts
         }
         lo = lo < 0 ? 0 : lo > nrows ? nrows : lo;
         hi = hi < lo ? lo : hi > nrows ? nrows : hi;
-        const int c = (int)((hi - lo + bm - 1) / bm);
+        c = (int)((uint32_t)(hi - lo + bm - 1) / (uint32_t)bm);
         int inc = c;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int v = __shfl_up(inc, d);
             inc += lane >= d ? v : 0;
         }
-        const int first = total + inc - c;
+        first = total + inc - c;
+        total += __builtin_amdgcn_readlane(inc, 63);
+    };
+    for (int e0 = 0; e0 <= experts; e0 += 64) stretch(e0);
+    const int want = order((uint32_t)total);
+    if (want < 0) return false;
+    const bool again = experts >= 64;                    // the lanes hold the last stretch of several
+    total = 0;
+    for (int e0 = 0;; e0 += 64) {
+        if (again) stretch(e0);
         const uint64_t hit = __ballot(want >= first && want < first + c);
         if (hit) {
             const int src = __ffsll((unsigned long long)hit) - 1;
@@ -243,10 +260,10 @@ __device__ __forceinline__ int find_row_tile(const int32_t *offsets, int experts
             pl.row0 = (int64_t)uniform64((uint64_t)__shfl((long long)r0, src));
             pl.rows = __builtin_amdgcn_readfirstlane(__shfl((int)(left < bm ? left : bm), src));
             pl.expert = e0 + src < experts ? e0 + src : -1;
+            return true;
         }
-        total += __builtin_amdgcn_readlane(inc, 63);
+        if (e0 + 64 > experts) return false;             // not reached: want is below the total
     }
-    return total;
 }
 
 // RUN neighbouring columns of one row, rounded once to BF16 or stored as FP32. Rows need no alignment:
@@ -283,56 +300,52 @@ __device__ __forceinline__ void store_run(const MatmulArgs &p, const TilePlace &
 __device__ __forceinline__ bool place_tile(const MatmulArgs &p, int bm, int bn, TilePlace &pl) {
     pl.split = 0;
     pl.expert = 0;
-    const int tn = (p.n + bn - 1) / bn;
+    const uint32_t tn = (uint32_t)(p.n + bn - 1) / (uint32_t)bn;
+    uint32_t im, in;
     if (p.mode == kMatmulExperts) {
-        pl.rows = 0;
-        const int tiles_m = find_row_tile(p.offsets, p.experts, p.m, bm, -1, pl);
-        const int64_t id = xcd_order(blockIdx.x, (int64_t)tiles_m * tn);
-        if (id < 0) return false;
         // all columns of up to 4 row tiles, then the next ones: the row tiles of one expert run together
-        int im, in;
-        constexpr int kPanel = 4;
-        const int64_t per = (int64_t)kPanel * tn;
-        const int pn = (int)(id / per), rr = (int)(id - pn * per);
-        const int h = tiles_m - pn * kPanel < kPanel ? tiles_m - pn * kPanel : kPanel;
-        im = pn * kPanel + rr % h;
-        in = rr / h;
-        find_row_tile(p.offsets, p.experts, p.m, bm, im, pl);
-        pl.n0 = in * bn;
+        const bool found = find_row_tile(p.offsets, p.experts, p.m, bm, [&](uint32_t tiles_m) {
+            const int id = xcd_order(blockIdx.x, tiles_m * tn);
+            if (id < 0) return -1;
+            panel_order<4>((uint32_t)id, tiles_m, tn, im, in);
+            return (int)im;
+        }, pl);
+        if (!found) return false;
+        pl.n0 = (int)in * bn;
         pl.k0 = 0;
         pl.k1 = p.k;
     } else {
-        const int tm = (int)((p.m + bm - 1) / bm);
-        const int64_t per = (int64_t)tm * tn;
-        int part;
-        int64_t t;
+        const uint32_t tm = (uint32_t)((p.m + bm - 1) / bm), per = tm * tn;
+        uint32_t part = 0, t;
         if (p.mode == kMatmulExpertsK) {
             // Experts have unequal ranges of k: each expert's tiles go to all 8 XCDs, in ranges of q (with
             // whole experts for an XCD the CUs stood idle for 38% of the time at 32 experts).
-            const int64_t q = (per + 7) >> 3, i = blockIdx.x >> 3;
-            part = (int)(i / q);
+            const uint32_t q = (per + 7) >> 3, i = blockIdx.x >> 3;
+            part = i / q;
             t = ((blockIdx.x + part) & 7) * q + i - part * q;
             if (t >= per) return false;
         } else {
-            const int64_t id = xcd_order(blockIdx.x, per * p.splits);
+            const int id = xcd_order(blockIdx.x, per * (uint32_t)p.splits);
             if (id < 0) return false;
-            part = (int)(id / per);
-            t = id - part * per;
+            t = (uint32_t)id;
+            if (p.splits > 1) {
+                part = t / per;
+                t -= part * per;
+            }
         }
-        int im, in;
-        panel_order(t, tm, tn, im, in);
+        panel_order<8>(t, tm, tn, im, in);
         pl.row0 = (int64_t)im * bm;
         pl.rows = (int)(p.m - pl.row0 < bm ? p.m - pl.row0 : bm);
-        pl.n0 = in * bn;
+        pl.n0 = (int)in * bn;
         if (p.mode == kMatmulExpertsK) {
-            pl.expert = part;
+            pl.expert = (int)part;
             int64_t lo = p.offsets[part], hi = p.offsets[part + 1];
             lo = lo < 0 ? 0 : lo > p.k ? p.k : lo & ~(int64_t)(kBK - 1);
             hi = hi < lo ? lo : hi > p.k ? p.k : hi;
             pl.k0 = lo;
             pl.k1 = hi;
         } else {
-            pl.split = part;
+            pl.split = (int)part;
             pl.k0 = (int64_t)part * p.split_k;
             pl.k1 = pl.k0 + p.split_k < p.k ? pl.k0 + p.split_k : p.k;
         }
@@ -405,43 +418,73 @@ __device__ __forceinline__ bool no_source(const MatmulArgs &p, int64_t row) {
     return src < 0 || src >= p.a_rows;
 }
 
-// Stores a wave's TM x TN values.
-template <int KIND, bool EXACT, int TM, int TN, typename V, int FM, int FN>
-__device__ __forceinline__ void store_tile(const MatmulArgs &p, const TilePlace &pl, int wm, int wn, int lane,
-                                           const V (&acc)[FM][FN]) {
-    if constexpr (EXACT) {                               // lane: column lane % 32, rows 8 q + 4 (lane / 32) + e
-        const int64_t plane = p.mode == kMatmulExpertsK ? pl.expert : pl.split;
+// FP32 results go through LDS to whole rows of BN columns: a store of 16 bytes a lane covers 1 KiB of
+// memory, one of 4 bytes 256 bytes in the same time. Lane: column lane % 32, rows 8 q + 4 (lane / 32) + e of a
+// 32 x 32 fragment; rows 4-7 of 8 hold columns c ^ 32, so that both halves of a wave write all banks. buf: the
+// operand tiles, which every wave has left.
+template <int BM, int BN, int TM, int TN, int NT, typename V, int FM, int FN>
+__device__ __forceinline__ void store_rows(const MatmulArgs &p, const TilePlace &pl, float *buf, int wm, int wn,
+                                           int t, const V (&acc)[FM][FN]) {
+    const int lane = t & 63, r32 = lane & 31, h = lane >> 5;
+    phase_end();
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const int r = wm * TM + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-                if (r >= pl.rows) continue;
-                const int64_t row = pl.row0 + r;
-                const bool zero = no_source(p, row);
-                float *y = (float *)p.y + (plane * p.m + row) * p.n;
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    const int n = pl.n0 + wn * TN + 32 * j + (lane & 31);
-                    if (n < p.n) __builtin_nontemporal_store(zero ? 0.0f : acc[i][j][e], y + n);
-                }
+                const int r = wm * TM + 32 * i + 8 * (e >> 2) + 4 * h + (e & 3), c = wn * TN + 32 * j + r32;
+                buf[r * BN + (c ^ (h << 5))] = acc[i][j][e];
             }
-    } else {                                             // lane: row lane % 16
-        const int g = lane >> 4;
-        constexpr int RUN = KIND == kKN || FN == 1 ? 4 : 8;
+    phase_end();
+    constexpr int CH = BN / 4, U = BM * CH / NT;         // 16-byte pieces of a row; those of a thread
+    const int64_t plane = p.mode == kMatmulExpertsK ? pl.expert : pl.split;
+    const int r0 = t / CH, c = 4 * (t % CH), n = pl.n0 + c;
+    float *y = (float *)p.y + (plane * p.m + pl.row0 + r0) * p.n + n;
+    const int64_t pitch = (int64_t)(NT / CH) * p.n;
+    typedef float any4 __attribute__((ext_vector_type(4), aligned(4)));     // rows need no alignment
+    static_assert(NT / CH % 8 == 0, "the rows of a thread hold their columns in the same order");
+    const float *src = buf + r0 * BN + (c ^ (((r0 >> 2) & 1) << 5));
+    if (pl.rows == BM && pl.n0 + BN <= p.n && !p.rows) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int r = wm * TM + 16 * i + (lane & 15);
-            if (r >= pl.rows) continue;
-            const int64_t row = pl.row0 + r;
-            const bool zero = no_source(p, row);
+        for (int u = 0; u < U; ++u, y += pitch)
+            __builtin_nontemporal_store((any4)*(const v4f32 *)(src + u * (NT / CH) * BN), (any4 *)y);
+        return;
+    }
+#pragma unroll 1
+    for (int u = 0; u < U; ++u, y += pitch) {
+        const int r = u * (NT / CH) + r0;
+        if (r >= pl.rows || n >= p.n) continue;
+        v4f32 v = *(const v4f32 *)(src + u * (NT / CH) * BN);
+        if (no_source(p, pl.row0 + r)) v = (v4f32)0.0f;
+        if (n + 4 <= p.n) {
+            __builtin_nontemporal_store((any4)v, (any4 *)y);
+        } else {
 #pragma unroll
-            for (int u = 0; u < 4 * FN / RUN; ++u) {
-                float v[RUN];
+            for (int e = 0; e < 3; ++e)
+                if (n + e < p.n) y[e] = v[e];
+        }
+    }
+}
+
+// Stores a wave's TM x TN values of an FP8 product. Lane: row lane % 16.
+template <int KIND, int TM, int TN, typename V, int FM, int FN>
+__device__ __forceinline__ void store_tile(const MatmulArgs &p, const TilePlace &pl, int wm, int wn, int lane,
+                                           const V (&acc)[FM][FN]) {
+    const int g = lane >> 4;
+    constexpr int RUN = KIND == kKN || FN == 1 ? 4 : 8;
 #pragma unroll
-                for (int e = 0; e < RUN; ++e) v[e] = zero ? 0.0f : acc[i][u * (RUN / 4) + e / 4][e % 4];
-                store_run<RUN>(p, pl, row, pl.n0 + wn * TN + 4 * RUN * u + RUN * g, v);
-            }
+    for (int i = 0; i < FM; ++i) {
+        const int r = wm * TM + 16 * i + (lane & 15);
+        if (r >= pl.rows) continue;
+        const int64_t row = pl.row0 + r;
+        const bool zero = no_source(p, row);
+#pragma unroll
+        for (int u = 0; u < 4 * FN / RUN; ++u) {
+            float v[RUN];
+#pragma unroll
+            for (int e = 0; e < RUN; ++e) v[e] = zero ? 0.0f : acc[i][u * (RUN / 4) + e / 4][e % 4];
+            store_run<RUN>(p, pl, row, pl.n0 + wn * TN + 4 * RUN * u + RUN * g, v);
         }
     }
 }
@@ -510,7 +553,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     typedef TileLoads<KIND, EXACT, BM, BN, TN, NT> Loads;
     typedef ScaleLoads<KIND, EXACT, BM, BN, NT> Scales;
     constexpr int LA = Loads::LA, LB = Loads::LB, LT = LA + LB, BA = Scales::BA;
-    static_assert(LA * NT * 16 == kA && LB * NT * 16 == kB, "tile and workgroup do not match");
+    static_assert(LA * NT * 16 == kA && LB * NT * 16 == kB && (!EXACT || BM * BN * 4 <= D * kStage), "tile and workgroup do not match");
     __shared__ __attribute__((aligned(1024))) uint8_t tiles[D][kStage];
     __shared__ __attribute__((aligned(256))) float raw[D][NT];
     __shared__ __attribute__((aligned(16))) float inv[2][NT];
@@ -763,7 +806,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     }
     wait_vmem();                                        // no load may still write LDS when the workgroup ends
 
-    store_tile<KIND, EXACT, TM, TN>(p, pl, wm, wn, lane, acc);
+    if constexpr (EXACT) store_rows<BM, BN, TM, TN, NT>(p, pl, (float *)&tiles[0][0], wm, wn, t, acc);
+    else store_tile<KIND, TM, TN>(p, pl, wm, wn, lane, acc);
 }
 
 // ---- the large tile in two alternating groups of waves --------------------------------------------
@@ -1009,7 +1053,7 @@ __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
         if (wave < 4) phase_end();                      // the others are one phase behind
         wait_vmem();                                    // no load may still write LDS when the workgroup ends
     }
-    store_tile<KIND, false, TM, TN>(p, pl, wm, wn, lane, acc);
+    store_tile<KIND, TM, TN>(p, pl, wm, wn, lane, acc);
 }
 
 // ---- launch ----------------------------------------------------------------------------------------
