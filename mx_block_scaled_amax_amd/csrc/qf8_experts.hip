@@ -51,6 +51,12 @@ __device__ __forceinline__ float wave_sum(float v) {
     for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
     return v;
 }
+// LDS written by one lane of a wave and read by another: the wave's LDS accesses run in order.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 // Order-preserving integers of floats; 0 is below every value.
 __device__ __forceinline__ uint32_t float_key(float v) {
     const uint32_t b = __float_as_uint(v);
@@ -159,9 +165,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
 #pragma unroll
             for (int i = 0; i < NE; ++i)
                 if (64 * i + lane < p.experts) sl[64 * i + lane] = s[i];
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            wave_lds_fence();
             int slots = 1;
             while (slots < p.groups) slots <<= 1;
             const int W = 64 / slots, grp = lane / W, sub = lane % W;
@@ -264,6 +268,99 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
     }
 }
 
+// Reductions over a row of 16 lanes; every lane of the row gets the result.
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+    v = umax(v, dpp_mov<0xB1>(v));
+    v = umax(v, dpp_mov<0x4E>(v));
+    v = umax(v, dpp_mov<0x141>(v));
+    return umax(v, dpp_mov<0x140>(v));
+}
+__device__ __forceinline__ float row_max(float v) {
+    const uint32_t k = row_max_u32(float_key(v));
+    return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k);
+}
+__device__ __forceinline__ double row_sum(double v) {
+    v += dpp_double<0xB1>(v);
+    v += dpp_double<0x4E>(v);
+    v += dpp_double<0x141>(v);
+    return v + dpp_double<0x140>(v);
+}
+
+// The same choice by logits with four tokens to a wave, one to each row of 16 lanes; lane l of a row holds
+// experts l, l + 16, ... (NE of them). With many tokens the time is the number of instructions, and a
+// round of the maximum costs about as many for four tokens as for one.
+template <typename T, int NE, int BY>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_rows_kernel(RouteArgs p) {
+    const int l16 = threadIdx.x & 15;
+    const int64_t tok = (int64_t)blockIdx.x * (4 * kRouteWaves) + (threadIdx.x >> 4);
+    if (tok >= p.tokens) return;                       // whole rows; nothing below leaves a row
+    const T *row = (const T *)p.logits + tok * p.experts;
+
+    float l[NE];
+    uint32_t key[NE];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int e = 16 * i + l16;
+        l[i] = e < p.experts ? load_logit(row, e) : -INFINITY;
+        top = fmaxf(top, l[i]);
+        key[i] = e >= p.experts ? 0u : BY == kByBf16 ? (float_key(l[i]) & 0xFFFF0000u) | (uint32_t)(0xFFFF - e) : float_key(l[i]);
+    }
+    const bool softmax = p.score == 0;
+    double total = 0.0;
+    if (softmax) {
+        top = row_max(top);
+        if (top == -INFINITY) top = 0.0f;
+        if (!p.renorm) {
+            double part = 0.0;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) part += exp((double)l[i] - (double)top);
+            total = row_sum(part);
+        }
+    }
+
+    int mine = 0;                                      // lane j of a row keeps the j-th choice
+    for (int j = 0; j < p.top_k; ++j) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < NE; ++i) best = umax(best, key[i]);
+        best = row_max_u32(best);
+        int e;
+        if constexpr (BY == kByBf16) {
+            e = 0xFFFF - (int)(best & 0xFFFFu);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) key[i] = key[i] == best ? 0u : key[i];       // no two keys are alike
+        } else {
+            uint32_t low = 0;                          // the lowest index among equal logits
+#pragma unroll
+            for (int i = 0; i < NE; ++i) low = umax(low, key[i] == best ? (uint32_t)(0xFFFF - 16 * i - l16) : 0u);
+            e = 0xFFFF - (int)row_max_u32(low);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) key[i] = 16 * i + l16 == e ? 0u : key[i];
+        }
+        mine = l16 == j ? e : mine;
+    }
+
+    double w = 0.0;
+    if (l16 < p.top_k) {
+        const double x = (double)load_logit(row, mine);
+        if (softmax) {
+            w = exp(x - (double)top);
+            if (!p.renorm) w = total > 0.0 ? w / total : 0.0;
+        } else {
+            w = sigmoid64(x);
+        }
+    }
+    if (p.renorm) {
+        const double sum = row_sum(w);
+        w = sum > 0.0 ? w / sum : 0.0;
+    }
+    if (l16 < p.top_k) {
+        p.ids[tok * p.top_k + l16] = mine;
+        p.weights[tok * p.top_k + l16] = (float)(w * (double)p.scale);
+    }
+}
+
 // Gradient of the logits. With w_j = scale p_j / T (T the sum of the chosen scores, or 1) and
 // g_j = scale dw_j:  dL/dp_j = (g_j - sum_i g_i p_i / T) / T, or g_j without renormalisation. Sigmoid:
 // dl_j = dL/dp_j p_j (1 - p_j). Softmax: dl_e = p_e (dL/dp_e - sum_j dL/dp_j p_j), where with
@@ -333,6 +430,73 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteA
     for (int i = 0; i < NE; ++i) {
         const int e = 64 * i + lane;
         if (e < p.experts) store_logit(out, e, v[i]);
+    }
+}
+
+// The same gradient with four tokens to a wave, one to each row of 16 lanes. A token's chosen entries
+// meet the others in LDS: experts are where the lanes of a row are not.
+template <typename T, int NE>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_backward_rows_kernel(RouteArgs p) {
+    __shared__ float grad[4 * kRouteWaves][16 * NE];
+    const int l16 = threadIdx.x & 15;
+    float *const mine = grad[threadIdx.x >> 4];
+    const int64_t tok = (int64_t)blockIdx.x * (4 * kRouteWaves) + (threadIdx.x >> 4);
+    if (tok >= p.tokens) return;                       // whole rows; nothing below leaves a row
+    const T *row = (const T *)p.logits + tok * p.experts;
+    T *out = (T *)p.dlogits + tok * p.experts;
+    const bool softmax = p.score == 0;
+    const bool all = softmax && !p.renorm;
+    const int id = l16 < p.top_k ? p.ids[tok * p.top_k + l16] : -1;
+    const bool have = id >= 0 && id < p.experts;
+    const double x = have ? (double)load_logit(row, id) : 0.0;
+    const double g = have ? (double)p.scale * (double)p.dweights[tok * p.top_k + l16] : 0.0;
+
+    float l[NE];
+    double total = 1.0, top = 0.0;
+    if (all) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int e = 16 * i + l16;
+            l[i] = e < p.experts ? load_logit(row, e) : -INFINITY;
+            m = fmaxf(m, l[i]);
+        }
+        m = row_max(m);
+        top = m == -INFINITY ? 0.0 : (double)m;
+        double part = 0.0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) part += exp((double)l[i] - top);
+        total = row_sum(part);
+    } else if (softmax) {
+        const float m = row_max(have ? (float)x : -INFINITY);
+        top = m == -INFINITY ? 0.0 : (double)m;
+    }
+    double s = 0.0;
+    if (have) s = softmax ? exp(x - top) : sigmoid64(x);
+    if (all) s = total > 0.0 ? s / total : 0.0;
+    double d, rest = 0.0;
+    if (p.renorm) {
+        const double sum = row_sum(s);
+        const double w = sum > 0.0 ? s / sum : 0.0;
+        const double mean = row_sum(g * w);
+        if (softmax) d = w * (g - mean);
+        else d = sum > 0.0 ? (g - mean) / sum * (s / (1.0 + exp(x))) : 0.0;
+    } else if (softmax) {
+        rest = row_sum(g * s);
+        d = s * (g - rest);
+    } else {
+        d = g * (s / (1.0 + exp(x)));
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        mine[16 * i + l16] = all && total > 0.0 ? (float)(-(exp((double)l[i] - top) / total) * rest) : 0.0f;
+    wave_lds_fence();
+    if (have) mine[id] = (float)d;
+    wave_lds_fence();
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int e = 16 * i + l16;
+        if (e < p.experts) store_logit(out, e, mine[e]);
     }
 }
 
@@ -643,6 +807,16 @@ __global__ __launch_bounds__(kCombineThreads) void combine_backward_kernel(Combi
 
 int launched() { return hipGetLastError() == hipSuccess ? QF8_OK : QF8_ERR_HIP; }
 
+// Whether four tokens share a wave. us a call, one token to a wave / four, top_k 8, BF16 logits:
+//   forward   4096 x 128  4.4 / 4.4   8192 x 128  5.7 / 4.6   16384 x 128  8.9 / 5.6
+//             4096 x 256  5.0 / 6.1   8192 x 256  6.7 / 6.4   16384 x 256  10.8 / 8.1 (FP32 7.5 / 8.1 at 8192)
+//   backward  1024 x 128  3.4 / 3.3   2048 x 256  3.7 / 3.9    4096 x 128  4.3 / 3.5    16384 x 128  8.9 / 4.4
+inline bool route_by_rows(const RouteArgs &p, bool backward) {
+    if (p.top_k > 16 || p.experts > 256) return false;
+    if (backward) return p.tokens > 2048;
+    return !p.bias && p.groups == 1 && p.tokens > (p.experts <= 128 ? 4096 : 8192);
+}
+
 template <typename T, int NE>
 int launch_route_ne(const RouteArgs &p, bool backward, hipStream_t s) {
     // few tokens: one wave per workgroup, so that they spread over the CUs
@@ -658,8 +832,22 @@ int launch_route_ne(const RouteArgs &p, bool backward, hipStream_t s) {
     }
     return launched();
 }
+// NE: 16 experts each.
+template <typename T, int NE>
+int launch_route_rows(const RouteArgs &p, bool backward, hipStream_t s) {
+    const int per = 4 * kRouteWaves;
+    const dim3 grid((unsigned)((p.tokens + per - 1) / per)), block(64 * kRouteWaves);
+    if (backward) hipLaunchKernelGGL((route_backward_rows_kernel<T, NE>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((route_rows_kernel<T, NE, sizeof(T) == 2 ? kByBf16 : kByFp32>), grid, block, 0, s, p);
+    return launched();
+}
 template <typename T>
 int launch_route_type(const RouteArgs &p, bool backward, hipStream_t s) {
+    if (route_by_rows(p, backward)) {
+        if (p.experts <= 64) return launch_route_rows<T, 4>(p, backward, s);
+        if (p.experts <= 128) return launch_route_rows<T, 8>(p, backward, s);
+        return launch_route_rows<T, 16>(p, backward, s);
+    }
     if (p.experts <= 64) return launch_route_ne<T, 1>(p, backward, s);
     if (p.experts <= 128) return launch_route_ne<T, 2>(p, backward, s);
     if (p.experts <= 256) return launch_route_ne<T, 4>(p, backward, s);

@@ -314,3 +314,44 @@ def test_graph_replays_the_layer(tokens):
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(4097, 1, 1), (4098, 8, 8), (4099, 60, 4), (4097, 64, 16), (4101, 100, 6),
+                                                  (4103, 128, 8), (8193, 129, 3), (8194, 256, 8), (8193, 250, 17)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_route_many_tokens(tokens, experts, top_k, dtype):
+    """Four tokens share a wave: token counts that leave rows of lanes empty, and masks and ties in some."""
+    x, gen = random_logits(tokens, experts, dtype, tokens + experts)
+    x[5] = float("-inf")
+    x[6] = 1.25
+    x[tokens - 1, experts // 2:] = float("-inf")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            check_route(x, top_k, score, renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(2051, 8, 2), (2050, 60, 4), (2049, 128, 8), (3001, 256, 16), (2053, 250, 5)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_route_backward_many_tokens(tokens, experts, top_k, dtype):
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            test_route_backward(tokens, experts, top_k, dtype, score, renorm)
+
+
+def test_route_backward_many_tokens_masked():
+    """Masked rows and ids outside the experts, among many tokens: the same values as a few at a time."""
+    x, gen = random_logits(2500, 96, torch.float32, 12)
+    x[7] = float("-inf")
+    x[11, 3:] = float("-inf")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            ids, _ = qf8.route_experts(x, 5, score=SCORE[score], renorm=renorm)
+            ids[13, 2], ids[14, 0] = -1, 96
+            dw = torch.randn(2500, 5, generator=gen, device="cuda")
+            got = qf8.route_experts_backward(x, ids, dw, score=SCORE[score], renorm=renorm)
+            few = torch.cat([qf8.route_experts_backward(x[i:i + 500].contiguous(), ids[i:i + 500].contiguous(),
+                                                        dw[i:i + 500].contiguous(), score=SCORE[score], renorm=renorm)
+                             for i in range(0, 2500, 500)])
+            # sums of at most 96 terms in fp64, in another order, then one rounding each
+            tol = few.abs().double() * 2.0 ** -23 + 2.0 ** -45 * dw.abs().double().max(dim=1, keepdim=True)[0]
+            assert bool(((got.double() - few.double()).abs() <= tol).all()) and bool(torch.isfinite(got).all())
