@@ -506,7 +506,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_rows_kernel(R
 // places. Larger ones: order_count_kernel leaves every workgroup's counts, then each workgroup of
 // order_place_kernel sums the counts of those before it and places its own choices. The rank of a
 // choice among equal ones of its wave is a population count of the lanes that ballots of the
-// expert's bits leave; nothing depends on the order of atomics (they only count).
+// expert's bits leave; nothing depends on the order of atomics (they only count). Latency bound: 131072
+// choices of 128 experts take 2.8 + 11.4 us (1.6 MB in and out), 512 of 256 in one workgroup 4.6 us.
 constexpr int kOrderThreads = 1024, kOrderWaves = kOrderThreads / 64;
 constexpr int kOrderOne = 4096;                        // choices up to which one workgroup does all
 constexpr int kOrderGroups = 256;                      // workgroups at most: each reads the counts of all
@@ -645,7 +646,8 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs p)
 // ---- the weighted sum ---------------------------------------------------------------------------
 //
 // y[t] = sum_j weights[t][j] x[slots[t][j]], in fp32, in the order of j, rounded once. Bound by the
-// rows of x: every thread keeps the 16-byte pieces of all its top_k rows in flight.
+// rows of x: every thread keeps the 16-byte pieces of all its top_k rows in flight. 8192 x 8 rows of 4096
+// BF16: 131 us, 4.6 TB/s (a copy of 2 GiB 4.9); the gradients below 278 us, 4.4 TB/s.
 template <typename T> struct Piece;                    // 16 bytes as fp32 values
 template <> struct Piece<uint16_t> {
     static constexpr int N = 8;

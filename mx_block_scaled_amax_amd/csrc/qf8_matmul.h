@@ -2,7 +2,7 @@
 //
 //   y[i][j] = sum over groups g of 128 along k of  (sum_{k in g} a[i][k] * b[j][k]) / (Sa[i][g] * Sb(j, g))
 //
-// where a, b are the values of the codes and a group scale S holds fl(x * S) in its codes. Three ways
+// where a, b are the values of the codes and a group scale S holds fl(x * S) in its codes. Four ways
 // to form it (kMath*):
 //   kMathFp8    one 16x16x128 FP8 MFMA covers exactly one group of k; its result is the group's
 //               partial sum, and what is left per group and element is one fp32 FMA with the
@@ -534,9 +534,10 @@ struct ScaleLoads {
 
 // BM x BN outputs per workgroup, WM x WN waves. Operand tiles of 128 bytes of k go straight from
 // memory to LDS into a ring of D stages: the loads of step s + D - 1 are issued under the products of
-// step s and waited for by count, with one barrier a step. Many workgroups hide each other's
-// latency with D = 2; a grid of about one workgroup per CU needs a deep ring (64 x 128 with D = 6 keeps
-// 120 KB in flight).
+// step s and waited for by count, with one barrier a step. Two workgroups share a CU and fill each
+// other's waits. At one a CU (1024 x 4096 x 4096 in 128 x 128 tiles, 33 us) a step of 0.85 us holds 0.25
+// us of products; a ring of 4 or 6 stages, twice the waves, or reading the next step's fragments a step
+// ahead gave nothing or lost up to 14%.
 //
 // LDS tiles of rows along k (a, and b unless KN): 128-byte rows of eight 16-byte chunks, chunk c of
 // row r at position c ^ swizzle(r). The lanes of the load fetch the permuted chunk, which stays
@@ -820,7 +821,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 //
 // so on every SIMD one wave feeds the matrix core while the other reads. In the plain form of the
 // tile both waves of a SIMD wait for the same barrier and the same reads: the matrix core was busy
-// 40% of the time on 8192 x 7168 x 18432 (1143 us).
+// 40% of the time on 8192 x 7168 x 18432 (1143 us). Now it is busy 47% (1054 us, 2.05 PFLOP/s): a phase
+// takes 910 cycles, 770 with exponents in place of the FMAs, for 512 of products. Without its loads it
+// takes 705 and 585, with loads that always hit L2 801 and 613, but at 1.6-1.7 GHz for 1.8-1.9: the card
+// is at its power limit, so cycles saved come back as time by half only.
 // Loads go to LDS as soon as a region is free in both groups: P2 of step s loads b, a's first halves
 // and a column of scales for step s + 2 (7 loads a wave), P0 loads a's second halves for step
 // s + 1 (2 loads); each has five to six phases to arrive and is waited for by count (9 newer loads may be in
