@@ -531,11 +531,20 @@ def _need(t, name, dtype, shape=None):
     return t.shape
 
 
-def _place(t, shape, dtype, like, name):
-    """The given output, checked, or a new one beside `like`. (new_empty with plain sizes takes 1.2 us,
-    torch.empty 1.7; a decoding step's calls are bound by the host.)"""
+def _fresh(like, shape, dtype, stream):
+    """A new tensor beside `like`, from the memory of the stream that will write it: another stream's may
+    still have work pending on it. (new_empty with plain sizes takes 1.2 us, torch.empty 1.7; a decoding
+    step's calls are bound by the host.)"""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return like.new_empty(*shape, dtype=dtype)
+    return like.new_empty(*shape) if like.dtype == dtype else like.new_empty(*shape, dtype=dtype)
+
+
+def _place(t, shape, dtype, like, name, stream):
+    """The given output, checked, or a new one."""
     if t is None:
-        return like.new_empty(*shape) if like.dtype == dtype else like.new_empty(*shape, dtype=dtype)
+        return _fresh(like, shape, dtype, stream)
     _need(t, name, dtype, shape)
     return t
 
@@ -590,11 +599,11 @@ def matmul_block(a, sa, b, sb, fmt_a, fmt_b, kind=WEIGHT_NK, pow2_scales=False, 
     _need(sa, "sa", torch.float32, (m, -(-k // 128)))
     _need(sb, "sb", torch.float32, _scale_shape(kind, n, k))
     code = _out_code(out_dtype)
-    out = _place(out, (m, n), out_dtype, a, "out")
+    out = _place(out, (m, n), out_dtype, a, "out", stream)
     lib = _load()
     if ws is None:
         need = _size_of("matmul_block_workspace_bytes", m, n, k, kind, code)
-        ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
+        ws = _fresh(a, (need,), torch.uint8, stream) if need else None
     _check(lib.matmul_block(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), m, n, k, fmt_a, fmt_b, kind,
                             FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code, _address(ws),
                             0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, a)), "matmul_block")
@@ -617,7 +626,7 @@ def matmul_block_experts(a, sa, b, sb, offsets, fmt_a, fmt_b, kind=WEIGHT_NK, ro
     _need(offsets, "offsets", torch.int32, (experts + 1,))
     nrows = tokens if rows is None else _need(rows, "rows", torch.int32, 1)[0]
     code = _out_code(out_dtype)
-    out = _place(out, (nrows, n), out_dtype, a, "out")
+    out = _place(out, (nrows, n), out_dtype, a, "out", stream)
     _check(_load().matmul_block_experts(a.data_ptr(), sa.data_ptr(), tokens, b.data_ptr(), sb.data_ptr(),
                                         offsets.data_ptr(), experts, _address(rows), nrows, n, k, fmt_a, fmt_b, kind,
                                         FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code,
@@ -638,7 +647,7 @@ def matmul_block_experts_wgrad(at, sat, bt, sbt, offsets, fmt_a, fmt_b, pow2_sca
     _need(sbt, "sbt", torch.float32, (n, -(-nrows // 128)))
     experts = _need(offsets, "offsets", torch.int32, 1)[0] - 1
     code = _out_code(out_dtype)
-    out = _place(out, (experts, m, n), out_dtype, at, "out")
+    out = _place(out, (experts, m, n), out_dtype, at, "out", stream)
     _check(_load().matmul_block_experts_wgrad(at.data_ptr(), sat.data_ptr(), bt.data_ptr(), sbt.data_ptr(),
                                               offsets.data_ptr(), experts, nrows, m, n, fmt_a, fmt_b,
                                               FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code,
@@ -658,8 +667,8 @@ def route_experts(logits, top_k, score=SCORE_SOFTMAX, bias=None, groups=1, top_g
     tokens, experts = _need(logits, "logits", logits.dtype, 2)
     if bias is not None:
         _need(bias, "bias", torch.float32, (experts,))
-    ids = _place(ids, (tokens, top_k), torch.int32, logits, "ids")
-    weights = _place(weights, (tokens, top_k), torch.float32, logits, "weights")
+    ids = _place(ids, (tokens, top_k), torch.int32, logits, "ids", stream)
+    weights = _place(weights, (tokens, top_k), torch.float32, logits, "weights", stream)
     _check(_load().route_experts(logits.data_ptr(), dtype, tokens, experts, top_k, score, _address(bias), groups,
                                  top_groups, int(renorm), scale, ids.data_ptr(), weights.data_ptr(),
                                  _stream_of(stream, logits)), "route_experts")
@@ -675,7 +684,7 @@ def route_experts_backward(logits, ids, dweights, score=SCORE_SOFTMAX, renorm=Tr
     if t != tokens:
         raise ValueError(f"ids must have {tokens} rows, got {t}")
     _need(dweights, "dweights", torch.float32, (tokens, top_k))
-    dlogits = _place(dlogits, (tokens, experts), logits.dtype, logits, "dlogits")
+    dlogits = _place(dlogits, (tokens, experts), logits.dtype, logits, "dlogits", stream)
     _check(_load().route_experts_backward(logits.data_ptr(), dtype, tokens, experts, ids.data_ptr(), dweights.data_ptr(),
                                           top_k, score, int(renorm), scale, dlogits.data_ptr(),
                                           _stream_of(stream, logits)), "route_experts_backward")
@@ -689,12 +698,12 @@ def order_experts(ids, experts, align=1, offsets=None, rows=None, slots=None, ws
     tokens, top_k = _need(ids, "ids", torch.int32, 2)
     lib = _load()
     nrows = _size_of("order_experts_rows", tokens, top_k, experts, align) if rows is None else rows.numel()
-    offsets = _place(offsets, (experts + 1,), torch.int32, ids, "offsets")
-    rows = _place(rows, (nrows,), torch.int32, ids, "rows")
-    slots = _place(slots, (tokens, top_k), torch.int32, ids, "slots")
+    offsets = _place(offsets, (experts + 1,), torch.int32, ids, "offsets", stream)
+    rows = _place(rows, (nrows,), torch.int32, ids, "rows", stream)
+    slots = _place(slots, (tokens, top_k), torch.int32, ids, "slots", stream)
     if ws is None:
         need = _size_of("order_experts_workspace_bytes", tokens, top_k, experts)
-        ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+        ws = _fresh(ids, (need,), torch.uint8, stream) if need else None
     _check(lib.order_experts(ids.data_ptr(), tokens, top_k, experts, align, offsets.data_ptr(), rows.data_ptr(), nrows,
                              slots.data_ptr(), _address(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                              _stream_of(stream, ids)), "order_experts")
@@ -708,7 +717,7 @@ def combine_experts(x, weights, slots, y=None, stream=None):
     nrows, dim = _need(x, "x", x.dtype, 2)
     tokens, top_k = _need(slots, "slots", torch.int32, 2)
     _need(weights, "weights", torch.float32, (tokens, top_k))
-    y = _place(y, (tokens, dim), x.dtype, x, "y")
+    y = _place(y, (tokens, dim), x.dtype, x, "y", stream)
     _check(_load().combine_experts(x.data_ptr(), dtype, nrows, dim, weights.data_ptr(), slots.data_ptr(), tokens, top_k,
                                    y.data_ptr(), _stream_of(stream, x)), "combine_experts")
     return y
@@ -723,8 +732,8 @@ def combine_experts_backward(dy, x, weights, slots, rows, dx=None, dweights=None
     _need(weights, "weights", torch.float32, (tokens, top_k))
     _need(dy, "dy", x.dtype, (tokens, dim))
     _need(rows, "rows", torch.int32, (nrows,))
-    dx = _place(dx, (nrows, dim), x.dtype, x, "dx")
-    dweights = _place(dweights, (tokens, top_k), torch.float32, x, "dweights")
+    dx = _place(dx, (nrows, dim), x.dtype, x, "dx", stream)
+    dweights = _place(dweights, (tokens, top_k), torch.float32, x, "dweights", stream)
     _check(_load().combine_experts_backward(dy.data_ptr(), x.data_ptr(), dtype, nrows, dim, weights.data_ptr(),
                                             slots.data_ptr(), rows.data_ptr(), tokens, top_k, dx.data_ptr(),
                                             dweights.data_ptr(), _stream_of(stream, x)), "combine_experts_backward")

@@ -372,3 +372,32 @@ def test_infinities_in_last_rows(rows, pow2):
     bad = ~torch.isfinite(y)
     assert bool(bad[m - 1].all())
     assert int(bad[:m - 1].sum()) == 0
+
+
+def test_outputs_belong_to_the_given_stream():
+    """With stream= the outputs and the workspace come from that stream's memory: a block that the current
+    stream has freed, but still has work pending on, is not taken."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(31)
+    m, n, k = 24, 1024, 8192                                   # split along k: a workspace too
+    a, sa = codes(gen, (m, k), "e4m3"), scales(gen, (m, k // 128), False)
+    b, sb, _ = operands(gen, "nk", n, k, "e4m3", False)
+    args = (a, sa, b, sb, qf8.E4M3, qf8.E4M3)
+    x = torch.randn(64, 4096, generator=gen, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(0, 8, (1500, 4), generator=gen, device="cuda", dtype=torch.int32)
+    slots = torch.randint(0, 64, (32, 2), generator=gen, device="cuda", dtype=torch.int32)
+    w = torch.rand(32, 2, generator=gen, device="cuda")
+    calls = [lambda s: (qf8.matmul_block(*args, stream=s),), lambda s: qf8.order_experts(ids, 8, stream=s),
+             lambda s: (qf8.combine_experts(x, w, slots, stream=s),)]
+    side = torch.cuda.Stream()
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        old = [torch.empty_like(t) for t in want for _ in range(4)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        for t in old:
+            t.fill_(7)
+        del t, old
+        got = call(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, t) for g, t in zip(got, want))
