@@ -406,8 +406,9 @@ qf8_status matmul_block_experts_wgrad(const uint8_t *at, const float *sat, const
  * Scores of the experts (softmax over the row or sigmoid, fp64 from the logits) and the choice of
  * top_k of them per token: choice = score + bias[e] (bias nullable fp32, for balance); with groups > 1
  * the experts are groups of experts/groups neighbours, a group is worth the sum of its two best
- * choices, and only the experts of the best top_groups groups can be chosen. Equal values: the lower
- * index first. ids [tokens][top_k] come in falling order of the choice, weights [tokens][top_k] are
+ * choices, and only the experts of the best top_groups groups can be chosen. Without bias and groups the
+ * logits themselves are compared: they order the scores, also where fp64 scores are equal. Equal values: the
+ * lower index first. ids [tokens][top_k] come in falling order of the choice, weights [tokens][top_k] are
  * scale * score, with renorm divided by the sum of the chosen scores (0 if that sum is 0).
  * A logit of -Inf or NaN has score 0 and comes after every number; +Inf reads as the largest finite
  * value; a row without finite logits gets the lowest indices and, with softmax, weights 0.
