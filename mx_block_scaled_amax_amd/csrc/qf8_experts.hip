@@ -507,7 +507,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_rows_kernel(R
 // order_place_kernel sums the counts of those before it and places its own choices. The rank of a
 // choice among equal ones of its wave is a population count of the lanes that ballots of the
 // expert's bits leave; nothing depends on the order of atomics (they only count). Latency bound: 131072
-// choices of 128 experts take 2.8 + 11.4 us (1.6 MB in and out), 512 of 256 in one workgroup 4.6 us.
+// choices of 128 experts take 2.8 + 7.5 us (1.6 MB in and out), 512 of 256 in one workgroup 4.6 us. Padding
+// written by one thread an expert and a 64-bit division for each choice had cost 3.9 us more.
 constexpr int kOrderThreads = 1024, kOrderWaves = kOrderThreads / 64;
 constexpr int kOrderOne = 4096;                        // choices up to which one workgroup does all
 constexpr int kOrderGroups = 256;                      // workgroups at most: each reads the counts of all
@@ -534,6 +535,7 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs p)
     __shared__ int count[kMaxExperts];                 // choices of each expert
     __shared__ int next[kMaxExperts];                  // next free row of each expert, for this workgroup
     __shared__ int scan[kOrderWaves];
+    __shared__ int pad[2][kMaxExperts];                // padding rows of each expert
     __shared__ int16_t rank[kOrderWaves * kMaxExperts];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int64_t lo = ONE ? 0 : (int64_t)blockIdx.x * p.chunk;
@@ -597,8 +599,13 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs p)
     // rows that hold no choice: the padding of the experts, and what follows the last one
     int end = 0;
     for (int w = 0; w < kOrderWaves; ++w) end += scan[w];
-    if (t < p.experts && t % gridDim.x == blockIdx.x)
-        for (int r = first + mine; r < first + padded && r < p.nrows; ++r) p.rows[r] = -1;
+    if (t < p.experts) {
+        pad[0][t] = first + mine;
+        pad[1][t] = first + padded;
+    }
+    __syncthreads();
+    for (int e = blockIdx.x * kOrderWaves + wave; e < p.experts; e += gridDim.x * kOrderWaves)
+        for (int r = pad[0][e] + lane; r < pad[1][e] && r < p.nrows; r += 64) p.rows[r] = -1;
     for (int64_t r = end + (int64_t)blockIdx.x * kOrderThreads + t; r < p.nrows; r += (int64_t)gridDim.x * kOrderThreads)
         p.rows[r] = -1;
 
@@ -633,7 +640,7 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs p)
             int slot = -1;
             if (ok) {
                 slot = next[e] + rank[wave * p.experts + e] + before_in_wave;
-                if (slot < p.nrows) p.rows[slot] = (int)(i / p.top_k);
+                if (slot < p.nrows) p.rows[slot] = (int)((uint32_t)i / (uint32_t)p.top_k);   // fewer than 2^31 choices
                 else slot = -1;
             }
             p.slots[i] = slot;
