@@ -508,7 +508,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_rows_kernel(R
 // choice among equal ones of its wave is a population count of the lanes that ballots of the
 // expert's bits leave; nothing depends on the order of atomics (they only count). Latency bound: 131072
 // choices of 128 experts take 2.8 + 7.5 us (1.6 MB in and out), 512 of 256 in one workgroup 4.6 us. Padding
-// written by one thread an expert and a 64-bit division for each choice had cost 3.9 us more.
+// written by one thread an expert, where 16 do it now, and a 64-bit division for each choice had cost 3.9 us more.
 constexpr int kOrderThreads = 1024, kOrderWaves = kOrderThreads / 64;
 constexpr int kOrderOne = 4096;                        // choices up to which one workgroup does all
 constexpr int kOrderGroups = 256;                      // workgroups at most: each reads the counts of all
@@ -599,13 +599,15 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs p)
     // rows that hold no choice: the padding of the experts, and what follows the last one
     int end = 0;
     for (int w = 0; w < kOrderWaves; ++w) end += scan[w];
-    if (t < p.experts) {
-        pad[0][t] = first + mine;
-        pad[1][t] = first + padded;
+    if (p.align > 1) {
+        if (t < p.experts) {
+            pad[0][t] = first + mine;
+            pad[1][t] = first + padded;
+        }
+        __syncthreads();
+        for (int e = blockIdx.x * (kOrderThreads / 16) + t / 16; e < p.experts; e += gridDim.x * (kOrderThreads / 16))
+            for (int r = pad[0][e] + t % 16; r < pad[1][e] && r < p.nrows; r += 16) p.rows[r] = -1;
     }
-    __syncthreads();
-    for (int e = blockIdx.x * kOrderWaves + wave; e < p.experts; e += gridDim.x * kOrderWaves)
-        for (int r = pad[0][e] + lane; r < pad[1][e] && r < p.nrows; r += 64) p.rows[r] = -1;
     for (int64_t r = end + (int64_t)blockIdx.x * kOrderThreads + t; r < p.nrows; r += (int64_t)gridDim.x * kOrderThreads)
         p.rows[r] = -1;
 
