@@ -507,7 +507,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_rows_kernel(R
 // order_place_kernel sums the counts of those before it and places its own choices. The rank of a
 // choice among equal ones of its wave is a population count of the lanes that ballots of the
 // expert's bits leave; nothing depends on the order of atomics (they only count). Latency bound: 131072
-// choices of 128 experts take 2.8 + 7.5 us (1.6 MB in and out), 512 of 256 in one workgroup 4.6 us. Padding
+// choices of 128 experts take 2.9 + 7.7 us (1.6 MB in and out), 512 of 256 in one workgroup 4.7 us. Padding
 // written by one thread an expert, where 16 do it now, and a 64-bit division for each choice had cost 3.9 us more.
 constexpr int kOrderThreads = 1024, kOrderWaves = kOrderThreads / 64;
 constexpr int kOrderOne = 4096;                        // choices up to which one workgroup does all
