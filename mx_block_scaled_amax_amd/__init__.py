@@ -555,6 +555,14 @@ def _size_of(name, *args):
     return getattr(_load(), name)(*args)
 
 
+def _workspace(ws, like, stream, name, *sizes):
+    """The given workspace, checked, or a new one of the size that the library names; None for none."""
+    if ws is not None:
+        return _dev_tensor(ws, "ws")
+    need = _size_of(name, *sizes)
+    return _fresh(like, (need,), torch.uint8, stream) if need else None
+
+
 def _address(t):
     return None if t is None else t.data_ptr()
 
@@ -600,13 +608,10 @@ def matmul_block(a, sa, b, sb, fmt_a, fmt_b, kind=WEIGHT_NK, pow2_scales=False, 
     _need(sb, "sb", torch.float32, _scale_shape(kind, n, k))
     code = _out_code(out_dtype)
     out = _place(out, (m, n), out_dtype, a, "out", stream)
-    lib = _load()
-    if ws is None:
-        need = _size_of("matmul_block_workspace_bytes", m, n, k, kind, code)
-        ws = _fresh(a, (need,), torch.uint8, stream) if need else None
-    _check(lib.matmul_block(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), m, n, k, fmt_a, fmt_b, kind,
-                            FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code, _address(ws),
-                            0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, a)), "matmul_block")
+    ws = _workspace(ws, a, stream, "matmul_block_workspace_bytes", m, n, k, kind, code)
+    _check(_load().matmul_block(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), m, n, k, fmt_a, fmt_b, kind,
+                                FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code, _address(ws),
+                                0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, a)), "matmul_block")
     return out
 
 
@@ -696,17 +701,14 @@ def order_experts(ids, experts, align=1, offsets=None, rows=None, slots=None, ws
     each row, -1 for padding; every expert starts at a multiple of align), slots [tokens][top_k] (the
     row of each choice). All int32; nothing is read back to the host."""
     tokens, top_k = _need(ids, "ids", torch.int32, 2)
-    lib = _load()
     nrows = _size_of("order_experts_rows", tokens, top_k, experts, align) if rows is None else rows.numel()
     offsets = _place(offsets, (experts + 1,), torch.int32, ids, "offsets", stream)
     rows = _place(rows, (nrows,), torch.int32, ids, "rows", stream)
     slots = _place(slots, (tokens, top_k), torch.int32, ids, "slots", stream)
-    if ws is None:
-        need = _size_of("order_experts_workspace_bytes", tokens, top_k, experts)
-        ws = _fresh(ids, (need,), torch.uint8, stream) if need else None
-    _check(lib.order_experts(ids.data_ptr(), tokens, top_k, experts, align, offsets.data_ptr(), rows.data_ptr(), nrows,
-                             slots.data_ptr(), _address(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                             _stream_of(stream, ids)), "order_experts")
+    ws = _workspace(ws, ids, stream, "order_experts_workspace_bytes", tokens, top_k, experts)
+    _check(_load().order_experts(ids.data_ptr(), tokens, top_k, experts, align, offsets.data_ptr(), rows.data_ptr(), nrows,
+                                 slots.data_ptr(), _address(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                 _stream_of(stream, ids)), "order_experts")
     return offsets, rows, slots
 
 
