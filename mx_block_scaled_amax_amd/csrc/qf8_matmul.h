@@ -216,14 +216,17 @@ __device__ __forceinline__ void panel_order(uint32_t t, uint32_t tm, uint32_t tn
 }
 
 // Row tiles of every expert, found by each wave from the offsets: expert e owns rows
-// [offsets[e], offsets[e+1]) and ceil(rows / bm) tiles; the rows after the last expert are one more
-// stretch, of zeros. order(total) maps the number of row tiles to the one whose place is wanted, < 0: none.
+// [offsets[e], offsets[e+1]) and ceil(rows / bm) tiles; the rows before the first expert and after the last
+// are two more stretches, of zeros. order(total) maps the number of row tiles to the one whose place is
+// wanted, < 0: none.
 template <typename Order>
 __device__ __forceinline__ bool find_row_tile(const int32_t *offsets, int experts, int64_t nrows, int bm, Order order,
                                               TilePlace &pl) {
     const int lane = threadIdx.x & 63;
     int64_t lo = 0, hi = 0;
-    int c = 0, first = 0, total = 0;
+    const int64_t start = offsets[0] < 0 ? 0 : offsets[0] > nrows ? nrows : offsets[0];
+    const int lead = (int)((uint32_t)(start + bm - 1) / (uint32_t)bm);   // tiles before the first expert
+    int c = 0, first = 0, total = lead;
     auto stretch = [&](int e0) {                         // those of 64 experts, a lane each
         const int e = e0 + lane;
         lo = hi = 0;
@@ -249,8 +252,14 @@ __device__ __forceinline__ bool find_row_tile(const int32_t *offsets, int expert
     for (int e0 = 0; e0 <= experts; e0 += 64) stretch(e0);
     const int want = order((uint32_t)total);
     if (want < 0) return false;
+    if (want < lead) {
+        pl.row0 = (int64_t)want * bm;
+        pl.rows = start - pl.row0 < bm ? (int)(start - pl.row0) : bm;
+        pl.expert = -1;
+        return true;
+    }
     const bool again = experts >= 64;                    // the lanes hold the last stretch of several
-    total = 0;
+    total = lead;
     for (int e0 = 0;; e0 += 64) {
         if (again) stretch(e0);
         const uint64_t hit = __ballot(want >= first && want < first + c);

@@ -141,7 +141,8 @@ int launch_matmul(const MatmulArgs &args, int fmt_a, int fmt_b, int kind, int po
         const double rows = (double)p.m / t.bm + 0.5 * used;
         return (rows > used ? rows : used) * (double)((p.n + t.bn - 1) / t.bn);
     });
-    const int64_t tm = p.m / sizes[pl.size].bm + p.experts + 1, tn = (p.n + sizes[pl.size].bn - 1) / sizes[pl.size].bn;
+    // the experts and the rows before and after them: each stretch may end inside a tile
+    const int64_t tm = p.m / sizes[pl.size].bm + p.experts + 2, tn = (p.n + sizes[pl.size].bn - 1) / sizes[pl.size].bn;
     return launch_by_format(p, fmt_a, fmt_b, kind, math, pl.size, tm * tn, s);
 }
 
