@@ -531,6 +531,14 @@ def _need(t, name, dtype, shape=None):
     return t.shape
 
 
+def _one_device(t, *others):
+    """Refuses tensors of another device than t's: the kernel would read their addresses on its own."""
+    device = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != device:
+            raise ValueError(f"all tensors must be on one device, got cuda:{device} and cuda:{o.get_device()}")
+
+
 def _fresh(like, shape, dtype, stream):
     """A new tensor beside `like`, from the memory of the stream that will write it: another stream's may
     still have work pending on it. (new_empty with plain sizes takes 1.2 us, torch.empty 1.7; a decoding
@@ -609,6 +617,7 @@ def matmul_block(a, sa, b, sb, fmt_a, fmt_b, kind=WEIGHT_NK, pow2_scales=False, 
     code = _out_code(out_dtype)
     out = _place(out, (m, n), out_dtype, a, "out", stream)
     ws = _workspace(ws, a, stream, "matmul_block_workspace_bytes", m, n, k, kind, code)
+    _one_device(a, sa, b, sb, out, ws)
     _check(_load().matmul_block(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), m, n, k, fmt_a, fmt_b, kind,
                                 FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code, _address(ws),
                                 0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, a)), "matmul_block")
@@ -632,6 +641,7 @@ def matmul_block_experts(a, sa, b, sb, offsets, fmt_a, fmt_b, kind=WEIGHT_NK, ro
     nrows = tokens if rows is None else _need(rows, "rows", torch.int32, 1)[0]
     code = _out_code(out_dtype)
     out = _place(out, (nrows, n), out_dtype, a, "out", stream)
+    _one_device(a, sa, b, sb, offsets, rows, out)
     _check(_load().matmul_block_experts(a.data_ptr(), sa.data_ptr(), tokens, b.data_ptr(), sb.data_ptr(),
                                         offsets.data_ptr(), experts, _address(rows), nrows, n, k, fmt_a, fmt_b, kind,
                                         FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code,
@@ -653,6 +663,7 @@ def matmul_block_experts_wgrad(at, sat, bt, sbt, offsets, fmt_a, fmt_b, pow2_sca
     experts = _need(offsets, "offsets", torch.int32, 1)[0] - 1
     code = _out_code(out_dtype)
     out = _place(out, (experts, m, n), out_dtype, at, "out", stream)
+    _one_device(at, sat, bt, sbt, offsets, out)
     _check(_load().matmul_block_experts_wgrad(at.data_ptr(), sat.data_ptr(), bt.data_ptr(), sbt.data_ptr(),
                                               offsets.data_ptr(), experts, nrows, m, n, fmt_a, fmt_b,
                                               FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code,
@@ -674,6 +685,7 @@ def route_experts(logits, top_k, score=SCORE_SOFTMAX, bias=None, groups=1, top_g
         _need(bias, "bias", torch.float32, (experts,))
     ids = _place(ids, (tokens, top_k), torch.int32, logits, "ids", stream)
     weights = _place(weights, (tokens, top_k), torch.float32, logits, "weights", stream)
+    _one_device(logits, bias, ids, weights)
     _check(_load().route_experts(logits.data_ptr(), dtype, tokens, experts, top_k, score, _address(bias), groups,
                                  top_groups, int(renorm), scale, ids.data_ptr(), weights.data_ptr(),
                                  _stream_of(stream, logits)), "route_experts")
@@ -690,6 +702,7 @@ def route_experts_backward(logits, ids, dweights, score=SCORE_SOFTMAX, renorm=Tr
         raise ValueError(f"ids must have {tokens} rows, got {t}")
     _need(dweights, "dweights", torch.float32, (tokens, top_k))
     dlogits = _place(dlogits, (tokens, experts), logits.dtype, logits, "dlogits", stream)
+    _one_device(logits, ids, dweights, dlogits)
     _check(_load().route_experts_backward(logits.data_ptr(), dtype, tokens, experts, ids.data_ptr(), dweights.data_ptr(),
                                           top_k, score, int(renorm), scale, dlogits.data_ptr(),
                                           _stream_of(stream, logits)), "route_experts_backward")
@@ -706,6 +719,7 @@ def order_experts(ids, experts, align=1, offsets=None, rows=None, slots=None, ws
     rows = _place(rows, (nrows,), torch.int32, ids, "rows", stream)
     slots = _place(slots, (tokens, top_k), torch.int32, ids, "slots", stream)
     ws = _workspace(ws, ids, stream, "order_experts_workspace_bytes", tokens, top_k, experts)
+    _one_device(ids, offsets, rows, slots, ws)
     _check(_load().order_experts(ids.data_ptr(), tokens, top_k, experts, align, offsets.data_ptr(), rows.data_ptr(), nrows,
                                  slots.data_ptr(), _address(ws), 0 if ws is None else ws.numel() * ws.element_size(),
                                  _stream_of(stream, ids)), "order_experts")
@@ -720,6 +734,7 @@ def combine_experts(x, weights, slots, y=None, stream=None):
     tokens, top_k = _need(slots, "slots", torch.int32, 2)
     _need(weights, "weights", torch.float32, (tokens, top_k))
     y = _place(y, (tokens, dim), x.dtype, x, "y", stream)
+    _one_device(x, weights, slots, y)
     _check(_load().combine_experts(x.data_ptr(), dtype, nrows, dim, weights.data_ptr(), slots.data_ptr(), tokens, top_k,
                                    y.data_ptr(), _stream_of(stream, x)), "combine_experts")
     return y
@@ -736,6 +751,7 @@ def combine_experts_backward(dy, x, weights, slots, rows, dx=None, dweights=None
     _need(rows, "rows", torch.int32, (nrows,))
     dx = _place(dx, (nrows, dim), x.dtype, x, "dx", stream)
     dweights = _place(dweights, (tokens, top_k), torch.float32, x, "dweights", stream)
+    _one_device(x, dy, weights, slots, rows, dx, dweights)
     _check(_load().combine_experts_backward(dy.data_ptr(), x.data_ptr(), dtype, nrows, dim, weights.data_ptr(),
                                             slots.data_ptr(), rows.data_ptr(), tokens, top_k, dx.data_ptr(),
                                             dweights.data_ptr(), _stream_of(stream, x)), "combine_experts_backward")
