@@ -370,8 +370,9 @@ qf8_status dequantize_nvfp4(const uint8_t *q, const uint8_t *s_blk, const float 
  * flags: QF8_FLAG_POW2_SCALES says that every scale is a power of two; then the exponents of sa and
  * sb alone may be read (the matrix core applies them). A factor 1/Sa * 1/Sb below
  * 2^-126 is held as a subnormal. NaN and Inf codes give what fp32 arithmetic gives.
- * k % 4 == 0, for QF8_WEIGHT_KN also n % 4 == 0; k, n <= 2^22; m < 2^31; k = 0 gives zeros. a, b, y and
- * ws 16-byte aligned, scales 4-byte; y overlaps no input.
+ * k % 4 == 0, for QF8_WEIGHT_KN also n % 4 == 0; k, n <= 2^22; m < 2^31, and no more
+ * output tiles than one launch holds (m < 2^28 serves for n <= 128); k = 0 gives zeros. a, b, y and ws
+ * 16-byte aligned, scales 4-byte; y overlaps no input.
  * ws: matmul_block_workspace_bytes() bytes (0: ws may be NULL): the partial sums of a product whose
  * k is split over workgroups; it needs no initialisation. */
 typedef enum qf8_operand { QF8_WEIGHT_NK = 0, QF8_WEIGHT_KN = 1, QF8_GROUPS_NK = 2 } qf8_operand;
@@ -412,8 +413,8 @@ qf8_status matmul_block_experts_wgrad(const uint8_t *at, const float *sat, const
  * scale * score, with renorm divided by the sum of the chosen scores (0 if that sum is 0).
  * A logit of -Inf or NaN has score 0 and comes after every number; +Inf reads as the largest finite
  * value; a row without finite logits gets the lowest indices and, with softmax, weights 0.
- * experts <= 1024, groups <= 64 and a divisor of experts, top_k <= 64 and <= top_groups * experts /
- * groups. logits [tokens][experts] BF16 or FP32. */
+ * tokens < 2^26, experts <= 1024, groups <= 64 and a divisor of experts, top_k <= 64 and <= top_groups *
+ * experts / groups. logits [tokens][experts] BF16 or FP32. */
 typedef enum qf8_score { QF8_SCORE_SOFTMAX = 0, QF8_SCORE_SIGMOID = 1 } qf8_score;
 
 qf8_status route_experts(const void *logits, qf8_dtype dtype, int64_t tokens, int experts, int top_k, qf8_score score,
@@ -439,13 +440,13 @@ qf8_status order_experts(const int32_t *ids, int64_t tokens, int top_k, int expe
                          int32_t *rows, int64_t nrows, int32_t *slots, void *ws, size_t ws_bytes, void *stream);
 
 /* Weighted sum: y[t] = sum_j weights[t][j] * x[slots[t][j]], in fp32, rounded once to x's type. x
- * [nrows][dim], y [tokens][dim]; a slot outside [0, nrows) adds nothing. */
+ * [nrows][dim], y [tokens][dim]; a slot outside [0, nrows) adds nothing. tokens < 2^24; nrows, dim < 2^31. */
 qf8_status combine_experts(const void *x, qf8_dtype dtype, int64_t nrows, int64_t dim, const float *weights,
                            const int32_t *slots, int64_t tokens, int top_k, void *y, void *stream);
 
 /* Its gradients: dx[slots[t][j]] = weights[t][j] * dy[t] (x's type), dweights[t][j] = dy[t] . x[slots[t][j]]
  * (fp32; 0 for a slot outside [0, nrows)). Rows of dx whose entry of rows [nrows] is no token are zeros;
- * rows and slots are those of one order_experts call. */
+ * rows and slots are those of one order_experts call. tokens + ceil(nrows / 64) < 2^24; dim < 2^31. */
 qf8_status combine_experts_backward(const void *dy, const void *x, qf8_dtype dtype, int64_t nrows, int64_t dim,
                                     const float *weights, const int32_t *slots, const int32_t *rows, int64_t tokens,
                                     int top_k, void *dx, float *dweights, void *stream);

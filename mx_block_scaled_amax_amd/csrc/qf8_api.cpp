@@ -33,6 +33,8 @@ inline bool dims_ok(int64_t rows, int64_t cols) {
 
 inline bool kind_ok(int kind) { return kind >= QF8_WEIGHT_NK && kind <= QF8_GROUPS_NK; }
 inline bool out_ok(int out) { return out == QF8_OUT_BF16 || out == QF8_OUT_FP32; }
+constexpr int64_t kMaxLaunchThreads = (int64_t)1 << 32;      // a launch counts its threads in 32 bits
+constexpr int64_t kMaxRouteTokens = kMaxLaunchThreads / 64;  // one token to a wave
 constexpr int64_t kMaxMatmulDim = 1 << 22;   // keeps every buffer offset of a tile below 2^31
 
 // the sizes a product takes: rows of codes are read as whole dwords
@@ -519,7 +521,7 @@ qf8_status route_experts(const void *logits, qf8_dtype dtype, int64_t tokens, in
                          const float *bias, int groups, int top_groups, int renorm, float scale, int32_t *ids,
                          float *weights, void *stream) {
     if (!dtype_ok(dtype) || (score != QF8_SCORE_SOFTMAX && score != QF8_SCORE_SIGMOID)) return QF8_ERR_ENUM;
-    if (tokens < 0 || tokens >= (int64_t)1 << 31 || experts < 1 || experts > qf8::kMaxExperts || groups < 1 ||
+    if (tokens < 0 || tokens >= kMaxRouteTokens || experts < 1 || experts > qf8::kMaxExperts || groups < 1 ||
         groups > qf8::kMaxExpertGroups || experts % groups != 0 || top_groups < 1 || top_groups > groups || top_k < 1 ||
         top_k > qf8::kMaxTopK || top_k > experts / groups * top_groups)
         return QF8_ERR_SHAPE;
@@ -539,7 +541,7 @@ qf8_status route_experts_backward(const void *logits, qf8_dtype dtype, int64_t t
                                   const float *dweights, int top_k, qf8_score score, int renorm, float scale,
                                   void *dlogits, void *stream) {
     if (!dtype_ok(dtype) || (score != QF8_SCORE_SOFTMAX && score != QF8_SCORE_SIGMOID)) return QF8_ERR_ENUM;
-    if (tokens < 0 || tokens >= (int64_t)1 << 31 || experts < 1 || experts > qf8::kMaxExperts || top_k < 1 ||
+    if (tokens < 0 || tokens >= kMaxRouteTokens || experts < 1 || experts > qf8::kMaxExperts || top_k < 1 ||
         top_k > qf8::kMaxTopK || top_k > experts)
         return QF8_ERR_SHAPE;
     if (tokens == 0) return QF8_OK;
@@ -581,9 +583,10 @@ qf8_status order_experts(const int32_t *ids, int64_t tokens, int top_k, int expe
 }
 
 namespace {
+// A workgroup of 256 threads takes one token.
 int check_combine(qf8_dtype dtype, int64_t nrows, int64_t dim, int64_t tokens, int top_k) {
     if (!dtype_ok(dtype)) return QF8_ERR_ENUM;
-    if (tokens < 0 || tokens >= (int64_t)1 << 30 || nrows < 0 || nrows >= (int64_t)1 << 31 || dim < 0 ||
+    if (tokens < 0 || tokens >= kMaxLaunchThreads / 256 || nrows < 0 || nrows >= (int64_t)1 << 31 || dim < 0 ||
         dim >= (int64_t)1 << 31 || top_k < 1 || top_k > qf8::kMaxTopK)
         return QF8_ERR_SHAPE;
     return QF8_OK;
@@ -608,6 +611,7 @@ qf8_status combine_experts_backward(const void *dy, const void *x, qf8_dtype dty
                                     int top_k, void *dx, float *dweights, void *stream) {
     const int c = check_combine(dtype, nrows, dim, tokens, top_k);
     if (c != QF8_OK) return status_of(c);
+    if (tokens + (nrows + 63) / 64 >= kMaxLaunchThreads / 256) return QF8_ERR_SHAPE;       // and 64 rows for the padding
     if (tokens == 0 && (nrows == 0 || dim == 0)) return QF8_OK;
     if ((tokens > 0 && (!weights || !slots || !dweights || (dim > 0 && !dy))) || (nrows > 0 && (!rows || (dim > 0 && (!x || !dx)))))
         return QF8_ERR_NULL;

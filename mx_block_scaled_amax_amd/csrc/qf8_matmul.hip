@@ -82,7 +82,7 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(const float *parts, in
 }
 
 int launch_by_format(const MatmulArgs &p, int fa, int fb, int kind, int math, int size, int64_t groups, hipStream_t s) {
-    if (groups > 0x7FFFFFFF) return QF8_ERR_SHAPE;       // workgroups are counted in 32 bits
+    if (groups * (size == 0 ? 512 : 256) > 0xFFFFFFFFll) return QF8_ERR_SHAPE;       // a launch counts threads in 32 bits
     if (fa == kE4M3)
         return fb == kE4M3 ? launch_matmul_formats<kE4M3, kE4M3>(p, kind, math, size, groups, s)
                            : launch_matmul_formats<kE4M3, kE5M2>(p, kind, math, size, groups, s);
