@@ -67,12 +67,12 @@ __device__ __forceinline__ float wave_max(float v) {
     return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k);
 }
 
-// Logits as the choice sees them: NaN reads as -Inf (never chosen before a number), +Inf as the
-// largest finite value, and -0 as +0 so that it ties with it.
+// Logits as the choice sees them: NaN reads as -Inf, +Inf as the largest finite value of the logits' type
+// (with which it ties, in the order and in the weights), and -0 as +0 so that it ties with it.
 template <typename T> __device__ __forceinline__ float load_logit(const T *p, int64_t i);
 template <> __device__ __forceinline__ float load_logit<uint16_t>(const uint16_t *p, int64_t i) {
     const float v = __uint_as_float((uint32_t)p[i] << 16);
-    return v != v ? -INFINITY : fminf(v, 3.40282346638528859812e+38f) + 0.0f;
+    return v != v ? -INFINITY : fminf(v, __uint_as_float(0x7F7F0000u)) + 0.0f;
 }
 template <> __device__ __forceinline__ float load_logit<float>(const float *p, int64_t i) {
     const float v = p[i];
