@@ -410,7 +410,8 @@ qf8_status matmul_block_experts_wgrad(const uint8_t *at, const float *sat, const
  * choices, and only the experts of the best top_groups groups can be chosen. Without bias and groups the
  * logits themselves are compared: they order the scores, also where fp64 scores are equal. Equal values: the
  * lower index first. ids [tokens][top_k] come in falling order of the choice, weights [tokens][top_k] are
- * scale * score, with renorm divided by the sum of the chosen scores (0 if that sum is 0).
+ * scale * score, with renorm divided by the sum of the chosen scores (0 if that sum is 0; softmax scores
+ * have their ratios however far they are below the row's largest).
  * A logit of -Inf or NaN has score 0 and comes after every number; +Inf reads as the largest finite
  * value of the logits' type; a row without finite logits gets the lowest indices and, with softmax, weights 0.
  * tokens < 2^26, experts <= 1024, groups <= 64 and a divisor of experts, top_k <= 64 and <= top_groups *

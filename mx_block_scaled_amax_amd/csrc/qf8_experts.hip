@@ -248,14 +248,21 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
     }
 
     // weights of the chosen, in fp64, rounded once
+    const bool have = lane < p.top_k && mine < p.experts;
+    const float x = have ? load_logit(row, mine) : -INFINITY;
+    if (BY == kByScore && softmax && p.renorm) {
+        // bias or groups may choose experts far below the largest logit, whose scores are 0 in fp64 but have
+        // ratios all the same: relative to the largest chosen logit, as in the gradient
+        top = wave_max(x);
+        if (top == -INFINITY) top = 0.0f;
+    }
     double w = 0.0;
-    if (lane < p.top_k && mine < p.experts) {
-        const double x = (double)load_logit(row, mine);
+    if (have) {
         if (softmax) {
-            w = exp(x - (double)top);
+            w = exp((double)x - (double)top);
             if (!p.renorm) w = total > 0.0 ? w / total : 0.0;
         } else {
-            w = sigmoid64(x);
+            w = sigmoid64((double)x);
         }
     }
     if (p.renorm) {

@@ -1,11 +1,12 @@
-"""The choice of experts at the ends of the range."""
+"""The choice of experts at the ends of the range: infinities and largest values, chosen experts whose
+scores underflow."""
 import math
 
 import pytest
 import torch
 
 import mx_block_scaled_amax_amd as qf8
-from test_gpu_experts import SCORE
+from test_gpu_experts import HALF, SCORE
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +29,29 @@ def test_infinity_is_the_largest_value_of_its_type(dtype, tokens, score):
         if score == "softmax":                               # p (g - mean) with p = 1/2 each; a sigmoid is flat there
             want[3], want[9] = 0.25, -0.25
         assert bool((d == want).all()), d[0].tolist()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("low", [-800.0, -30000.0, None])
+def test_weights_of_chosen_experts_whose_scores_underflow(dtype, low):
+    """The bias chooses experts far below the largest logit: softmax scores that underflow have ratios all the
+    same, and the gradient is that of the weights."""
+    low = torch.finfo(dtype).min / 2 if low is None else low
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    x = torch.randn(40, 24, generator=gen, device="cuda")
+    x[:, 12:] = low if abs(low) > 1e6 else low + 2.0 * x[:, 12:]
+    x = x.to(dtype)
+    bias = torch.zeros(24, device="cuda")
+    bias[14:19] = torch.linspace(3.0, 2.0, 5, device="cuda")
+    ids, w = qf8.route_experts(x, 4, bias=bias, scale=1.5)
+    assert bool((ids == torch.arange(14, 18, device="cuda")).all())
+    l = x.double().cpu().requires_grad_()
+    chosen = l.gather(1, ids.long().cpu())
+    want = 1.5 * torch.softmax(chosen, 1)
+    assert bool(((w.double().cpu() - want).abs() <= want * (2.0 ** -24 * 1.01) + 1e-45).all()), w[0].tolist()
+    dw = torch.randn(40, 4, generator=gen, device="cuda")
+    got = qf8.route_experts_backward(x, ids, dw, scale=1.5).double().cpu()
+    (grad,) = torch.autograd.grad(want, l, dw.double().cpu())
+    tol = grad.abs() * HALF[dtype] * 1.01 + 2.0 ** -45 * dw.abs().double().cpu().max(dim=1, keepdim=True)[0]
+    assert bool(((got - grad).abs() <= tol).all())
