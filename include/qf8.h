@@ -412,8 +412,11 @@ qf8_status matmul_block_experts_wgrad(const uint8_t *at, const float *sat, const
  * lower index first. ids [tokens][top_k] come in falling order of the choice, weights [tokens][top_k] are
  * scale * score, with renorm divided by the sum of the chosen scores (0 if that sum is 0; softmax scores
  * have their ratios however far they are below the row's largest).
- * A logit of -Inf or NaN has score 0 and comes after every number; +Inf reads as the largest finite
- * value of the logits' type; a row without finite logits gets the lowest indices and, with softmax, weights 0.
+ * A logit of -Inf or NaN has score 0. Without bias and groups it comes after every number; with them
+ * it is compared by score + bias like the others, that is by bias[e], and can be chosen, with weight 0,
+ * before a number whose score + bias is lower. A bias of -Inf puts an expert after every other (bias holds
+ * no +Inf or NaN). +Inf reads as the largest finite value of the logits' type; a row without finite logits
+ * has equal scores (without bias: the lowest indices) and weights 0.
  * tokens < 2^26, experts <= 1024, groups <= 64 and a divisor of experts, top_k <= 64 and <= top_groups *
  * experts / groups. logits [tokens][experts] BF16 or FP32. */
 typedef enum qf8_score { QF8_SCORE_SOFTMAX = 0, QF8_SCORE_SIGMOID = 1 } qf8_score;

@@ -677,8 +677,9 @@ def route_experts(logits, top_k, score=SCORE_SOFTMAX, bias=None, groups=1, top_g
                   ids=None, weights=None, stream=None):
     """Choice of top_k experts for each token from logits [tokens][experts] (BF16 or FP32). bias:
     float32 [experts], added to the scores for the choice only; groups > 1: only the experts of the
-    best top_groups groups (by the sum of their two best choices). Returns (ids int32, weights
-    float32), both [tokens][top_k], in falling order of the choice."""
+    best top_groups groups (by the sum of their two best choices). A logit of -Inf or NaN has score 0:
+    it comes last without bias and groups, and is compared by 0 + bias with them (a bias of -Inf shuts an
+    expert out). Returns (ids int32, weights float32), both [tokens][top_k], in falling order of the choice."""
     dtype = _in_code(logits, "logits")
     tokens, experts = _need(logits, "logits", logits.dtype, 2)
     if bias is not None:

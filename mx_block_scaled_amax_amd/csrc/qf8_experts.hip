@@ -95,10 +95,11 @@ __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(
 // One wave per token; lane l holds experts l, l + 64, ... (NE of them). Selection compares either
 // the logits themselves (scores rise with them, so without bias and groups the order is exact) or
 // the scores plus bias in fp64: fp32 scores would tie or swap experts whose scores differ by less
-// than 2^-24, and the chosen indices have to be those of the definition. What is read is 2-4 bytes
-// an expert; the time is that of the top_k rounds of a wave-wide maximum, so a round's key is as small
-// as it can be: BF16 logits and the index in one 32-bit word (no two alike, so the maximum is the
-// choice), FP32 logits in one with ties looked up afterwards, scores in two.
+// than 2^-24, and the chosen indices have to be those of the definition (a masked logit is compared by
+// 0 + bias there, like any score). What is read is 2-4 bytes an expert; the time is that of the top_k
+// rounds of a wave-wide maximum, so a round's key is as small as it can be: BF16 logits and the index in
+// one 32-bit word (no two alike, so the maximum is the choice), FP32 logits in one with ties looked up
+// afterwards, scores in two.
 constexpr int kRouteWaves = 4;
 enum { kByBf16 = 0, kByFp32 = 1, kByScore = 2 };
 

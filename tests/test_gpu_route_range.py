@@ -1,12 +1,12 @@
 """The choice of experts at the ends of the range: infinities and largest values, chosen experts whose
-scores underflow."""
+scores underflow, experts that bias or mask shut out."""
 import math
 
 import pytest
 import torch
 
 import mx_block_scaled_amax_amd as qf8
-from test_gpu_experts import HALF, SCORE
+from test_gpu_experts import HALF, SCORE, check_route, random_logits
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,38 @@ def test_weights_of_chosen_experts_whose_scores_underflow(dtype, low):
     (grad,) = torch.autograd.grad(want, l, dw.double().cpu())
     tol = grad.abs() * HALF[dtype] * 1.01 + 2.0 ** -45 * dw.abs().double().cpu().max(dim=1, keepdim=True)[0]
     assert bool(((got - grad).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_choice_is_score_plus_bias_in_masked_places(score, dtype):
+    """With a bias or groups a masked logit is compared by 0 + bias, as the formula has it; its weight is 0. A
+    bias of -Inf shuts an expert out."""
+    x, _ = random_logits(50, 64, dtype, 77)
+    x[:, 5] = -math.inf
+    x[:, 20] = math.nan
+    x[3, 8:] = -math.inf
+    x[4] = -math.inf
+    bias = torch.linspace(-0.2, 0.2, 64, device="cuda")
+    bias[5] = 5.0
+    ids, w = check_route(x, 6, score, bias=bias)
+    assert bool((ids[:, 0] == 5).all()) and bool((w[:, 0] == 0).all())
+    check_route(x, 6, score, bias=bias, groups=8, top_groups=3)
+    check_route(x, 6, score, groups=8, top_groups=3)
+    bias[[2, 5, 17, 40]] = -math.inf
+    ids, w = check_route(x, 6, score, bias=bias)
+    assert not bool(((ids == 2) | (ids == 5) | (ids == 17) | (ids == 40)).any())
+    ids, w = check_route(x, 6, score, bias=bias, groups=8, top_groups=3)
+    assert not bool(((ids == 2) | (ids == 5) | (ids == 17) | (ids == 40)).any())
+
+
+@pytest.mark.parametrize("tokens", [3, 3000])
+def test_lowest_value_is_a_number(tokens):
+    """Without bias and groups -Inf comes after the type's lowest value, at a higher index too."""
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.full((tokens, 96), -math.inf, dtype=dtype, device="cuda")
+        x[:, 50:53] = torch.finfo(dtype).min
+        x[:, 70] = 0.0
+        for score in ("softmax", "sigmoid"):
+            ids, _ = check_route(x, 5, score)
+            assert ids[tokens - 1].tolist() == [70, 50, 51, 52, 0]
