@@ -789,7 +789,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
                 for (int j = 0; j < FN; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if constexpr (KIND == kGroups) acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e] * sa[i], sbg[j][e], acc[i][j][e]);
+                        // the factor first: part times one far scale alone could leave the range
+                        if constexpr (KIND == kGroups) acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], sa[i] * sbg[j][e], acc[i][j][e]);
                         else acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], sa[i], acc[i][j][e]);
                     }
             };
