@@ -13,7 +13,8 @@
 //   kMathExact  the codes become BF16 (exactly) and go through 32x32x16 BF16 MFMAs, the group's sum
 //               then scaled by an FMA.
 //   kMathExactPow2  the same with power-of-two scales: the conversion to BF16 multiplies by 1/S,
-//               which is still exact, and the sums need no scaling.
+//               which is exact for 1/S of 2^-64 to 2^64, and the sums need no scaling. A tile that meets
+//               another scale is done again as by kMathExact.
 // Why two precisions: the FP8 MFMAs of gfx950 align the products of each 8 neighbours along k to the
 // largest of them and keep 14 bits (measured: beside a product of 2^16 one of 2^3 counts and one of
 // 2^2 is lost; 1.4e-5 relative error on normal data, for the 16x16x32 form too), while the BF16
@@ -120,6 +121,11 @@ template <int MATH>
 __device__ __forceinline__ float inverse_scale(float s) {
     if constexpr (MATH == kMathE8m0) return __uint_as_float(umax(254u - umin((__float_as_uint(s) >> 23) & 0xFFu, 254u), 0u));
     else return 1.0f / s;
+}
+
+// 2^-64 <= f <= 2^64: BF16 holds any code (2^-16 to 2^16) times f in full.
+__device__ __forceinline__ bool near_one(float f) {
+    return __float_as_uint(f) - 0x1F800000u <= 0x5F800000u - 0x1F800000u;
 }
 
 template <int FA, int FB>
@@ -560,7 +566,7 @@ struct ScaleLoads {
 template <int FA, int FB, int KIND, int MATH, int BM, int BN, int WM, int WN, int D>
 __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs p) {
     constexpr int NT = 64 * WM * WN, TM = BM / WM, TN = BN / WN;
-    constexpr bool POW2 = MATH == kMathE8m0 || MATH == kMathExactPow2, EXACT = MATH >= kMathExact;
+    constexpr bool POW2 = MATH == kMathE8m0, EXACT = MATH >= kMathExact;
     constexpr int FR = EXACT ? 32 : 16, FM = TM / FR, FN = TN / FR;      // fragments
     constexpr int kA = BM * kBK, kB = BN * kBK, kStage = kA + kB;
     typedef TileLoads<KIND, EXACT, BM, BN, TN, NT> Loads;
@@ -580,245 +586,268 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
     const int kend = (int)(pl.k1 - pl.k0);
     const int gk = (int)((p.k + kBK - 1) / kBK), g0 = (int)(pl.k0 / kBK);
 
-    Loads ld;
-    ld.init(p, pl, steps, t);
-    Scales ls;
-    if (steps) ls.init(p, pl, t, wave, gk, g0);
-
     constexpr int FV = FR * FR / 64;                     // values of a fragment in a lane
     typedef float frag __attribute__((ext_vector_type(FV)));
     frag acc[FM][FN];
+    // FOLD: the scales go into the operands. Seldom a scale is too far from 1 for that; the tile is then done again
+    // without. (A choice at each step costs all that folding gains: 525 us for 7168 x 4096 x 8192 in FP32, as without
+    // folding, against 465.)
+    bool far = false;
+    auto all_steps = [&](auto folded) QF8_INLINE {
+        constexpr bool FOLD = decltype(folded)::value;
+        Loads ld;
+        ld.init(p, pl, steps, t);
+        Scales ls;
+        if (steps) ls.init(p, pl, t, wave, gk, g0);
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = (frag)0.0f;
+            for (int j = 0; j < FN; ++j) acc[i][j] = (frag)0.0f;
 
-    // The loads of step n_load: piece u of LA + LB, then the scales of step n_load + 1. Past the last
-    // step the buffers have length 0: the loads still run, so that counts hold, and leave zeros nobody uses.
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)lds_address(&tiles[0][0])) + (uint32_t)wave * 1024u;
-    const uint32_t lds_raw = __builtin_amdgcn_readfirstlane((int)lds_address(&raw[0][0])) + (uint32_t)wave * 256u;
-    int n_load = 0, n_scale = 0, at_load = 0, at_scale = 0;              // steps, and their places in the rings
-    auto load_scale = [&]() {
-        if (n_scale >= steps) ls.buf.left = 0;
-        lds_dma4(ls.buf.rsrc(), ls.off, lds_raw + (uint32_t)at_scale * NT * 4u);
-        ls.buf.advance(ls.step);
-        ++n_scale;
-        at_scale = at_scale + 1 == D ? 0 : at_scale + 1;
-    };
-    auto load_piece = [&](int u) {
-        const uint32_t at = lds0 + (uint32_t)at_load * kStage;
-        if (u == 0 && n_load >= steps) ld.ba.left = ld.bb.left = 0;
-        if (u < LA) lds_dma16(ld.ba.rsrc(), ld.va[u < LA ? u : 0], at + (uint32_t)u * NT * 16u);
-        else if (u < LT) lds_dma16(ld.bb.rsrc(), ld.vb[u < LA ? 0 : u - LA], at + kA + (uint32_t)(u - LA) * NT * 16u);
-        if (u == LT) {
-            ld.ba.advance(kBK);
-            ld.bb.advance(ld.stepb);
-            load_scale();
-            ++n_load;
-            at_load = at_load + 1 == D ? 0 : at_load + 1;
-        }
-    };
-
-    if (steps) {
-        load_scale();
-#pragma unroll
-        for (int d = 0; d < D - 1; ++d)
-#pragma unroll
-            for (int u = 0; u <= LT; ++u) load_piece(u);
-        wait_vmem_but<(D - 1) * (LT + 1)>();
-        phase_end();
-        inv[0][t] = inverse_scale<MATH>(raw[0][t]);
-    }
-    int at = 0;                                          // stage of step s
-    for (int s = 0; s < steps; ++s) {
-        wait_vmem_but<(D - 2) * (LT + 1)>();
-        phase_end();
-        uint8_t *const ta = tiles[at], *const tb = ta + kA;
-        const float *const sc = inv[s & 1];
-        at = at + 1 == D ? 0 : at + 1;
-        const int krem = kend - s * kBK;
-        if (krem < kBK) {                               // the last step of a k that is no multiple of 128
-#pragma unroll
-            for (int i = 0; i < LA; ++i) {
-                const int id = i * NT + t, row = id >> 3, ch = (id & 7) ^ swizzle(row);
-                uint4 *at = (uint4 *)(ta + 16 * id);
-                if (16 * ch + 16 > krem) *at = keep_bytes(*at, krem - 16 * ch);
+        // The loads of step n_load: piece u of LA + LB, then the scales of step n_load + 1. Past the last
+        // step the buffers have length 0: the loads still run, so that counts hold, and leave zeros nobody uses.
+        const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)lds_address(&tiles[0][0])) + (uint32_t)wave * 1024u;
+        const uint32_t lds_raw = __builtin_amdgcn_readfirstlane((int)lds_address(&raw[0][0])) + (uint32_t)wave * 256u;
+        int n_load = 0, n_scale = 0, at_load = 0, at_scale = 0;              // steps, and their places in the rings
+        auto load_scale = [&]() {
+            if (n_scale >= steps) ls.buf.left = 0;
+            lds_dma4(ls.buf.rsrc(), ls.off, lds_raw + (uint32_t)at_scale * NT * 4u);
+            ls.buf.advance(ls.step);
+            ++n_scale;
+            at_scale = at_scale + 1 == D ? 0 : at_scale + 1;
+        };
+        auto load_piece = [&](int u) {
+            const uint32_t at = lds0 + (uint32_t)at_load * kStage;
+            if (u == 0 && n_load >= steps) ld.ba.left = ld.bb.left = 0;
+            if (u < LA) lds_dma16(ld.ba.rsrc(), ld.va[u < LA ? u : 0], at + (uint32_t)u * NT * 16u);
+            else if (u < LT) lds_dma16(ld.bb.rsrc(), ld.vb[u < LA ? 0 : u - LA], at + kA + (uint32_t)(u - LA) * NT * 16u);
+            if (u == LT) {
+                ld.ba.advance(kBK);
+                ld.bb.advance(ld.stepb);
+                load_scale();
+                ++n_load;
+                at_load = at_load + 1 == D ? 0 : at_load + 1;
             }
+        };
+
+        if (steps) {
+            load_scale();
 #pragma unroll
-            for (int i = 0; i < LB; ++i) {
-                const int id = i * NT + t;
-                uint4 *at = (uint4 *)(tb + 16 * id);
-                if constexpr (KIND == kKN) {
-                    if (id / (BN / 16) >= krem) *at = make_uint4(0, 0, 0, 0);
-                } else {
-                    const int row = id >> 3, ch = (id & 7) ^ swizzle(row);
+            for (int d = 0; d < D - 1; ++d)
+#pragma unroll
+                for (int u = 0; u <= LT; ++u) load_piece(u);
+            wait_vmem_but<(D - 1) * (LT + 1)>();
+            phase_end();
+            const float f = inverse_scale<MATH>(raw[0][t]);
+            if constexpr (EXACT && FOLD) far = !near_one(f);
+            inv[0][t] = f;
+        }
+        int at = 0;                                          // stage of step s
+        for (int s = 0; s < steps; ++s) {
+            wait_vmem_but<(D - 2) * (LT + 1)>();
+            phase_end();
+            uint8_t *const ta = tiles[at], *const tb = ta + kA;
+            const float *const sc = inv[s & 1];
+            at = at + 1 == D ? 0 : at + 1;
+            const int krem = kend - s * kBK;
+            if (krem < kBK) {                               // the last step of a k that is no multiple of 128
+#pragma unroll
+                for (int i = 0; i < LA; ++i) {
+                    const int id = i * NT + t, row = id >> 3, ch = (id & 7) ^ swizzle(row);
+                    uint4 *at = (uint4 *)(ta + 16 * id);
                     if (16 * ch + 16 > krem) *at = keep_bytes(*at, krem - 16 * ch);
                 }
-            }
-            phase_end();
-        }
-        float next;                                      // scale of the next step, inverted after the products
-        if constexpr (EXACT) {
-            // lane (r32, h): row r32 of a fragment; slice u of 16 k holds, for half h, the 8 codes at
-            // k = 16 (2 (u / 2) + h) + 8 (u % 2). a comes first, so that a lane ends with one column.
-            const int r32 = lane & 31, h = lane >> 5;
-            // With power-of-two scales a lane's row of each operand carries its own factor.
-            float ea[FM], eb[FN];
 #pragma unroll
-            for (int i = 0; i < FM; ++i) ea[i] = POW2 ? sc[wm * TM + 32 * i + r32] : 1.0f;
-#pragma unroll
-            for (int j = 0; j < FN; ++j) eb[j] = POW2 ? sc[BA + (KIND == kGroups ? wn * TN + 32 * j + r32 : wn * TN / 128)] : 1.0f;
-            v8bf16 fb[FN][8];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if constexpr (KIND == kKN) {
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const int kr = 16 * (2 * (u >> 1) + h) + 8 * (u & 1) + (r16 >> 1);
-                        const int ch = (wn * TN + 32 * j) / 16 + ((lane >> 4) & 1);
-                        const v2i32 q = read_transposed(tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1));
-                        fb[j][u] = codes_to_bf16<FB>((uint32_t)q.x, (uint32_t)q.y, eb[j]);
-                    }
-                } else {
-                    const int row = wn * TN + 32 * j + r32;
-#pragma unroll
-                    for (int u = 0; u < 8; u += 2) {
-                        const uint4 q = *(const uint4 *)(tb + row * kBK + (((u + h) ^ swizzle(row)) << 4));
-                        fb[j][u] = codes_to_bf16<FB>(q.x, q.y, eb[j]);
-                        fb[j][u + 1] = codes_to_bf16<FB>(q.z, q.w, eb[j]);
+                for (int i = 0; i < LB; ++i) {
+                    const int id = i * NT + t;
+                    uint4 *at = (uint4 *)(tb + 16 * id);
+                    if constexpr (KIND == kKN) {
+                        if (id / (BN / 16) >= krem) *at = make_uint4(0, 0, 0, 0);
+                    } else {
+                        const int row = id >> 3, ch = (id & 7) ^ swizzle(row);
+                        if (16 * ch + 16 > krem) *at = keep_bytes(*at, krem - 16 * ch);
                     }
                 }
+                phase_end();
             }
-            next = raw[at][t];
+            float next;                                      // scale of the next step, inverted after the products
+            if constexpr (EXACT) {
+                // lane (r32, h): row r32 of a fragment; slice u of 16 k holds, for half h, the 8 codes at
+                // k = 16 (2 (u / 2) + h) + 8 (u % 2). a comes first, so that a lane ends with one column.
+                const int r32 = lane & 31, h = lane >> 5;
+                // Folded, a lane's row of each operand carries its own factor.
+                float ea[FM], eb[FN];
 #pragma unroll
-            for (int u = 0; u <= LT; ++u) load_piece(u);
+                for (int i = 0; i < FM; ++i) ea[i] = FOLD ? sc[wm * TM + 32 * i + r32] : 1.0f;
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int row = wm * TM + 32 * i + r32;
-                v16f32 part[FN];
+                for (int j = 0; j < FN; ++j) eb[j] = FOLD ? sc[BA + (KIND == kGroups ? wn * TN + 32 * j + r32 : wn * TN / 128)] : 1.0f;
+                v8bf16 fb[FN][8];
 #pragma unroll
-                for (int j = 0; j < FN; ++j) part[j] = POW2 ? (v16f32)acc[i][j] : (v16f32)0.0f;
+                for (int j = 0; j < FN; ++j) {
+                    if constexpr (KIND == kKN) {
 #pragma unroll
-                for (int u = 0; u < 8; u += 2) {
-                    const uint4 q = *(const uint4 *)(ta + row * kBK + (((u + h) ^ swizzle(row)) << 4));
-                    const v8bf16 f0 = codes_to_bf16<FA>(q.x, q.y, ea[i]), f1 = codes_to_bf16<FA>(q.z, q.w, ea[i]);
+                        for (int u = 0; u < 8; ++u) {
+                            const int kr = 16 * (2 * (u >> 1) + h) + 8 * (u & 1) + (r16 >> 1);
+                            const int ch = (wn * TN + 32 * j) / 16 + ((lane >> 4) & 1);
+                            const v2i32 q = read_transposed(tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1));
+                            fb[j][u] = codes_to_bf16<FB>((uint32_t)q.x, (uint32_t)q.y, eb[j]);
+                        }
+                    } else {
+                        const int row = wn * TN + 32 * j + r32;
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) part[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f0, fb[j][u], part[j], 0, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) part[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1, fb[j][u + 1], part[j], 0, 0, 0);
-                }
-                if constexpr (POW2) {
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) acc[i][j] = part[j];
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        v4f32 sa = *(const v4f32 *)(sc + wm * TM + 32 * i + 8 * q + 4 * h);
-                        if constexpr (KIND != kGroups) sa *= sc[BA + wn * TN / 128];
-#pragma unroll
-                        for (int j = 0; j < FN; ++j) {
-                            v4f32 f = sa;
-                            if constexpr (KIND == kGroups) f *= sc[BA + wn * TN + 32 * j + r32];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[i][j][4 * q + e] = __builtin_fmaf(part[j][4 * q + e], f[e], acc[i][j][4 * q + e]);
+                        for (int u = 0; u < 8; u += 2) {
+                            const uint4 q = *(const uint4 *)(tb + row * kBK + (((u + h) ^ swizzle(row)) << 4));
+                            fb[j][u] = codes_to_bf16<FB>(q.x, q.y, eb[j]);
+                            fb[j][u + 1] = codes_to_bf16<FB>(q.z, q.w, eb[j]);
                         }
                     }
                 }
-            }
-            // conversions and scaling run in the shadow of the products: 8 vector instructions a product
+                next = raw[at][t];
 #pragma unroll
-            for (int m = 0; m < FM * FN * 8; ++m) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, POW2 ? 5 : 9, 0);
-            }
-        } else {
-            // lane (r16, g) holds row r16 of a fragment and k = 16 g + [0, 16) and 64 + 16 g + [0, 16).
-            // Products of fragment i run while the fragments of i + 1 are read and the sums of i - 1
-            // are scaled; the next step's loads are issued in between, a few at a time, so that no
-            // wave stands in a full load queue while the matrix core idles.
-            const uint32_t swz = (uint32_t)((g ^ swizzle(r16)) << 4);
-            const uint8_t *const pa = ta + (wm * TM + r16) * kBK;
-            auto frag_a = [&](int i) {
-                return join16(*(const uint4 *)(pa + i * 16 * kBK + swz), *(const uint4 *)(pa + i * 16 * kBK + (swz ^ 64u)));
-            };
-            v8i32 fb[FN];
-            v8i32 fa = frag_a(0);
+                for (int u = 0; u <= LT; ++u) load_piece(u);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if constexpr (KIND == kKN) {
-                    v2i32 q[4];
+                for (int i = 0; i < FM; ++i) {
+                    const int row = wm * TM + 32 * i + r32;
+                    v16f32 part[FN];
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        // 16 lanes read 8 rows of k x 16 columns; two neighbouring lanes cover a row
-                        const int kr = (h >> 1) * 64 + 16 * g + 8 * (h & 1) + (r16 >> 1);
-                        const int ch = (wn * TN + 16 * j) / 16;
-                        q[h] = read_transposed(tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1));
+                    for (int j = 0; j < FN; ++j) part[j] = FOLD ? (v16f32)acc[i][j] : (v16f32)0.0f;
+#pragma unroll
+                    for (int u = 0; u < 8; u += 2) {
+                        const uint4 q = *(const uint4 *)(ta + row * kBK + (((u + h) ^ swizzle(row)) << 4));
+                        const v8bf16 f0 = codes_to_bf16<FA>(q.x, q.y, ea[i]), f1 = codes_to_bf16<FA>(q.z, q.w, ea[i]);
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) part[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f0, fb[j][u], part[j], 0, 0, 0);
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) part[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1, fb[j][u + 1], part[j], 0, 0, 0);
                     }
-                    fb[j] = v8i32{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
-                } else {
-                    const uint8_t *src = tb + (wn * TN + r16) * kBK + j * 16 * kBK;
-                    fb[j] = join16(*(const uint4 *)(src + swz), *(const uint4 *)(src + (swz ^ 64u)));
+                    if constexpr (FOLD) {
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) acc[i][j] = part[j];
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            v4f32 sa = *(const v4f32 *)(sc + wm * TM + 32 * i + 8 * q + 4 * h);
+                            if constexpr (KIND != kGroups) sa *= sc[BA + wn * TN / 128];
+#pragma unroll
+                            for (int j = 0; j < FN; ++j) {
+                                v4f32 f = sa;
+                                if constexpr (KIND == kGroups) f *= sc[BA + wn * TN + 32 * j + r32];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    acc[i][j][4 * q + e] = __builtin_fmaf(part[j][4 * q + e], f[e], acc[i][j][4 * q + e]);
+                            }
+                        }
+                    }
                 }
-            }
-            v4f32 sbg[FN];
-            int ebg[FN];
-            float sa[FM];
+                // conversions and scaling run in the shadow of the products: 8 vector instructions a product
 #pragma unroll
-            for (int i = 0; i < FM; ++i) sa[i] = sc[wm * TM + 16 * i + r16];
-            if constexpr (KIND == kGroups) {
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    if constexpr (POW2) ebg[j] = __float_as_int(sc[BA + wn * TN + 16 * j + r16]);
-                    else sbg[j] = *(const v4f32 *)(sc + BA + wn * TN + 16 * j + 4 * g);
+                for (int m = 0; m < FM * FN * 8; ++m) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, FOLD ? 5 : 9, 0);
                 }
             } else {
-                const float sbu = sc[BA + wn * TN / 128];
-                if constexpr (POW2) {
+                // lane (r16, g) holds row r16 of a fragment and k = 16 g + [0, 16) and 64 + 16 g + [0, 16).
+                // Products of fragment i run while the fragments of i + 1 are read and the sums of i - 1
+                // are scaled; the next step's loads are issued in between, a few at a time, so that no
+                // wave stands in a full load queue while the matrix core idles.
+                const uint32_t swz = (uint32_t)((g ^ swizzle(r16)) << 4);
+                const uint8_t *const pa = ta + (wm * TM + r16) * kBK;
+                auto frag_a = [&](int i) {
+                    return join16(*(const uint4 *)(pa + i * 16 * kBK + swz), *(const uint4 *)(pa + i * 16 * kBK + (swz ^ 64u)));
+                };
+                v8i32 fb[FN];
+                v8i32 fa = frag_a(0);
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) ebg[j] = __float_as_int(sbu);
-                } else {
+                for (int j = 0; j < FN; ++j) {
+                    if constexpr (KIND == kKN) {
+                        v2i32 q[4];
 #pragma unroll
-                    for (int i = 0; i < FM; ++i) sa[i] *= sbu;
-                }
-            }
-            next = raw[at][t];
-            v4f32 part[2][FN];
-            auto scale = [&](int i) {                   // acc += part * (1/Sa 1/Sb)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // the factor first: part times one far scale alone could leave the range
-                        if constexpr (KIND == kGroups) acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], sa[i] * sbg[j][e], acc[i][j][e]);
-                        else acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], sa[i], acc[i][j][e]);
+                        for (int h = 0; h < 4; ++h) {
+                            // 16 lanes read 8 rows of k x 16 columns; two neighbouring lanes cover a row
+                            const int kr = (h >> 1) * 64 + 16 * g + 8 * (h & 1) + (r16 >> 1);
+                            const int ch = (wn * TN + 16 * j) / 16;
+                            q[h] = read_transposed(tb + kr * BN + ((ch ^ (kr & 7)) << 4) + 8 * (r16 & 1));
+                        }
+                        fb[j] = v8i32{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
+                    } else {
+                        const uint8_t *src = tb + (wn * TN + r16) * kBK + j * 16 * kBK;
+                        fb[j] = join16(*(const uint4 *)(src + swz), *(const uint4 *)(src + (swz ^ 64u)));
                     }
-            };
-            constexpr int PI = (LT + FM) / FM;          // load pieces issued per fragment
+                }
+                v4f32 sbg[FN];
+                int ebg[FN];
+                float sa[FM];
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                v8i32 next;
-                if (i + 1 < FM) next = frag_a(i + 1);
-#pragma unroll
-                for (int u = i * PI; u < (i + 1) * PI && u <= LT; ++u) load_piece(u);
-                if constexpr (POW2) {
+                for (int i = 0; i < FM; ++i) sa[i] = sc[wm * TM + 16 * i + r16];
+                if constexpr (KIND == kGroups) {
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
-                        acc[i][j] = mfma_e8m0<FA, FB>(fb[j], fa, acc[i][j], ebg[j], __float_as_int(sa[i]));
+                        if constexpr (POW2) ebg[j] = __float_as_int(sc[BA + wn * TN + 16 * j + r16]);
+                        else sbg[j] = *(const v4f32 *)(sc + BA + wn * TN + 16 * j + 4 * g);
                     }
                 } else {
+                    const float sbu = sc[BA + wn * TN / 128];
+                    if constexpr (POW2) {
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) part[i & 1][j] = mfma_raw<FA, FB>(fb[j], fa, v4f32{0.0f, 0.0f, 0.0f, 0.0f});
-                    if (i > 0) scale(i - 1);
+                        for (int j = 0; j < FN; ++j) ebg[j] = __float_as_int(sbu);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < FM; ++i) sa[i] *= sbu;
+                    }
                 }
-                if (i + 1 < FM) fa = next;
+                next = raw[at][t];
+                v4f32 part[2][FN];
+                auto scale = [&](int i) {                   // acc += part * (1/Sa 1/Sb)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // the factor first: part times one far scale alone could leave the range
+                            if constexpr (KIND == kGroups) acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], sa[i] * sbg[j][e], acc[i][j][e]);
+                            else acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], sa[i], acc[i][j][e]);
+                        }
+                };
+                constexpr int PI = (LT + FM) / FM;          // load pieces issued per fragment
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    v8i32 next;
+                    if (i + 1 < FM) next = frag_a(i + 1);
+#pragma unroll
+                    for (int u = i * PI; u < (i + 1) * PI && u <= LT; ++u) load_piece(u);
+                    if constexpr (POW2) {
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) {
+                            acc[i][j] = mfma_e8m0<FA, FB>(fb[j], fa, acc[i][j], ebg[j], __float_as_int(sa[i]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) part[i & 1][j] = mfma_raw<FA, FB>(fb[j], fa, v4f32{0.0f, 0.0f, 0.0f, 0.0f});
+                        if (i > 0) scale(i - 1);
+                    }
+                    if (i + 1 < FM) fa = next;
+                }
+                if constexpr (!POW2) scale(FM - 1);
             }
-            if constexpr (!POW2) scale(FM - 1);
+            asm volatile("" : "+v"(next));
+            const float f = inverse_scale<MATH>(next);
+            if constexpr (EXACT && FOLD) far = far || (s + 1 < steps && !near_one(f));
+            inv[(s + 1) & 1][t] = f;
         }
-        asm volatile("" : "+v"(next));
-        inv[(s + 1) & 1][t] = inverse_scale<MATH>(next);
+        wait_vmem();                                        // no load may still write LDS when the workgroup ends
+    };
+    all_steps(std::integral_constant<bool, MATH == kMathExactPow2>());
+    if constexpr (MATH == kMathExactPow2) {
+        phase_end();                                    // every wave has left the last step
+        raw[0][t] = far ? 1.0f : 0.0f;
+        phase_end();
+        bool any = false;
+#pragma unroll
+        for (int w = 0; w < NT / 64; ++w) any = any || raw[0][64 * w + lane] != 0.0f;
+        if (__any(any)) {
+            phase_end();
+            all_steps(std::false_type());
+        }
     }
-    wait_vmem();                                        // no load may still write LDS when the workgroup ends
 
     if constexpr (EXACT) store_rows<BM, BN, TM, TN, NT>(p, pl, (float *)&tiles[0][0], wm, wn, t, acc);
     else store_tile<KIND, TM, TN>(p, pl, wm, wn, lane, acc);
