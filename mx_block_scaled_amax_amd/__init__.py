@@ -31,6 +31,7 @@ __all__ = [
 E4M3, E5M2 = 0, 1
 ROUND_DOWN, ROUND_UP = 0, 1
 FLAG_POW2_SCALES = 1
+FLAG_FP32_SUMS = 16                       # products (QF8_FLAG_FP32_SUMS)
 EST_MAX, EST_RECENT, EST_MEAN = 0, 1, 2   # delayed-scaling estimators (qf8_estimator)
 DELAYED_SPLIT_AMAX = 1                    # qf8_delayed_flags
 WEIGHT_NK, WEIGHT_KN, GROUPS_NK = 0, 1, 2  # qf8_operand: layout of the second operand of a product
@@ -592,6 +593,10 @@ def _in_code(t, name):
     raise TypeError(f"{name} must be a torch.bfloat16 or torch.float32 tensor")
 
 
+def _product_flags(pow2_scales, fp32_sums):
+    return (FLAG_POW2_SCALES if pow2_scales else 0) | (FLAG_FP32_SUMS if fp32_sums else 0)
+
+
 def _scale_shape(kind, n, k):
     if kind == WEIGHT_NK:
         return -(-n // 128), -(-k // 128)
@@ -601,12 +606,12 @@ def _scale_shape(kind, n, k):
 
 
 def matmul_block(a, sa, b, sb, fmt_a, fmt_b, kind=WEIGHT_NK, pow2_scales=False, out_dtype=torch.bfloat16, out=None,
-                 ws=None, stream=None):
+                 ws=None, stream=None, fp32_sums=False):
     """y [m][n] = values(a) times values(b), where values are decode(codes) / scale. a: uint8 codes
     [m][k] with 1x128 group scales sa; b and sb by kind: WEIGHT_NK [n][k] and WEIGHT_KN [k][n] in
     128x128 blocks, GROUPS_NK [n][k] in 1x128 groups. pow2_scales: every scale is a power of two. A
     float32 result has fp32 sums; a bfloat16 one those of the FP8 matrix instructions, which keep 14
-    bits of each 8 products."""
+    bits of each 8 products, or with fp32_sums those of a float32 one, at about half the rate."""
     m, k = _need(a, "a", torch.uint8, 2)
     bs = _need(b, "b", torch.uint8, 2)
     n, kb = (bs[1], bs[0]) if kind == WEIGHT_KN else bs
@@ -616,16 +621,16 @@ def matmul_block(a, sa, b, sb, fmt_a, fmt_b, kind=WEIGHT_NK, pow2_scales=False, 
     _need(sb, "sb", torch.float32, _scale_shape(kind, n, k))
     code = _out_code(out_dtype)
     out = _place(out, (m, n), out_dtype, a, "out", stream)
-    ws = _workspace(ws, a, stream, "matmul_block_workspace_bytes", m, n, k, kind, code)
+    ws = _workspace(ws, a, stream, "matmul_block_workspace_bytes", m, n, k, kind, _FP32 if fp32_sums else code)
     _one_device(a, sa, b, sb, out, ws)
     _check(_load().matmul_block(a.data_ptr(), sa.data_ptr(), b.data_ptr(), sb.data_ptr(), m, n, k, fmt_a, fmt_b, kind,
-                                FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code, _address(ws),
+                                _product_flags(pow2_scales, fp32_sums), out.data_ptr(), code, _address(ws),
                                 0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, a)), "matmul_block")
     return out
 
 
 def matmul_block_experts(a, sa, b, sb, offsets, fmt_a, fmt_b, kind=WEIGHT_NK, rows=None, pow2_scales=False,
-                         out_dtype=torch.bfloat16, out=None, stream=None):
+                         out_dtype=torch.bfloat16, out=None, stream=None, fp32_sums=False):
     """One weight per expert: b [experts][n][k] (WEIGHT_NK) or [experts][k][n] (WEIGHT_KN). Rows
     offsets[e] .. offsets[e+1] of the result are those of expert e; row i reads row rows[i] of a (a
     negative entry: zeros), or row i without rows. Rows of no expert are zeros."""
@@ -644,13 +649,13 @@ def matmul_block_experts(a, sa, b, sb, offsets, fmt_a, fmt_b, kind=WEIGHT_NK, ro
     _one_device(a, sa, b, sb, offsets, rows, out)
     _check(_load().matmul_block_experts(a.data_ptr(), sa.data_ptr(), tokens, b.data_ptr(), sb.data_ptr(),
                                         offsets.data_ptr(), experts, _address(rows), nrows, n, k, fmt_a, fmt_b, kind,
-                                        FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code,
+                                        _product_flags(pow2_scales, fp32_sums), out.data_ptr(), code,
                                         _stream_of(stream, a)), "matmul_block_experts")
     return out
 
 
 def matmul_block_experts_wgrad(at, sat, bt, sbt, offsets, fmt_a, fmt_b, pow2_scales=False, out_dtype=torch.float32,
-                               out=None, stream=None):
+                               out=None, stream=None, fp32_sums=False):
     """Weight gradients [experts][m][n]: values(at)[:, rows of e] times values(bt)[:, rows of e]
     transposed, for codes at [m][nrows] and bt [n][nrows] in 1x128 groups along the rows; offsets
     are multiples of 128."""
@@ -666,7 +671,7 @@ def matmul_block_experts_wgrad(at, sat, bt, sbt, offsets, fmt_a, fmt_b, pow2_sca
     _one_device(at, sat, bt, sbt, offsets, out)
     _check(_load().matmul_block_experts_wgrad(at.data_ptr(), sat.data_ptr(), bt.data_ptr(), sbt.data_ptr(),
                                               offsets.data_ptr(), experts, nrows, m, n, fmt_a, fmt_b,
-                                              FLAG_POW2_SCALES if pow2_scales else 0, out.data_ptr(), code,
+                                              _product_flags(pow2_scales, fp32_sums), out.data_ptr(), code,
                                               _stream_of(stream, at)), "matmul_block_experts_wgrad")
     return out
 

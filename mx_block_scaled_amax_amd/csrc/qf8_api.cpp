@@ -37,6 +37,9 @@ constexpr int64_t kMaxLaunchThreads = (int64_t)1 << 32;      // a launch counts 
 constexpr int64_t kMaxRouteTokens = kMaxLaunchThreads / 64;  // one token to a wave
 constexpr int64_t kMaxMatmulDim = 1 << 22;   // keeps every buffer offset of a tile below 2^31
 
+constexpr int kMatmulFlags = QF8_FLAG_POW2_SCALES | QF8_FLAG_FP32_SUMS;
+inline bool fp32_sums(int flags, int out) { return out == QF8_OUT_FP32 || (flags & QF8_FLAG_FP32_SUMS); }
+
 // the sizes a product takes: rows of codes are read as whole dwords
 inline bool matmul_dims_ok(int64_t m, int64_t n, int64_t k, int kind) {
     if (m < 0 || n < 0 || k < 0 || m >= (int64_t)1 << 31 || n > kMaxMatmulDim || k > kMaxMatmulDim) return false;
@@ -450,18 +453,18 @@ qf8_status dequantize_mx(const uint8_t *q, const uint8_t *s, int64_t rows, int64
 
 size_t matmul_block_workspace_bytes(int64_t m, int64_t n, int64_t k, qf8_operand kind, qf8_out_dtype out_dtype) {
     if (!kind_ok(kind) || !out_ok(out_dtype) || !matmul_dims_ok(m, n, k, kind)) return 0;
-    return qf8::matmul_workspace(m, n, k, kind, out_dtype == QF8_OUT_BF16);
+    return qf8::matmul_workspace(m, n, k, kind, out_dtype == QF8_OUT_FP32);
 }
 
 qf8_status matmul_block(const uint8_t *a, const float *sa, const uint8_t *b, const float *sb, int64_t m, int64_t n,
                         int64_t k, qf8_fmt fmt_a, qf8_fmt fmt_b, qf8_operand kind, int flags, void *y,
                         qf8_out_dtype out_dtype, void *ws, size_t ws_bytes, void *stream) {
-    if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b) || !kind_ok(kind) || !out_ok(out_dtype) || (flags & ~QF8_FLAG_POW2_SCALES))
+    if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b) || !kind_ok(kind) || !out_ok(out_dtype) || (flags & ~kMatmulFlags))
         return QF8_ERR_ENUM;
     if (!matmul_dims_ok(m, n, k, kind)) return QF8_ERR_SHAPE;
     if (m == 0 || n == 0) return QF8_OK;
     if (!y || (k > 0 && (!a || !sa || !b || !sb))) return QF8_ERR_NULL;
-    const size_t need = qf8::matmul_workspace(m, n, k, kind, out_dtype == QF8_OUT_BF16);
+    const size_t need = qf8::matmul_workspace(m, n, k, kind, fp32_sums(flags, out_dtype));
     if (need > 0 && (!ws || ws_bytes < need)) return QF8_ERR_WORKSPACE;
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(ws, 16))
         return QF8_ERR_ALIGN;
@@ -470,6 +473,7 @@ qf8_status matmul_block(const uint8_t *a, const float *sa, const uint8_t *b, con
     p.m = m; p.n = (int)n; p.k = k; p.a_rows = m;
     p.mode = qf8::kMatmulDense;
     p.out_bf16 = out_dtype == QF8_OUT_BF16;
+    p.fp32_sums = fp32_sums(flags, out_dtype);
     return status_of(qf8::launch_matmul(p, fmt_a, fmt_b, kind, flags & QF8_FLAG_POW2_SCALES, (float *)ws, as_stream(stream)));
 }
 
@@ -478,7 +482,7 @@ qf8_status matmul_block_experts(const uint8_t *a, const float *sa, int64_t token
                                 int64_t k, qf8_fmt fmt_a, qf8_fmt fmt_b, qf8_operand kind, int flags, void *y,
                                 qf8_out_dtype out_dtype, void *stream) {
     if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b) || (kind != QF8_WEIGHT_NK && kind != QF8_WEIGHT_KN) || !out_ok(out_dtype) ||
-        (flags & ~QF8_FLAG_POW2_SCALES))
+        (flags & ~kMatmulFlags))
         return QF8_ERR_ENUM;
     if (!matmul_dims_ok(nrows, n, k, kind) || tokens < 0 || experts < 1 || experts > qf8::kMaxExperts) return QF8_ERR_SHAPE;
     if (rows ? tokens >= (int64_t)1 << 31 || (k > 0 && tokens > 0xFFFFFFFFll / k) : tokens != nrows) return QF8_ERR_SHAPE;
@@ -493,6 +497,7 @@ qf8_status matmul_block_experts(const uint8_t *a, const float *sa, int64_t token
     p.experts = experts;
     p.mode = qf8::kMatmulExperts;
     p.out_bf16 = out_dtype == QF8_OUT_BF16;
+    p.fp32_sums = fp32_sums(flags, out_dtype);
     return status_of(qf8::launch_matmul(p, fmt_a, fmt_b, kind, flags & QF8_FLAG_POW2_SCALES, nullptr, as_stream(stream)));
 }
 
@@ -500,7 +505,7 @@ qf8_status matmul_block_experts_wgrad(const uint8_t *at, const float *sat, const
                                       const int32_t *offsets, int experts, int64_t nrows, int64_t m, int64_t n,
                                       qf8_fmt fmt_a, qf8_fmt fmt_b, int flags, void *y, qf8_out_dtype out_dtype,
                                       void *stream) {
-    if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b) || !out_ok(out_dtype) || (flags & ~QF8_FLAG_POW2_SCALES)) return QF8_ERR_ENUM;
+    if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b) || !out_ok(out_dtype) || (flags & ~kMatmulFlags)) return QF8_ERR_ENUM;
     if (!matmul_dims_ok(m, n, nrows, QF8_GROUPS_NK) || experts < 1 || experts > qf8::kMaxExperts) return QF8_ERR_SHAPE;
     if (m == 0 || n == 0) return QF8_OK;
     if (!y || !offsets || (nrows > 0 && (!at || !sat || !bt || !sbt))) return QF8_ERR_NULL;
@@ -513,6 +518,7 @@ qf8_status matmul_block_experts_wgrad(const uint8_t *at, const float *sat, const
     p.experts = experts;
     p.mode = qf8::kMatmulExpertsK;
     p.out_bf16 = out_dtype == QF8_OUT_BF16;
+    p.fp32_sums = fp32_sums(flags, out_dtype);
     return status_of(qf8::launch_matmul(p, fmt_a, fmt_b, QF8_GROUPS_NK, flags & QF8_FLAG_POW2_SCALES, nullptr,
                                         as_stream(stream)));
 }

@@ -108,11 +108,11 @@ struct MatmulArgs {
     int64_t m, k, a_rows;
     int n, experts, mode, splits;
     int64_t split_k;             // k of one split, a multiple of 128
-    int out_bf16;
+    int out_bf16, fp32_sums;
 };
 int launch_matmul(const MatmulArgs &p, int fmt_a, int fmt_b, int kind, int pow2, float *ws, hipStream_t s);
 // Bytes of partial sums launch_matmul uses for a dense product (0: none).
-size_t matmul_workspace(int64_t m, int64_t n, int64_t k, int kind, int out_bf16);
+size_t matmul_workspace(int64_t m, int64_t n, int64_t k, int kind, int fp32_sums);
 
 // The expert layer: choice of experts, order of the rows, weighted sum.
 constexpr int kMaxExperts = 1024, kMaxTopK = 64, kMaxExpertGroups = 64;

@@ -20,7 +20,8 @@
 // 2^2 is lost; 1.4e-5 relative error on normal data, for the 16x16x32 form too), while the BF16
 // MFMA keeps fp32's 24 bits. A BF16 result is rounded to 8 bits, a hundred times that error, so it
 // takes the FP8 instructions (4.4-4.8 PFLOP/s alone); an FP32 result is asked for where sums count
-// (weight gradients) and takes the BF16 ones (1.7 PFLOP/s alone), whose sums are true fp32 sums.
+// (weight gradients) and takes the BF16 ones (1.7 PFLOP/s alone), whose sums are true fp32 sums, as does a
+// BF16 result on request.
 //
 // Orientation: b's rows are the MFMA's first operand, so a lane of the result holds one row i of y
 // and neighbouring j: 1/Sa is one register per fragment and Sb's block is uniform.
@@ -436,7 +437,7 @@ __device__ __forceinline__ bool no_source(const MatmulArgs &p, int64_t row) {
     return src < 0 || src >= p.a_rows;
 }
 
-// FP32 results go through LDS to whole rows of BN columns: a store of 16 bytes a lane covers 1 KiB of
+// Results of fp32 sums go through LDS to whole rows of BN columns: a store of 16 bytes a lane covers 1 KiB of
 // memory, one of 4 bytes 256 bytes in the same time. Lane: column lane % 32, rows 8 q + 4 (lane / 32) + e of a
 // 32 x 32 fragment; rows 4-7 of 8 hold columns c ^ 32, so that both halves of a wave write all banks. buf: the
 // operand tiles, which every wave has left.
@@ -458,11 +459,30 @@ __device__ __forceinline__ void store_rows(const MatmulArgs &p, const TilePlace 
     constexpr int CH = BN / 4, U = BM * CH / NT;         // 16-byte pieces of a row; those of a thread
     const int64_t plane = p.mode == kMatmulExpertsK ? pl.expert : pl.split;
     const int r0 = t / CH, c = 4 * (t % CH), n = pl.n0 + c;
-    float *y = (float *)p.y + (plane * p.m + pl.row0 + r0) * p.n + n;
-    const int64_t pitch = (int64_t)(NT / CH) * p.n;
+    const int64_t first = (plane * p.m + pl.row0 + r0) * p.n + n, pitch = (int64_t)(NT / CH) * p.n;
     typedef float any4 __attribute__((ext_vector_type(4), aligned(4)));     // rows need no alignment
     static_assert(NT / CH % 8 == 0, "the rows of a thread hold their columns in the same order");
     const float *src = buf + r0 * BN + (c ^ (((r0 >> 2) & 1) << 5));
+    if (p.out_bf16) {
+        uint16_t *y = (uint16_t *)p.y + first;
+#pragma unroll 4
+        for (int u = 0; u < U; ++u, y += pitch) {
+            const int r = u * (NT / CH) + r0;
+            if (r >= pl.rows || n >= p.n) continue;
+            const v4f32 v = *(const v4f32 *)(src + u * (NT / CH) * BN);
+            const bool zero = no_source(p, pl.row0 + r);
+            const uint32_t w[2] = {zero ? 0u : pack_bf16(v[0], v[1]), zero ? 0u : pack_bf16(v[2], v[3])};
+            if (n + 4 <= p.n) {
+                __builtin_memcpy(y, w, sizeof(w));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (n + e < p.n) y[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            }
+        }
+        return;
+    }
+    float *y = (float *)p.y + first;
     if (pl.rows == BM && pl.n0 + BN <= p.n && !p.rows) {
 #pragma unroll
         for (int u = 0; u < U; ++u, y += pitch)

@@ -92,10 +92,10 @@ int launch_by_format(const MatmulArgs &p, int fa, int fb, int kind, int math, in
 
 }  // namespace
 
-size_t matmul_workspace(int64_t m, int64_t n, int64_t k, int kind, int out_bf16) {
+size_t matmul_workspace(int64_t m, int64_t n, int64_t k, int kind, int fp32_sums) {
     (void)kind;
     if (m == 0 || n == 0 || k == 0) return 0;
-    const Plan pl = plan_dense(m, n, k, !out_bf16);
+    const Plan pl = plan_dense(m, n, k, fp32_sums != 0);
     return pl.splits > 1 ? (size_t)pl.splits * m * n * sizeof(float) : 0;
 }
 
@@ -104,7 +104,7 @@ int launch_matmul(const MatmulArgs &args, int fmt_a, int fmt_b, int kind, int po
     if (p.m == 0 || p.n == 0) return QF8_OK;
     p.splits = 1;
     p.split_k = p.k;
-    const bool exact = !args.out_bf16;
+    const bool exact = args.fp32_sums != 0;
     const int math = exact ? (pow2 ? kMathExactPow2 : kMathExact) : pow2 ? kMathE8m0 : kMathFp8;
     const TileSize *sizes = kTileSizes;
     if (p.mode == kMatmulDense) {

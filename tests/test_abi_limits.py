@@ -40,3 +40,18 @@ def test_more_tokens_than_a_launch_holds():
     assert lib.combine_experts(F, 0, 64, 8, F, F, (1 << 24) - 1, 2, None, None) == -1
     assert lib.route_experts(F, 0, (1 << 26) - 1, 8, 2, 0, None, 1, 1, 1, 1.0, F, None, None) == -1
     assert lib.combine_experts_backward(F, F, 0, 1 << 12, 8, F, F, F, (1 << 24) - 65, 2, None, F, None) == -1
+
+
+def test_flags_of_products():
+    """fp32 sums for BF16 results are bit 16; other bits are refused. Their workspace is that of FP32 results."""
+    lib = qf8._load()
+
+    def mm(flags, ws_bytes):
+        return lib.matmul_block(F, F, F, F, 8, 128, 65536, 0, 0, 0, flags, None, 0, F, ws_bytes, None)
+    assert mm(32, 1 << 40) == -2 and mm(16 | 4, 1 << 40) == -2
+    assert mm(16, 1 << 40) == -1 and mm(17, 1 << 40) == -1                                       # only y is missing
+
+    def short(flags, out):
+        need = lib.matmul_block_workspace_bytes(8, 128, 65536, 0, 1)
+        return lib.matmul_block(F, F, F, F, 8, 128, 65536, 0, 0, 0, flags, F, out, F, need - 1, None)
+    assert short(16, 0) == -5 and short(0, 1) == -5
