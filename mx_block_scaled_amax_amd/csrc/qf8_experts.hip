@@ -518,7 +518,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_rows_kernel(R
 // choices of 128 experts take 2.9 + 7.7 us (1.6 MB in and out), 512 of 256 in one workgroup 4.7 us. Padding
 // written by one thread an expert, where 16 do it now, and a 64-bit division for each choice had cost 3.9 us more.
 constexpr int kOrderThreads = 1024, kOrderWaves = kOrderThreads / 64;
-constexpr int kOrderOne = 4096;                        // choices up to which one workgroup does all
+// Choices up to which one workgroup does all. us, one workgroup / two kernels: 1024 of 64 experts 4.7 / 6.6, 2048 6.4 / 7.1,
+// 4096 10.0 / 7.3; of 256 with rows padded to 128: 1024 7.7 / 9.7, 2048 9.7 / 9.1, 4096 13.7 / 8.8.
+constexpr int kOrderOne = 2048;
 constexpr int kOrderGroups = 256;                      // workgroups at most: each reads the counts of all
 inline int64_t order_chunk(int64_t n) {                // choices of a workgroup
     const int64_t c = (n + kOrderGroups - 1) / kOrderGroups;
