@@ -840,7 +840,9 @@ inline bool route_by_rows(const RouteArgs &p, bool backward) {
 
 template <typename T, int NE>
 int launch_route_ne(const RouteArgs &p, bool backward, hipStream_t s) {
-    // few tokens: one wave per workgroup, so that they spread over the CUs
+    // few tokens: one wave per workgroup, so that they spread over the CUs. us, 1 wave / 4: 64 x 128 BF16 3.1 / 3.4,
+    // 1024 3.4 / 3.5, 2048 3.8 / 3.5; 64 x 256 with bias and groups 7.3 / 7.7, 1024 7.7 / 7.7, 4096 11.2 / 10.9;
+    // backward 64 x 128 3.1 / 3.3, 1024 3.3 / 3.4, 2048 3.7 / 3.4
     const int waves = p.tokens <= 1024 ? 1 : kRouteWaves;
     const dim3 grid((unsigned)((p.tokens + waves - 1) / waves)), block(64 * waves);
     if (backward) {
@@ -918,9 +920,11 @@ int launch_combine(const CombineArgs &args, int dtype, int backward, hipStream_t
         return launched();
     }
     if (p.tokens == 0) return QF8_OK;
-    // few tokens: a row's pieces spread over several workgroups
+    // A row's pieces spread over several workgroups, but for many tokens of few rows. us, several / one, BF16: 64 x 8
+    // rows of 7168 6.3 / 15.6, 1024 x 8 31.5 / 34.2, 4096 x 8 113 / 127, 8192 x 8 of 4096 124 / 130, 16384 x 4 of 2880
+    // 116 / 116; 16384 x 2 of 7168 169 / 161, 65536 x 2 of 2100 583 / 558, 32768 x 1 of 4096 137 / 126
     const int64_t per = (p.dim + (int64_t)kCombineThreads * N - 1) / ((int64_t)kCombineThreads * N);
-    const unsigned gy = (unsigned)(p.tokens >= 2048 ? 1 : per < 64 ? per : 64);
+    const unsigned gy = (unsigned)(p.tokens >= 2048 && p.top_k <= 2 ? 1 : per < 64 ? per : 64);
     const dim3 grid((unsigned)p.tokens, gy);
     if (dtype == QF8_IN_BF16) hipLaunchKernelGGL((combine_kernel<uint16_t>), grid, dim3(kCombineThreads), 0, s, p);
     else hipLaunchKernelGGL((combine_kernel<float>), grid, dim3(kCombineThreads), 0, s, p);
