@@ -887,11 +887,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 // takes 910 cycles, 770 with exponents in place of the FMAs, for 512 of products. Without its loads it
 // takes 705 and 585, with loads that always hit L2 801 and 613, but at 1.6-1.7 GHz for 1.8-1.9: the card
 // is at its power limit, so cycles saved come back as time by half only.
-// Loads go to LDS as soon as a region is free in both groups: P2 of step s loads b, a's first halves
-// and a column of scales for step s + 2 (7 loads a wave), P0 loads a's second halves for step
-// s + 1 (2 loads); each has five to six phases to arrive and is waited for by count (9 newer loads may be in
-// flight). Scales arrive one step earlier than their codes; P0 of the step before inverts them, one
-// per thread.
+// Loads go to LDS between the products, as soon as a region is free in both groups (the second group reads
+// what the first read one phase before):
+//   P1 of step s  a's second halves of step s + 1 (2 loads a wave), where those of s - 1 were: last read in
+//                 the second group's P2 of s - 1, the first group's P3 of s - 1
+//   P3 of step s  b and a's first halves of step s + 2 (6 loads), where those of s were: last read in the
+//                 second group's P0 of s, the first group's P1 of s; and the scales of step s + 3 (1 load),
+//                 where the same thread read those of s + 1 in P1
+// They are waited for by count three phases after: the second halves of s in P0 of s (7 newer loads may be in
+// flight), b and the first halves of s + 1 in P2 of s (2 newer, and the scales of s + 2 with them). A wave's
+// wait is followed by its group's barrier, the other group's by the next one, and the first read comes two
+// barriers after. P1 of step s inverts the scales of s + 1, one per thread; P0 of s + 1 reads them.
 template <int FA, int FB, int KIND, int MATH>
 __global__ __launch_bounds__(512, 2) void matmul_large_kernel(MatmulArgs p) {
     static_assert(KIND != kGroups && MATH < kMathExact, "one scale of b for each wave and step");
