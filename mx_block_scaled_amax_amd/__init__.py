@@ -510,13 +510,13 @@ def _stream_of(stream, t):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
-def _need(t, name, dtype, shape=None, like=None):
-    """A contiguous device tensor of this type; shape: a tuple, or a number of dimensions; on the device of
-    the tensor like (the kernel would read another device's address on its own)."""
+def _need(t, name, dtype, shape=None, device=None):
+    """A contiguous device tensor of this type; shape: a tuple, or a number of dimensions; device: the index of
+    the first tensor's (the kernel would read another device's address on its own)."""
     try:                                                 # what a right call takes
         s = t.shape
         if (t.is_cuda and t.dtype == dtype and (len(s) == shape or s == shape) and t.is_contiguous()
-                and (like is None or t.get_device() == like.get_device())):
+                and (device is None or t.get_device() == device)):
             return s
     except AttributeError:
         pass
@@ -531,13 +531,13 @@ def _need(t, name, dtype, shape=None, like=None):
         raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    _same_device(t, name, like)
+    _same_device(t, name, device)
     return t.shape
 
 
-def _same_device(t, name, like):
-    if like is not None and t.get_device() != like.get_device():
-        raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, others on {like.device}")
+def _same_device(t, name, device):
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"all tensors must be on one device: {name} is on {t.device}, others on cuda:{device}")
 
 
 def _fresh(like, shape, dtype, stream):
@@ -554,7 +554,7 @@ def _place(t, shape, dtype, like, name, stream):
     """The given output, checked, or a new one."""
     if t is None:
         return _fresh(like, shape, dtype, stream)
-    _need(t, name, dtype, shape, like)
+    _need(t, name, dtype, shape, like.get_device())
     return t
 
 
@@ -567,7 +567,7 @@ def _size_of(name, *args):
 def _workspace(ws, like, stream, name, *sizes):
     """The given workspace, checked, or a new one of the size that the library names; None for none."""
     if ws is not None:
-        _same_device(_dev_tensor(ws, "ws"), "ws", like)
+        _same_device(_dev_tensor(ws, "ws"), "ws", like.get_device())
         return ws
     need = _size_of(name, *sizes)
     return _fresh(like, (need,), torch.uint8, stream) if need else None
@@ -614,12 +614,13 @@ def matmul_block(a, sa, b, sb, fmt_a, fmt_b, kind=WEIGHT_NK, pow2_scales=False, 
     float32 result has fp32 sums; a bfloat16 one those of the FP8 matrix instructions, which keep 14
     bits of each 8 products, or with fp32_sums those of a float32 one, at about half the rate."""
     m, k = _need(a, "a", torch.uint8, 2)
-    bs = _need(b, "b", torch.uint8, 2, a)
+    device = a.get_device()
+    bs = _need(b, "b", torch.uint8, 2, device)
     n, kb = (bs[1], bs[0]) if kind == WEIGHT_KN else bs
     if kb != k:
         raise ValueError(f"b must have {k} values along the sum, got {kb}")
-    _need(sa, "sa", torch.float32, (m, -(-k // 128)), a)
-    _need(sb, "sb", torch.float32, _scale_shape(kind, n, k), a)
+    _need(sa, "sa", torch.float32, (m, -(-k // 128)), device)
+    _need(sb, "sb", torch.float32, _scale_shape(kind, n, k), device)
     code = _out_code(out_dtype)
     out = _place(out, (m, n), out_dtype, a, "out", stream)
     ws = _workspace(ws, a, stream, "matmul_block_workspace_bytes", m, n, k, kind, _FP32 if fp32_sums else code)
@@ -635,15 +636,16 @@ def matmul_block_experts(a, sa, b, sb, offsets, fmt_a, fmt_b, kind=WEIGHT_NK, ro
     offsets[e] .. offsets[e+1] of the result are those of expert e; row i reads row rows[i] of a (a
     negative entry: zeros), or row i without rows. Rows of no expert are zeros."""
     tokens, k = _need(a, "a", torch.uint8, 2)
-    experts, n, kb = _need(b, "b", torch.uint8, 3, a)
+    device = a.get_device()
+    experts, n, kb = _need(b, "b", torch.uint8, 3, device)
     if kind == WEIGHT_KN:
         n, kb = kb, n
     if kb != k:
         raise ValueError(f"b must have {k} values along the sum, got {kb}")
-    _need(sa, "sa", torch.float32, (tokens, -(-k // 128)), a)
-    _need(sb, "sb", torch.float32, (experts,) + _scale_shape(kind, n, k), a)
-    _need(offsets, "offsets", torch.int32, (experts + 1,), a)
-    nrows = tokens if rows is None else _need(rows, "rows", torch.int32, 1, a)[0]
+    _need(sa, "sa", torch.float32, (tokens, -(-k // 128)), device)
+    _need(sb, "sb", torch.float32, (experts,) + _scale_shape(kind, n, k), device)
+    _need(offsets, "offsets", torch.int32, (experts + 1,), device)
+    nrows = tokens if rows is None else _need(rows, "rows", torch.int32, 1, device)[0]
     code = _out_code(out_dtype)
     out = _place(out, (nrows, n), out_dtype, a, "out", stream)
     _check(_load().matmul_block_experts(a.data_ptr(), sa.data_ptr(), tokens, b.data_ptr(), sb.data_ptr(),
@@ -659,12 +661,13 @@ def matmul_block_experts_wgrad(at, sat, bt, sbt, offsets, fmt_a, fmt_b, pow2_sca
     transposed, for codes at [m][nrows] and bt [n][nrows] in 1x128 groups along the rows; offsets
     are multiples of 128."""
     m, nrows = _need(at, "at", torch.uint8, 2)
-    n, nb = _need(bt, "bt", torch.uint8, 2, at)
+    device = at.get_device()
+    n, nb = _need(bt, "bt", torch.uint8, 2, device)
     if nb != nrows:
         raise ValueError(f"bt must have {nrows} columns, got {nb}")
-    _need(sat, "sat", torch.float32, (m, -(-nrows // 128)), at)
-    _need(sbt, "sbt", torch.float32, (n, -(-nrows // 128)), at)
-    experts = _need(offsets, "offsets", torch.int32, 1, at)[0] - 1
+    _need(sat, "sat", torch.float32, (m, -(-nrows // 128)), device)
+    _need(sbt, "sbt", torch.float32, (n, -(-nrows // 128)), device)
+    experts = _need(offsets, "offsets", torch.int32, 1, device)[0] - 1
     code = _out_code(out_dtype)
     out = _place(out, (experts, m, n), out_dtype, at, "out", stream)
     _check(_load().matmul_block_experts_wgrad(at.data_ptr(), sat.data_ptr(), bt.data_ptr(), sbt.data_ptr(),
@@ -686,7 +689,7 @@ def route_experts(logits, top_k, score=SCORE_SOFTMAX, bias=None, groups=1, top_g
     dtype = _in_code(logits, "logits")
     tokens, experts = _need(logits, "logits", logits.dtype, 2)
     if bias is not None:
-        _need(bias, "bias", torch.float32, (experts,), logits)
+        _need(bias, "bias", torch.float32, (experts,), logits.get_device())
     ids = _place(ids, (tokens, top_k), torch.int32, logits, "ids", stream)
     weights = _place(weights, (tokens, top_k), torch.float32, logits, "weights", stream)
     _check(_load().route_experts(logits.data_ptr(), dtype, tokens, experts, top_k, score, _address(bias), groups,
@@ -700,10 +703,11 @@ def route_experts_backward(logits, ids, dweights, score=SCORE_SOFTMAX, renorm=Tr
     """Gradient of the logits from that of the weights of route_experts (same score, renorm, scale)."""
     dtype = _in_code(logits, "logits")
     tokens, experts = _need(logits, "logits", logits.dtype, 2)
-    t, top_k = _need(ids, "ids", torch.int32, 2, logits)
+    device = logits.get_device()
+    t, top_k = _need(ids, "ids", torch.int32, 2, device)
     if t != tokens:
         raise ValueError(f"ids must have {tokens} rows, got {t}")
-    _need(dweights, "dweights", torch.float32, (tokens, top_k), logits)
+    _need(dweights, "dweights", torch.float32, (tokens, top_k), device)
     dlogits = _place(dlogits, (tokens, experts), logits.dtype, logits, "dlogits", stream)
     _check(_load().route_experts_backward(logits.data_ptr(), dtype, tokens, experts, ids.data_ptr(), dweights.data_ptr(),
                                           top_k, score, int(renorm), scale, dlogits.data_ptr(),
@@ -732,8 +736,9 @@ def combine_experts(x, weights, slots, y=None, stream=None):
     rows adds nothing."""
     dtype = _in_code(x, "x")
     nrows, dim = _need(x, "x", x.dtype, 2)
-    tokens, top_k = _need(slots, "slots", torch.int32, 2, x)
-    _need(weights, "weights", torch.float32, (tokens, top_k), x)
+    device = x.get_device()
+    tokens, top_k = _need(slots, "slots", torch.int32, 2, device)
+    _need(weights, "weights", torch.float32, (tokens, top_k), device)
     y = _place(y, (tokens, dim), x.dtype, x, "y", stream)
     _check(_load().combine_experts(x.data_ptr(), dtype, nrows, dim, weights.data_ptr(), slots.data_ptr(), tokens, top_k,
                                    y.data_ptr(), _stream_of(stream, x)), "combine_experts")
@@ -745,10 +750,11 @@ def combine_experts_backward(dy, x, weights, slots, rows, dx=None, dweights=None
     call; rows of dx that hold no token are zeros."""
     dtype = _in_code(x, "x")
     nrows, dim = _need(x, "x", x.dtype, 2)
-    tokens, top_k = _need(slots, "slots", torch.int32, 2, x)
-    _need(weights, "weights", torch.float32, (tokens, top_k), x)
-    _need(dy, "dy", x.dtype, (tokens, dim), x)
-    _need(rows, "rows", torch.int32, (nrows,), x)
+    device = x.get_device()
+    tokens, top_k = _need(slots, "slots", torch.int32, 2, device)
+    _need(weights, "weights", torch.float32, (tokens, top_k), device)
+    _need(dy, "dy", x.dtype, (tokens, dim), device)
+    _need(rows, "rows", torch.int32, (nrows,), device)
     dx = _place(dx, (nrows, dim), x.dtype, x, "dx", stream)
     dweights = _place(dweights, (tokens, top_k), torch.float32, x, "dweights", stream)
     _check(_load().combine_experts_backward(dy.data_ptr(), x.data_ptr(), dtype, nrows, dim, weights.data_ptr(),
