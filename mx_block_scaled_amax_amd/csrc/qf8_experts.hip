@@ -666,7 +666,7 @@ __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs p)
 //
 // y[t] = sum_j weights[t][j] x[slots[t][j]], in fp32, in the order of j, rounded once. Bound by the
 // rows of x: every thread keeps the 16-byte pieces of all its top_k rows in flight. 8192 x 8 rows of 4096
-// BF16: 131 us, 4.6 TB/s (a copy of 2 GiB 4.9); the gradients below 278 us, 4.4 TB/s.
+// BF16: 125 us, 4.8 TB/s (a copy of 2 GiB 4.9); the gradients below 278 us, 4.4 TB/s.
 template <typename T> struct Piece;                    // 16 bytes as fp32 values
 template <> struct Piece<uint16_t> {
     static constexpr int N = 8;

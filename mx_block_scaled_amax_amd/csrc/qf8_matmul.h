@@ -883,10 +883,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tile_kernel(MatmulArgs
 //
 // so on every SIMD one wave feeds the matrix core while the other reads. In the plain form of the
 // tile both waves of a SIMD wait for the same barrier and the same reads: the matrix core was busy
-// 40% of the time on 8192 x 7168 x 18432 (1143 us). Now it is busy 47% (1051 us, 2.06 PFLOP/s): a phase
-// takes 910 cycles, 770 with exponents in place of the FMAs, for 512 of products. Without its loads it
-// takes 705 and 585, with loads that always hit L2 801 and 613, but at 1.6-1.7 GHz for 1.8-1.9: the card
-// is at its power limit, so cycles saved come back as time by half only.
+// 40% of the time on 8192 x 7168 x 18432 (1143 us). Now a pass takes 1052 us, 2.06 PFLOP/s; counted in a
+// slower run (1150 us at 1.90 GHz) it was busy 47%, which is 52% of 1052 us at that clock. A phase takes
+// 910 cycles, 770 with exponents in place of the FMAs, for 512 of products. Without its loads it takes 705
+// and 585, with loads that always hit L2 801 and 613, but at 1.6-1.7 GHz for 1.8-1.9: the card is at its
+// power limit, so cycles saved come back as time by half only.
 // Loads go to LDS between the products, as soon as a region is free in both groups (the second group reads
 // what the first read one phase before):
 //   P1 of step s  a's second halves of step s + 1 (2 loads a wave), where those of s - 1 were: last read in
