@@ -416,7 +416,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteA
         const double w = sum > 0.0 ? s / sum : 0.0;
         const double mean = wave_sum(g * w, p.top_k);
         if (softmax) d = w * (g - mean);
-        else d = sum > 0.0 ? (g - mean) / sum * (s / (1.0 + exp(x))) : 0.0;
+        else d = w * (g - mean) / (1.0 + exp(x));       // p_j / T first: 1 / T alone may leave fp64
     } else if (softmax) {
         rest = wave_sum(g * s, p.top_k);
         d = s * (g - rest);
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_rows_kernel(R
         const double w = sum > 0.0 ? s / sum : 0.0;
         const double mean = row_sum(g * w);
         if (softmax) d = w * (g - mean);
-        else d = sum > 0.0 ? (g - mean) / sum * (s / (1.0 + exp(x))) : 0.0;
+        else d = w * (g - mean) / (1.0 + exp(x));       // p_j / T first: 1 / T alone may leave fp64
     } else if (softmax) {
         rest = row_sum(g * s);
         d = s * (g - rest);

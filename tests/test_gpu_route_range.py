@@ -90,3 +90,23 @@ def test_lowest_value_is_a_number(tokens):
         for score in ("softmax", "sigmoid"):
             ids, _ = check_route(x, 5, score)
             assert ids[tokens - 1].tolist() == [70, 50, 51, 52, 0]
+
+
+@pytest.mark.parametrize("tokens", [5, 3000])
+@pytest.mark.parametrize("at", [-600.0, -700.0, -708.0])
+def test_gradient_of_small_sigmoid_scores(tokens, at):
+    """Scores near fp64's smallest have ratios, and a gradient, like others: there a sigmoid is exp, so the
+    renormalised weights are a softmax of the chosen logits and 1 - p is 1."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(9)
+    x = at + torch.rand(tokens, 20, generator=gen, device="cuda")
+    ids, w = qf8.route_experts(x, 4, score=qf8.SCORE_SIGMOID)
+    chosen = torch.softmax(x.double().gather(1, ids.long()), 1)
+    # fp64's own error: 2^-52 of an exponent of up to 709, doubled for the sum
+    slack = 2.0 ** -24 * 1.01 + 2.0 ** -40
+    assert bool(((w.double() - chosen).abs() <= chosen * slack).all())
+    dw = 30.0 * torch.randn(tokens, 4, generator=gen, device="cuda")
+    got = qf8.route_experts_backward(x, ids, dw, score=qf8.SCORE_SIGMOID).double()
+    g = dw.double()
+    want = torch.zeros_like(got).scatter_(1, ids.long(), chosen * (g - (g * chosen).sum(1, keepdim=True)))
+    assert bool(((got - want).abs() <= want.abs() * slack + 2.0 ** -40 * g.abs().max(1, keepdim=True)[0]).all())
