@@ -457,6 +457,85 @@ qf8_status combine_experts_backward(const void *dy, const void *x, qf8_dtype dty
                                     const float *weights, const int32_t *slots, const int32_t *rows, int64_t tokens,
                                     int top_k, void *dx, float *dweights, void *stream);
 
+/* ---- around the expert layer ---------------------------------------------------------------------
+ * Root-mean-square norm of a residual stream, its result in FP8 codes with 1x128 scales:
+ *   h = rnd(x + residual) in the residual's type (h = x without a residual),
+ *   R = 1 / sqrt(mean_c h^2 + eps),   y = h R weight,   codes and scales of y as quantize_block gives them.
+ * Sums are fp32 in a fixed order (a row whose squares overflow fp32 is summed again, scaled); y is rounded to FP8
+ * from fp32, not by way of BF16. x [rows][cols] of dtype; residual (nullable) and h [rows][cols] of residual_dtype,
+ * h required with a residual and allowed to be the residual itself; weight [cols] of weight_dtype. q [rows][cols] and scales
+ * [rows][ceil(cols/128)]: both or neither; y (nullable) [rows][cols] of dtype; at least one of q and y. rstd
+ * (nullable): R, [rows] fp32, for the backward pass. nonfinite (nullable) is set where y holds Inf or NaN.
+ * flags: QF8_FLAG_POW2_SCALES. cols % 8 == 0, cols <= 16384; 0 < eps < infinity. Tensors 16-byte aligned, scales
+ * and rstd 4-byte; no other output overlaps an input. */
+qf8_status rms_norm_quantize(const void *x, qf8_dtype dtype, const void *residual, qf8_dtype residual_dtype,
+                             const void *weight, qf8_dtype weight_dtype, int64_t rows, int64_t cols, float eps, qf8_fmt fmt,
+                             int flags, uint8_t *q, float *scales, void *h, void *y, float *rstd, int32_t *nonfinite,
+                             void *stream);
+
+/* Gradients of y = h R weight, with n = h R and g = dy weight:
+ *   dx = R (g - n mean_c(g n)) + dres,   dweight = sum over the rows of dy n.
+ * dy [rows][cols] of dtype; h, dres (nullable: the gradient that reaches h past the norm) and dx of h_dtype, dx allowed
+ * to be dres itself; rstd as the forward pass gave it; dweight (nullable) [cols] fp32, summed in a fixed order. dx is the
+ * gradient of x and of the residual. ws: rms_norm_backward_workspace_bytes() bytes (needed for dweight only),
+ * 16-byte aligned, no initialisation. */
+size_t rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+qf8_status rms_norm_backward(const void *dy, qf8_dtype dtype, const void *h, qf8_dtype h_dtype, const float *rstd,
+                             const void *weight, qf8_dtype weight_dtype, const void *dres, int64_t rows, int64_t cols,
+                             void *dx, float *dweight, void *ws, size_t ws_bytes, void *stream);
+
+/* Gated activation of a product's two halves: y = act(a) * b for x = [a | b], x [rows][2 cols], in fp32. Codes q
+ * [rows][cols] with 1x128 scales [rows][ceil(cols/128)] (both or neither) and y (nullable) [rows][cols] of dtype; at least
+ * one of the two. act: SiLU, a sigmoid(a), or the tanh form of GELU, a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2.
+ * cols % 8 == 0; rows * ceil(cols/128) < 2^31. flags: QF8_FLAG_POW2_SCALES. nonfinite (nullable) is set where y holds
+ * Inf or NaN (a = -Inf gives NaN). */
+typedef enum qf8_act { QF8_ACT_SILU = 0, QF8_ACT_GELU = 1 } qf8_act;
+
+qf8_status gated_act_quantize(const void *x, qf8_dtype dtype, int64_t rows, int64_t cols, qf8_act act, qf8_fmt fmt, int flags,
+                              uint8_t *q, float *scales, void *y, int32_t *nonfinite, void *stream);
+
+/* Its gradients from dy [rows][cols]: [dy b act'(a) | dy act(a)], as codes q [rows][2 cols] with 1x128 scales
+ * [rows][2 cols / 128] (both or neither; cols % 128 == 0 with them) and as dx (nullable) [rows][2 cols] of dtype; at least
+ * one of the two. */
+qf8_status gated_act_backward(const void *dy, const void *x, qf8_dtype dtype, int64_t rows, int64_t cols, qf8_act act,
+                              qf8_fmt fmt, int flags, uint8_t *q, float *scales, void *dx, int32_t *nonfinite, void *stream);
+
+/* A whole expert layer with gated activation for a few tokens, in two kernels:
+ *   y[t] = sum_j weights[t][j] W2[e] a,  a = rnd_bf16(act(A x[t]) * (B x[t])),  W1[e] = [A; B],  e = ids[t][j].
+ * x and y [tokens][dim] BF16. w1: codes [experts][2 hidden][dim] with 128x128 scales s1
+ * [experts][ceil(2 hidden/128)][ceil(dim/128)]; w2: codes [experts][dim][hidden], s2 [experts][ceil(dim/128)]
+ * [ceil(hidden/128)], both of fmt as quantize_block writes them. The activations are not quantized: products of BF16
+ * with the codes' exact values, fp32 sums, y rounded once. ids, weights [tokens][top_k] as route_experts gives them; an
+ * id outside [0, experts) adds nothing, one that a token has twice counts with the sum of its weights. The same
+ * call gives the same bits. tokens <= 64, tokens * top_k <= 1024, experts <= 1024, top_k <= 64; dim, hidden
+ * multiples of 16 and <= 32768. Tensors and ws 16-byte aligned, scales, ids and weights 4-byte; y overlaps no input.
+ * ws: expert_layer_tokens_workspace_bytes() bytes, no initialisation. */
+size_t expert_layer_tokens_workspace_bytes(int64_t tokens, int top_k, int64_t hidden);
+qf8_status expert_layer_tokens(const void *x, int64_t tokens, int64_t dim, const uint8_t *w1, const float *s1,
+                               const uint8_t *w2, const float *s2, int experts, int64_t hidden, qf8_fmt fmt, qf8_act act,
+                               const int32_t *ids, const float *weights, int top_k, void *y, void *ws, size_t ws_bytes,
+                               void *stream);
+
+/* Norm over all gradients of a step, and the gradients scaled down to a largest norm:
+ *   N = sqrt(sum g^2),  c = min(1, max_norm / (N + 1e-6)),  out = rnd(g fl32(c)).
+ * grads: count host entries (read before the call returns); each tensor has n >= 0 values of its dtype at g and writes n
+ * values of the same type to out, which may be g itself; with out NULL in every entry (or in none) only the norm is
+ * computed. N is summed in fp64 in a fixed order. norm (nullable): N as one fp32. Where N is Inf or NaN the factor is 1
+ * and nonfinite (nullable) is set. max_norm > 0. Tensors at the alignment of their type (those at 16 bytes are
+ * read faster); out overlaps no g but its own. count <= 2^20, n < 2^36.
+ * ws: clip_grads_workspace_bytes() bytes, 16-byte aligned, no initialisation. */
+typedef struct qf8_grad {
+    const void *g;
+    void *out;
+    int64_t n;
+    int32_t dtype;               /* qf8_dtype */
+    int32_t reserved;            /* 0 */
+} qf8_grad;
+
+size_t clip_grads_workspace_bytes(const qf8_grad *grads, int count);
+qf8_status clip_grads(const qf8_grad *grads, int count, float max_norm, float *norm, int32_t *nonfinite, void *ws,
+                      size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

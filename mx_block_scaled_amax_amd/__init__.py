@@ -10,6 +10,9 @@ Formats: ``E4M3`` (max 448) and ``E5M2`` (max 57344), OCP encodings. Inputs: ``t
 or ``torch.float32`` CUDA tensors, contiguous, 2-D ``[rows, cols]`` (1-D tensors count as one
 row). Outputs are ``torch.uint8`` tensors of raw fp8 / E8M0 bytes.
 """
+import array
+import collections
+import contextlib
 import ctypes
 import functools
 import os
@@ -26,6 +29,8 @@ __all__ = [
     "WEIGHT_NK", "WEIGHT_KN", "GROUPS_NK", "SCORE_SOFTMAX", "SCORE_SIGMOID",
     "matmul_block", "matmul_block_experts", "matmul_block_experts_wgrad",
     "route_experts", "route_experts_backward", "order_experts", "combine_experts", "combine_experts_backward",
+    "ACT_SILU", "ACT_GELU", "rms_norm_quantize", "rms_norm_backward", "gated_act_quantize", "gated_act_backward",
+    "expert_layer_tokens", "grad_norm", "clip_grads",
 ]
 
 E4M3, E5M2 = 0, 1
@@ -36,6 +41,7 @@ EST_MAX, EST_RECENT, EST_MEAN = 0, 1, 2   # delayed-scaling estimators (qf8_esti
 DELAYED_SPLIT_AMAX = 1                    # qf8_delayed_flags
 WEIGHT_NK, WEIGHT_KN, GROUPS_NK = 0, 1, 2  # qf8_operand: layout of the second operand of a product
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1       # qf8_score
+ACT_SILU, ACT_GELU = 0, 1                 # qf8_act
 _BF16, _FP32 = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -104,6 +110,16 @@ def _load():
         "order_experts": (i32, [vp, i64, i32, i32, i32, vp, vp, i64, vp, vp, sz, vp]),
         "combine_experts": (i32, [vp, i32, i64, i64, vp, vp, i64, i32, vp, vp]),
         "combine_experts_backward": (i32, [vp, vp, i32, i64, i64, vp, vp, vp, i64, i32, vp, vp, vp]),
+        "rms_norm_quantize": (i32, [vp, i32, vp, i32, vp, i32, i64, i64, ctypes.c_float, i32, i32, vp, vp, vp, vp, vp, vp,
+                                    vp]),
+        "rms_norm_backward_workspace_bytes": (sz, [i64, i64]),
+        "rms_norm_backward": (i32, [vp, i32, vp, i32, vp, vp, i32, vp, i64, i64, vp, vp, vp, sz, vp]),
+        "gated_act_quantize": (i32, [vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp]),
+        "gated_act_backward": (i32, [vp, vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp]),
+        "expert_layer_tokens_workspace_bytes": (sz, [i64, i32, i64]),
+        "expert_layer_tokens": (i32, [vp, i64, i64, vp, vp, vp, vp, i32, i64, i32, i32, vp, vp, i32, vp, vp, sz, vp]),
+        "clip_grads_workspace_bytes": (sz, [vp, i32]),
+        "clip_grads": (i32, [vp, i32, ctypes.c_float, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)
@@ -761,3 +777,220 @@ def combine_experts_backward(dy, x, weights, slots, rows, dx=None, dweights=None
                                             slots.data_ptr(), rows.data_ptr(), tokens, top_k, dx.data_ptr(),
                                             dweights.data_ptr(), _stream_of(stream, x)), "combine_experts_backward")
     return dx, dweights
+
+
+# ---- around the expert layer ---------------------------------------------------------------------
+
+_current_device = torch.cuda.current_device
+
+
+def _on(device):
+    """The kernels run on the current device: the tensors' one for the time of a call."""
+    return _NOTHING if device == _current_device() else torch.cuda.device(device)
+
+
+_NOTHING = contextlib.nullcontext()
+
+NormResult = collections.namedtuple("NormResult", "q scales h y rstd")
+
+
+def _flag(nonfinite, device):
+    if nonfinite is not None:
+        _need(nonfinite, "nonfinite", torch.int32, (1,), device)
+    return _address(nonfinite)
+
+
+def rms_norm_quantize(x, weight, fmt, residual=None, eps=1e-6, pow2_scales=False, want_y=False, want_rstd=False, q=None,
+                      scales=None, h=None, y=None, rstd=None, nonfinite=None, stream=None):
+    """Root-mean-square norm of x [rows][cols] plus the residual, in FP8 codes with 1x128 scales. x and the residual
+    BF16 or FP32; h, their sum in the residual's type, may be given as the residual itself (then it is added in
+    place). fmt None: no codes, y alone. want_y: also the result in x's type; want_rstd: 1 / root mean square of each row,
+    for the backward pass. Returns (q, scales, h, y, rstd) by name, None for what is not asked for (h is x without a
+    residual)."""
+    dtype = _in_code(x, "x")
+    rows, cols = _need(x, "x", x.dtype, 2)
+    device = x.get_device()
+    w_dtype = _in_code(weight, "weight")
+    _need(weight, "weight", weight.dtype, (cols,), device)
+    r_dtype = dtype
+    if residual is not None:
+        r_dtype = _in_code(residual, "residual")
+        _need(residual, "residual", residual.dtype, (rows, cols), device)
+        h = _place(h, (rows, cols), residual.dtype, x, "h", stream)
+    elif h is not None:
+        raise ValueError("h is written only with a residual")
+    if fmt is not None:
+        q = _place(q, (rows, cols), torch.uint8, x, "q", stream)
+        scales = _place(scales, (rows, -(-cols // 128)), torch.float32, x, "scales", stream)
+    elif q is not None or scales is not None:
+        raise ValueError("q and scales need a format")
+    if want_y or y is not None or fmt is None:
+        y = _place(y, (rows, cols), x.dtype, x, "y", stream)
+    if want_rstd or rstd is not None:
+        rstd = _place(rstd, (rows,), torch.float32, x, "rstd", stream)
+    with _on(device):
+        _check(_load().rms_norm_quantize(x.data_ptr(), dtype, _address(residual), r_dtype, weight.data_ptr(), w_dtype, rows,
+                                         cols, eps, 0 if fmt is None else fmt, FLAG_POW2_SCALES if pow2_scales else 0,
+                                         _address(q), _address(scales), _address(h), _address(y), _address(rstd),
+                                         _flag(nonfinite, device), _stream_of(stream, x)), "rms_norm_quantize")
+    return NormResult(q, scales, x if residual is None else h, y, rstd)
+
+
+def rms_norm_backward(dy, h, rstd, weight, dres=None, want_dweight=True, dx=None, dweight=None, ws=None, stream=None):
+    """Gradients of rms_norm_quantize's y from dy [rows][cols]: (dx, dweight). h and rstd are those of the forward
+    pass; dres (h's type): the gradient that reaches h past the norm, added to dx, which may be dres itself. dx, of h's
+    type, is the gradient of x and of the residual; dweight is float32, None unless wanted."""
+    dtype = _in_code(dy, "dy")
+    rows, cols = _need(dy, "dy", dy.dtype, 2)
+    device = dy.get_device()
+    h_dtype, w_dtype = _in_code(h, "h"), _in_code(weight, "weight")
+    _need(h, "h", h.dtype, (rows, cols), device)
+    _need(rstd, "rstd", torch.float32, (rows,), device)
+    _need(weight, "weight", weight.dtype, (cols,), device)
+    if dres is not None:
+        _need(dres, "dres", h.dtype, (rows, cols), device)
+    dx = _place(dx, (rows, cols), h.dtype, dy, "dx", stream)
+    if want_dweight or dweight is not None:
+        dweight = _place(dweight, (cols,), torch.float32, dy, "dweight", stream)
+        ws = _workspace(ws, dy, stream, "rms_norm_backward_workspace_bytes", rows, cols)
+    with _on(device):
+        _check(_load().rms_norm_backward(dy.data_ptr(), dtype, h.data_ptr(), h_dtype, rstd.data_ptr(), weight.data_ptr(),
+                                         w_dtype, _address(dres), rows, cols, dx.data_ptr(), _address(dweight),
+                                         _address(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                         _stream_of(stream, dy)), "rms_norm_backward")
+    return dx, dweight
+
+
+def _halves(x):
+    rows, both = _need(x, "x", x.dtype, 2)
+    if both % 2:
+        raise ValueError(f"x must have two halves of columns, got {both}")
+    return rows, both // 2
+
+
+def gated_act_quantize(x, fmt, act=ACT_SILU, pow2_scales=False, want_y=False, q=None, scales=None, y=None, nonfinite=None,
+                       stream=None):
+    """act(a) * b for x = [a | b], x [rows][2 cols] BF16 or FP32: codes [rows][cols] with 1x128 scales, and with want_y
+    the values in x's type; fmt None: the values alone. Returns (q, scales, y), None for what is not asked for."""
+    dtype = _in_code(x, "x")
+    rows, cols = _halves(x)
+    device = x.get_device()
+    if fmt is not None:
+        q = _place(q, (rows, cols), torch.uint8, x, "q", stream)
+        scales = _place(scales, (rows, -(-cols // 128)), torch.float32, x, "scales", stream)
+    elif q is not None or scales is not None:
+        raise ValueError("q and scales need a format")
+    if want_y or y is not None or fmt is None:
+        y = _place(y, (rows, cols), x.dtype, x, "y", stream)
+    with _on(device):
+        _check(_load().gated_act_quantize(x.data_ptr(), dtype, rows, cols, act, 0 if fmt is None else fmt,
+                                          FLAG_POW2_SCALES if pow2_scales else 0, _address(q), _address(scales), _address(y),
+                                          _flag(nonfinite, device), _stream_of(stream, x)), "gated_act_quantize")
+    return q, scales, y
+
+
+def gated_act_backward(dy, x, fmt, act=ACT_SILU, pow2_scales=False, want_dx=False, q=None, scales=None, dx=None,
+                       nonfinite=None, stream=None):
+    """Gradients of both halves of x [rows][2 cols] from dy [rows][cols] of its type: codes [rows][2 cols] with 1x128
+    scales (cols a multiple of 128), and with want_dx the values in x's type; fmt None: the values alone. Returns
+    (q, scales, dx), None for what is not asked for."""
+    dtype = _in_code(x, "x")
+    rows, cols = _halves(x)
+    device = x.get_device()
+    _need(dy, "dy", x.dtype, (rows, cols), device)
+    if fmt is not None:
+        q = _place(q, (rows, 2 * cols), torch.uint8, x, "q", stream)
+        scales = _place(scales, (rows, 2 * -(-cols // 128)), torch.float32, x, "scales", stream)
+    elif q is not None or scales is not None:
+        raise ValueError("q and scales need a format")
+    if want_dx or dx is not None or fmt is None:
+        dx = _place(dx, (rows, 2 * cols), x.dtype, x, "dx", stream)
+    with _on(device):
+        _check(_load().gated_act_backward(dy.data_ptr(), x.data_ptr(), dtype, rows, cols, act, 0 if fmt is None else fmt,
+                                          FLAG_POW2_SCALES if pow2_scales else 0, _address(q), _address(scales),
+                                          _address(dx), _flag(nonfinite, device), _stream_of(stream, x)), "gated_act_backward")
+    return q, scales, dx
+
+
+def expert_layer_tokens(x, w1, s1, w2, s2, ids, weights, fmt, act=ACT_SILU, y=None, ws=None, stream=None):
+    """A whole expert layer for at most 64 tokens: y[t] = sum_j weights[t][j] W2[e] (act(A x[t]) * (B x[t])) with
+    W1[e] = [A; B] and e = ids[t][j] (an id outside the experts adds nothing). x [tokens][dim] bfloat16; w1 codes [experts]
+    [2 hidden][dim] and w2 codes [experts][dim][hidden] with their 128x128 scales; ids and weights as route_experts gives
+    them. The activations are not quantized. Returns y [tokens][dim] bfloat16."""
+    tokens, dim = _need(x, "x", torch.bfloat16, 2)
+    device = x.get_device()
+    experts, both, d1 = _need(w1, "w1", torch.uint8, 3, device)
+    if d1 != dim or both % 2:
+        raise ValueError(f"w1 must be [experts][2 hidden][{dim}], got {tuple(w1.shape)}")
+    hidden = both // 2
+    _need(w2, "w2", torch.uint8, (experts, dim, hidden), device)
+    _need(s1, "s1", torch.float32, (experts, -(-both // 128), -(-dim // 128)), device)
+    _need(s2, "s2", torch.float32, (experts, -(-dim // 128), -(-hidden // 128)), device)
+    t, top_k = _need(ids, "ids", torch.int32, 2, device)
+    if t != tokens:
+        raise ValueError(f"ids must have {tokens} rows, got {t}")
+    _need(weights, "weights", torch.float32, (tokens, top_k), device)
+    y = _place(y, (tokens, dim), torch.bfloat16, x, "y", stream)
+    ws = _workspace(ws, x, stream, "expert_layer_tokens_workspace_bytes", tokens, top_k, hidden)
+    with _on(device):
+        _check(_load().expert_layer_tokens(x.data_ptr(), tokens, dim, w1.data_ptr(), s1.data_ptr(), w2.data_ptr(),
+                                           s2.data_ptr(), experts, hidden, fmt, act, ids.data_ptr(), weights.data_ptr(),
+                                           top_k, y.data_ptr(), _address(ws),
+                                           0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, x)),
+               "expert_layer_tokens")
+    return y
+
+
+def _clip(grads, out, max_norm, norm, nonfinite, ws, stream, what):
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients given")
+    like = grads[0]
+    entries = array.array("q")
+    device = None
+    for i, g in enumerate(grads):
+        code = _in_code(g, f"grads[{i}]")
+        if not g.is_cuda or not g.is_contiguous() or g.get_device() != device:
+            _need(g, f"grads[{i}]", g.dtype, g.shape, device)       # the first tensor's device is that of all
+            device = g.get_device()
+        at = g.data_ptr()
+        to = 0
+        if out is not None:
+            o = out[i]
+            if o is g:
+                to = at
+            else:
+                _need(o, f"out[{i}]", g.dtype, g.shape, device)
+                to = o.data_ptr()
+        entries.extend((at, to, g.numel(), code))
+    norm = _place(norm, (1,), torch.float32, like, "norm", stream)
+    lib, where, count = _load(), entries.buffer_info()[0], len(grads)
+    need = lib.clip_grads_workspace_bytes(where, count)
+    if ws is not None:
+        _same_device(_dev_tensor(ws, "ws"), "ws", device)
+    else:
+        ws = _fresh(like, (need,), torch.uint8, stream)
+    with _on(device):
+        _check(lib.clip_grads(where, count, max_norm, norm.data_ptr(), _flag(nonfinite, device), ws.data_ptr(),
+                              ws.numel() * ws.element_size(), _stream_of(stream, like)), what)
+    return norm
+
+
+def grad_norm(grads, norm=None, nonfinite=None, ws=None, stream=None):
+    """sqrt of the sum of all squares of the tensors grads (BF16 or FP32, any shapes, contiguous), summed in fp64: a
+    float32 tensor of one element."""
+    return _clip(grads, None, float("inf"), norm, nonfinite, ws, stream, "grad_norm")
+
+
+def clip_grads(grads, max_norm, out=None, norm=None, nonfinite=None, ws=None, stream=None):
+    """Scales the tensors grads by min(1, max_norm / (N + 1e-6)), N their grad_norm, in place or into the tensors out
+    of the same shapes and types. Where N is not finite they are left as they are (copied to out) and nonfinite,
+    an int32 tensor of one element, is set to 1. Returns N, a float32 tensor of one element; nothing is read back to the host."""
+    grads = list(grads)
+    if out is None:
+        out = grads
+    else:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"out must have {len(grads)} tensors, got {len(out)}")
+    return _clip(grads, out, max_norm, norm, nonfinite, ws, stream, "clip_grads")

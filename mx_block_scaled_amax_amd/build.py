@@ -11,8 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqf8.so")
 SOURCES = ["qf8_api.cpp", "qf8_tensor.hip", "qf8_block.hip", "qf8_mx.hip", "qf8_dequant.hip", "qf8_requant.hip", "qf8_fp4.hip",
-           "qf8_experts.hip", "qf8_matmul.hip", "qf8_matmul_e4m3_e4m3.hip", "qf8_matmul_e4m3_e5m2.hip",
-           "qf8_matmul_e5m2_e4m3.hip", "qf8_matmul_e5m2_e5m2.hip"]
+           "qf8_experts.hip", "qf8_norm.hip", "qf8_gate.hip", "qf8_layer.hip", "qf8_clip.hip", "qf8_matmul.hip",
+           "qf8_matmul_e4m3_e4m3.hip", "qf8_matmul_e4m3_e5m2.hip", "qf8_matmul_e5m2_e4m3.hip", "qf8_matmul_e5m2_e5m2.hip"]
 ARCH = "gfx950"
 
 

@@ -631,3 +631,173 @@ qf8_status combine_experts_backward(const void *dy, const void *x, qf8_dtype dty
 }
 
 }  // extern "C"
+
+// ---- around the expert layer ---------------------------------------------------------------------
+namespace {
+inline bool act_ok(int act) { return act == QF8_ACT_SILU || act == QF8_ACT_GELU; }
+
+// the sizes of a norm's rows, forward and backward
+inline bool norm_dims_ok(int64_t rows, int64_t cols) {
+    return dims_ok(rows, cols) && cols % 8 == 0 && cols <= qf8::kMaxNormCols;
+}
+
+// gated activation: n columns of results, in one run (forward) or two
+int check_gate(const void *dy, const void *x, int dtype, int64_t rows, int64_t cols, int act, int fmt, int flags,
+               const uint8_t *q, const float *scales, const void *y, const int32_t *nonfinite, int backward) {
+    if (!dtype_ok(dtype) || !act_ok(act) || (q && !fmt_ok(fmt)) || (flags & ~QF8_FLAG_POW2_SCALES)) return QF8_ERR_ENUM;
+    if (rows < 0 || cols < 0 || cols % 8 != 0 || cols >= (int64_t)1 << 30 || rows >= (int64_t)1 << 31 ||
+        rows * ((cols + 127) / 128) >= (int64_t)1 << 31)
+        return QF8_ERR_SHAPE;
+    if (backward && q && cols % 128 != 0) return QF8_ERR_SHAPE;
+    if (rows * cols == 0) return QF8_OK;
+    if (!x || (backward && !dy) || !q != !scales || (!q && !y)) return QF8_ERR_NULL;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(q, 16) || !aligned(y, 16) || !aligned(scales, 4) ||
+        !aligned(nonfinite, 4))
+        return QF8_ERR_ALIGN;
+    return QF8_OK;
+}
+
+int gate(const void *dy, const void *x, int dtype, int64_t rows, int64_t cols, int act, int fmt, int flags, uint8_t *q,
+         float *scales, void *y, int32_t *nonfinite, int backward, void *stream) {
+    const int c = check_gate(dy, x, dtype, rows, cols, act, fmt, flags, q, scales, y, nonfinite, backward);
+    if (c != QF8_OK || rows * cols == 0) return c;
+    qf8::GateArgs p = {};
+    p.x = x; p.dy = dy; p.y = y; p.q = q; p.scales = scales; p.nonfinite = nonfinite;
+    p.cols = cols;
+    p.gcols = (uint32_t)((cols + 127) / 128);
+    p.groups = (uint32_t)rows * p.gcols;
+    p.fmt = fmt; p.pow2 = flags & QF8_FLAG_POW2_SCALES;
+    return qf8::launch_gate(p, dtype, act, backward, as_stream(stream));
+}
+
+// -1: refused
+int64_t clip_workspace(const qf8_grad *grads, int count) {
+    if (count < 0 || count > 1 << 20 || (count > 0 && !grads)) return -1;
+    int64_t chunks = 0;
+    for (int i = 0; i < count; ++i) {
+        if (grads[i].n < 0 || grads[i].n >= (int64_t)1 << 36) return -1;
+        chunks += qf8::clip_chunks(grads[i].n);
+    }
+    return (chunks * 8 + 15) / 16 * 16 + 16;
+}
+}  // namespace
+
+extern "C" {
+
+qf8_status rms_norm_quantize(const void *x, qf8_dtype dtype, const void *residual, qf8_dtype residual_dtype,
+                             const void *weight, qf8_dtype weight_dtype, int64_t rows, int64_t cols, float eps, qf8_fmt fmt,
+                             int flags, uint8_t *q, float *scales, void *h, void *y, float *rstd, int32_t *nonfinite,
+                             void *stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || (residual && !dtype_ok(residual_dtype)) || (q && !fmt_ok(fmt)) ||
+        (flags & ~QF8_FLAG_POW2_SCALES))
+        return QF8_ERR_ENUM;
+    if (!norm_dims_ok(rows, cols) || !(eps > 0.0f) || !(eps <= 3.40282346638528859812e+38f)) return QF8_ERR_SHAPE;
+    if (rows * cols == 0) return QF8_OK;
+    if (!x || !weight || !q != !scales || (!q && !y) || (residual && !h)) return QF8_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(q, 16) || !aligned(h, 16) ||
+        !aligned(y, 16) || !aligned(scales, 4) || !aligned(rstd, 4) || !aligned(nonfinite, 4))
+        return QF8_ERR_ALIGN;
+    qf8::NormArgs p = {};
+    p.x = x; p.residual = residual; p.weight = weight; p.q = q; p.scales = scales; p.h = h; p.y = y; p.rstd = rstd;
+    p.nonfinite = nonfinite;
+    p.rows = rows; p.cols = cols; p.gcols = (cols + 127) / 128;
+    p.eps = eps;
+    p.w_fp32 = weight_dtype == QF8_IN_FP32;
+    p.fmt = fmt; p.pow2 = flags & QF8_FLAG_POW2_SCALES;
+    return status_of(qf8::launch_norm(p, dtype, residual_dtype, as_stream(stream)));
+}
+
+size_t rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+    return norm_dims_ok(rows, cols) ? (size_t)(qf8::norm_backward_groups(rows, cols) * cols * 4) : 0;
+}
+
+qf8_status rms_norm_backward(const void *dy, qf8_dtype dtype, const void *h, qf8_dtype h_dtype, const float *rstd,
+                             const void *weight, qf8_dtype weight_dtype, const void *dres, int64_t rows, int64_t cols,
+                             void *dx, float *dweight, void *ws, size_t ws_bytes, void *stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(h_dtype) || !dtype_ok(weight_dtype)) return QF8_ERR_ENUM;
+    if (!norm_dims_ok(rows, cols)) return QF8_ERR_SHAPE;
+    if (cols == 0 || (rows == 0 && !dweight)) return QF8_OK;
+    if (rows > 0 && (!dy || !h || !rstd || !weight || !dx)) return QF8_ERR_NULL;
+    const size_t need = dweight ? rms_norm_backward_workspace_bytes(rows, cols) : 0;
+    if (need > 0 && (!ws || ws_bytes < need)) return QF8_ERR_WORKSPACE;
+    if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(dres, 16) || !aligned(dx, 16) ||
+        !aligned(ws, 16) || !aligned(rstd, 4) || !aligned(dweight, 4))
+        return QF8_ERR_ALIGN;
+    qf8::NormArgs p = {};
+    p.dy = dy; p.hin = h; p.rstd_in = rstd; p.weight = weight; p.dres = dres; p.dx = dx;
+    p.partial = dweight ? (float *)ws : nullptr;
+    p.rows = rows; p.cols = cols;
+    p.w_fp32 = weight_dtype == QF8_IN_FP32;
+    return status_of(qf8::launch_norm_backward(p, dtype, h_dtype, dweight, as_stream(stream)));
+}
+
+qf8_status gated_act_quantize(const void *x, qf8_dtype dtype, int64_t rows, int64_t cols, qf8_act act, qf8_fmt fmt, int flags,
+                              uint8_t *q, float *scales, void *y, int32_t *nonfinite, void *stream) {
+    return status_of(gate(nullptr, x, dtype, rows, cols, act, fmt, flags, q, scales, y, nonfinite, 0, stream));
+}
+
+qf8_status gated_act_backward(const void *dy, const void *x, qf8_dtype dtype, int64_t rows, int64_t cols, qf8_act act,
+                              qf8_fmt fmt, int flags, uint8_t *q, float *scales, void *dx, int32_t *nonfinite, void *stream) {
+    return status_of(gate(dy, x, dtype, rows, cols, act, fmt, flags, q, scales, dx, nonfinite, 1, stream));
+}
+
+static bool layer_dims_ok(int64_t tokens, int top_k, int64_t hidden) {
+    return tokens >= 0 && tokens <= qf8::kLayerTokens && top_k >= 1 && top_k <= qf8::kMaxTopK &&
+           tokens * top_k <= qf8::kLayerChoices && hidden >= 0 && hidden % 16 == 0 && hidden <= qf8::kMaxLayerDim;
+}
+
+size_t expert_layer_tokens_workspace_bytes(int64_t tokens, int top_k, int64_t hidden) {
+    return layer_dims_ok(tokens, top_k, hidden) ? qf8::layer_workspace(tokens, top_k, hidden) : 0;
+}
+
+qf8_status expert_layer_tokens(const void *x, int64_t tokens, int64_t dim, const uint8_t *w1, const float *s1,
+                               const uint8_t *w2, const float *s2, int experts, int64_t hidden, qf8_fmt fmt, qf8_act act,
+                               const int32_t *ids, const float *weights, int top_k, void *y, void *ws, size_t ws_bytes,
+                               void *stream) {
+    if (!fmt_ok(fmt) || !act_ok(act)) return QF8_ERR_ENUM;
+    if (!layer_dims_ok(tokens, top_k, hidden) || dim < 0 || dim % 16 != 0 || dim > qf8::kMaxLayerDim || experts < 1 ||
+        experts > qf8::kMaxExperts)
+        return QF8_ERR_SHAPE;
+    if (tokens == 0 || dim == 0) return QF8_OK;
+    if (!x || !ids || !weights || !y || (hidden > 0 && (!w1 || !s1 || !w2 || !s2))) return QF8_ERR_NULL;
+    if (!ws || ws_bytes < qf8::layer_workspace(tokens, top_k, hidden)) return QF8_ERR_WORKSPACE;
+    if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(y, 16) || !aligned(ws, 16) || !aligned(s1, 4) ||
+        !aligned(s2, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+        return QF8_ERR_ALIGN;
+    qf8::LayerArgs p = {};
+    p.x = (const uint16_t *)x; p.w1 = w1; p.s1 = s1; p.w2 = w2; p.s2 = s2; p.ids = ids; p.weights = weights;
+    p.y = (uint16_t *)y;
+    p.tokens = (int)tokens; p.top_k = top_k; p.experts = experts; p.dim = (int)dim; p.hidden = (int)hidden;
+    return status_of(qf8::launch_layer(p, fmt, act, ws, as_stream(stream)));
+}
+
+size_t clip_grads_workspace_bytes(const qf8_grad *grads, int count) {
+    const int64_t need = clip_workspace(grads, count);
+    return need < 0 ? 0 : (size_t)need;
+}
+
+qf8_status clip_grads(const qf8_grad *grads, int count, float max_norm, float *norm, int32_t *nonfinite, void *ws,
+                      size_t ws_bytes, void *stream) {
+    if (count > 0 && !grads) return QF8_ERR_NULL;
+    const int64_t need = clip_workspace(grads, count);
+    if (need < 0 || !(max_norm > 0.0f)) return QF8_ERR_SHAPE;
+    int written = 0, held = 0;
+    for (int i = 0; i < count; ++i) {
+        const qf8_grad &g = grads[i];
+        if (!dtype_ok(g.dtype)) return QF8_ERR_ENUM;
+        if (g.n == 0) continue;
+        if (!g.g) return QF8_ERR_NULL;
+        const uintptr_t a = g.dtype == QF8_IN_FP32 ? 4 : 2;
+        if (!aligned(g.g, a) || !aligned(g.out, a)) return QF8_ERR_ALIGN;
+        ++held;
+        written += g.out != nullptr;
+    }
+    if (written != 0 && written != held) return QF8_ERR_NULL;
+    if (!norm && written == 0 && !nonfinite) return QF8_OK;
+    if (!ws || ws_bytes < (size_t)need) return QF8_ERR_WORKSPACE;
+    if (!aligned(ws, 16) || !aligned(norm, 4) || !aligned(nonfinite, 4)) return QF8_ERR_ALIGN;
+    return status_of(qf8::launch_clip(grads, count, max_norm, written > 0, norm, (float *)ws, (double *)((char *)ws + 16),
+                                      nonfinite, as_stream(stream)));
+}
+
+}  // extern "C"

@@ -146,4 +146,69 @@ struct CombineArgs {
 };
 int launch_combine(const CombineArgs &p, int dtype, int backward, hipStream_t s);
 
+// Norm of a residual stream with FP8 codes, and its gradients.
+constexpr int64_t kMaxNormCols = 16384;
+struct NormArgs {
+    const void *x, *residual, *weight;
+    uint8_t *q;
+    float *scales, *rstd;
+    void *h, *y;
+    int32_t *nonfinite;
+    const void *dy, *hin, *dres; // backward pass
+    const float *rstd_in;
+    void *dx;
+    float *partial;              // [norm_backward_groups][cols]
+    int64_t rows, cols, gcols;
+    float eps;
+    int w_fp32, fmt, pow2;
+};
+int launch_norm(const NormArgs &p, int dtype, int residual_dtype, hipStream_t s);
+int64_t norm_backward_groups(int64_t rows, int64_t cols);
+int launch_norm_backward(const NormArgs &p, int dtype, int h_dtype, float *dw, hipStream_t s);
+
+// Gated activation with FP8 codes, and its gradients.
+struct GateArgs {
+    const void *x, *dy;
+    void *y;                     // the result, or the halves' gradients
+    uint8_t *q;
+    float *scales;
+    int32_t *nonfinite;
+    int64_t cols;
+    uint32_t gcols, groups;      // groups of a row's half, and of all rows
+    int fmt, pow2;
+};
+int launch_gate(const GateArgs &p, int dtype, int act, int backward, hipStream_t s);
+
+// A whole expert layer for a few tokens.
+constexpr int kLayerTokens = 64, kLayerChoices = 1024, kMaxLayerDim = 32768;
+struct LayerArgs {
+    const uint16_t *x;
+    const uint8_t *w1, *w2;
+    const float *s1, *s2;
+    const int32_t *ids;
+    const float *weights;
+    uint16_t *y;
+    int tokens, top_k, experts, dim, hidden;
+    uint16_t *a;                 // workspace: activations [choice][hidden], and the list of jobs
+    uint32_t *jobs, *entries;
+    float *entry_weights;
+    int *job_count;
+};
+size_t layer_workspace(int64_t tokens, int top_k, int64_t hidden);
+int launch_layer(const LayerArgs &p, int fmt, int act, void *ws, hipStream_t s);
+
+// Norm over many tensors, and scaling to a largest norm. The tensors of a launch travel in its arguments.
+constexpr int kClipTensors = 128;
+constexpr int64_t kMaxClipGrid = (int64_t)1 << 23;       // threads of a launch are counted in 32 bits
+struct ClipBatch {
+    const void *g[kClipTensors];
+    void *out[kClipTensors];
+    int64_t size[kClipTensors];  // values * 2 + (FP32)
+    uint32_t first[kClipTensors];
+    int count;
+};
+int64_t clip_chunks(int64_t n);
+int launch_clip(const qf8_grad *grads, int count, float max_norm, int write, float *norm, float *factor, double *partial,
+                int32_t *nonfinite, hipStream_t s);
+
 }  // namespace qf8
