@@ -9,7 +9,7 @@
 // times up to sixteen tokens); a 128x128 block's sums meet 1/S in fp32. The activations are not quantized.
 //
 // Every workgroup of the first kernel sorts the choices by expert on its own (in LDS, at most 1024 of them); the first
-// one leaves the list, cut into jobs of up to 16 NT tokens of an expert, in the workspace for the second kernel.
+// one leaves the list, cut into pieces of up to sixteen tokens of an expert, in the workspace for the second kernel.
 #include <type_traits>
 
 #include "qf8_act.h"
@@ -23,12 +23,15 @@ typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
 typedef float v4f32 __attribute__((ext_vector_type(4)));
 
 // ---- jobs ---------------------------------------------------------------------------------------
-// A job in 32 bits: expert (10), first entry (11), entries - 1 (6). An entry: choice t * top_k + j (16) and token.
-constexpr int kMaxJobs = kLayerChoices;              // a job has an entry at least
-__device__ __forceinline__ uint32_t pack_job(int e, int start, int n) { return (uint32_t)(e | start << 10 | (n - 1) << 21); }
+// A job in 32 bits: expert (10), first entry (10), entries - 1 (6). A piece of one, up to sixteen entries, has its number
+// in the job and the number of the job's pieces - 1 too (2 each). An entry: choice t * top_k + j (16) and token.
+constexpr int kMaxJobs = kLayerChoices;              // a job, and a piece, has an entry at least
+__device__ __forceinline__ uint32_t pack_job(int e, int start, int n) { return (uint32_t)(e | start << 10 | (n - 1) << 20); }
 __device__ __forceinline__ int job_expert(uint32_t j) { return (int)(j & 1023); }
-__device__ __forceinline__ int job_start(uint32_t j) { return (int)(j >> 10 & 2047); }
-__device__ __forceinline__ int job_count(uint32_t j) { return (int)(j >> 21) + 1; }
+__device__ __forceinline__ int job_start(uint32_t j) { return (int)(j >> 10 & 1023); }
+__device__ __forceinline__ int job_count(uint32_t j) { return (int)(j >> 20 & 63) + 1; }
+__device__ __forceinline__ int piece_number(uint32_t j) { return (int)(j >> 26 & 3); }
+__device__ __forceinline__ int piece_total(uint32_t j) { return (int)(j >> 28 & 3) + 1; }
 
 struct Jobs {
     uint32_t job[kMaxJobs];          // one for each chosen expert, with all its entries
@@ -40,9 +43,9 @@ struct Jobs {
 
 // All threads of the workgroup; ends with a barrier. The order of an expert's entries is this workgroup's own: what
 // leaves it (activations) is placed by choice. A token that names an expert twice has one entry, at its first choice.
-// cut: the jobs of up to per_job entries go to p.jobs, their number to p.job_count.
+// cut: the pieces go to p.jobs, their number to p.job_count.
 template <int THREADS>
-__device__ void find_jobs(const LayerArgs &p, bool cut, int per_job, Jobs &s) {
+__device__ void find_jobs(const LayerArgs &p, bool cut, Jobs &s) {
     const int n = p.tokens * p.top_k;
     for (int i = threadIdx.x; i < n; i += THREADS) {
         const int e = p.ids[i];
@@ -61,7 +64,7 @@ __device__ void find_jobs(const LayerArgs &p, bool cut, int per_job, Jobs &s) {
         int entries = 0, jobs = 0, pieces = 0;
         for (int base = 0; base < p.experts; base += 64) {
             const int e = base + (int)threadIdx.x;
-            const int c = e < p.experts ? s.start[e] : 0, q = (c + per_job - 1) / per_job;
+            const int c = e < p.experts ? s.start[e] : 0, q = (c + 15) / 16;
             int before = c, qbefore = q;              // inclusive sums over the lanes
 #pragma unroll
             for (int off = 1; off < 64; off <<= 1) {
@@ -73,7 +76,8 @@ __device__ void find_jobs(const LayerArgs &p, bool cut, int per_job, Jobs &s) {
             if (e < p.experts) s.start[e] = at;
             if (c > 0) s.job[jobs + __popcll(chosen & ((1ull << threadIdx.x) - 1))] = pack_job(e, at, c);
             for (int k = 0; cut && k < q; ++k)
-                p.jobs[pieces + qbefore - q + k] = pack_job(e, at + k * per_job, c - k * per_job < per_job ? c - k * per_job : per_job);
+                p.jobs[pieces + qbefore - q + k] =
+                    pack_job(e, at + k * 16, c - k * 16 < 16 ? c - k * 16 : 16) | (uint32_t)k << 26 | (uint32_t)(q - 1) << 28;
             entries += __shfl(before, 63);
             pieces += __shfl(qbefore, 63);
             jobs += __popcll(chosen);
@@ -114,47 +118,83 @@ __device__ __forceinline__ v8bf16 operand(uint32_t lo, uint32_t hi) {
     return v8bf16{p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y};
 }
 
-// 128 values of k for RT tiles of sixteen rows of a weight and NT of sixteen tokens. Lane (r, g) = (lane % 16,
-// lane / 16) holds k = 64 h + 16 g .. + 15 of row (token) r, h = 0, 1: two 16-byte loads of codes, four of BF16. The
-// products' own order of k is another one, the same for both operands.
-template <int RT, int NT>
-struct Step {
-    uint4 w[RT][2];
-    uint4 x[NT][4];
-};
+// 128 values of k for RT tiles of sixteen rows of a weight and up to sixteen tokens. Both are loaded in whole lines, a
+// weight eight rows to an instruction (lane l: chunk l % 8 of row l / 8), the tokens four (chunk l % 16 of token l / 16, as
+// many instructions as there are tokens for), and turned in LDS, 4 KB of a wave's own, into the products' layout: lane
+// (r, g) = (lane % 16, lane / 16) holds k = 64 h + 16 g .. + 15 of row (token) r, h = 0, 1. The products' own order of k
+// is another one, the same for both. Weights loaded straight into that layout, half a line of a row each, came at 5.7 TB/s
+// (6.3 cached) against 7.1 in a loop of loads alone (64 weights of 4096x7168); tokens loaded so took four
+// instructions where eight tokens need two, and the vector memory units were the bound of the second kernel.
+// Chunk c of row r, rows of 128 and of 256 bytes: sixteen lanes that read one chunk of sixteen rows, or that write whole
+// rows, meet no bank twice.
+__device__ __forceinline__ int chunk128(int r, int c) { return r * 128 + ((c ^ (r >> 1)) & 7) * 16; }
+__device__ __forceinline__ int chunk256(int r, int c) { return r * 256 + ((c ^ r) & 15) * 16; }
 
-template <int FMT, int RT, int NT>
-__device__ __forceinline__ void multiply(const Step<RT, NT> &s, const float (&inv)[RT], bool second, v4f32 (&acc)[RT][NT]) {
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        v8bf16 w[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            w[2 * h] = operand<FMT>(s.w[r][h].x, s.w[r][h].y);
-            w[2 * h + 1] = operand<FMT>(s.w[r][h].z, s.w[r][h].w);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (n > 0 && !second) continue;           // the same for the whole wave
-            v4f32 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[k], __builtin_bit_cast(v8bf16, s.x[n][k]), sum, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][n][i] = __builtin_fmaf(sum[i], inv[r], acc[r][n][i]);
-        }
-    }
+// The lane, computed where it is used: addresses that hang on it stay out of the registers of the loops around.
+__device__ __forceinline__ int lane_here() {
+    int lane = (int)(threadIdx.x & 63);
+    asm volatile("" : "+v"(lane));
+    return lane;
 }
 
-constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64;
+// Loaded rows into the products' layout, over the same LDS one after the other (a wave's LDS operations keep their
+// order); the registers they come from can be loaded again then.
+template <int RT>
+__device__ __forceinline__ void turn_weights(const uint4 (&w)[RT][2], char *tile, uint4 (&o)[RT][2]) {
+    const int lane = lane_here(), r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) *(uint4 *)(tile + t * 2048 + chunk128(8 * q + (lane >> 3), lane & 7)) = w[t][q];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) o[t][h] = *(const uint4 *)(tile + t * 2048 + chunk128(r, g + 4 * h));
+}
+__device__ __forceinline__ void place_tokens(const uint4 (&x)[4], int instructions, char *tile) {
+    const int lane = lane_here(), r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (q < instructions) *(uint4 *)(tile + chunk256(4 * q + g, r)) = x[q];
+}
+
+// Products of turned weights, tiles T0 on, with placed tokens, one half of the 128 values of k after the other (the fence keeps the
+// second half's operands out of the registers meanwhile). Tokens behind the last one are what LDS held: their columns are
+// not used.
+template <int FMT, int RT, int T0 = 0, int N>
+__device__ __forceinline__ void multiply(const uint4 (&w)[N][2], const char *tile, const float (&inv)[RT], v4f32 (&acc)[RT]) {
+    const int lane = lane_here(), r = lane & 15, g = lane >> 4;
+    v4f32 sum[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) sum[t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const v8bf16 x0 = *(const v8bf16 *)(tile + chunk256(r, 8 * h + 2 * g));
+        const v8bf16 x1 = *(const v8bf16 *)(tile + chunk256(r, 8 * h + 2 * g + 1));
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FMT>(w[T0 + t][h].x, w[T0 + t][h].y), x0, sum[t], 0, 0, 0);
+            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FMT>(w[T0 + t][h].z, w[T0 + t][h].w), x1, sum[t], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(sum[t][i], inv[t], acc[t][i]);
+}
+
+constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64, kUpGroups = 3;      // workgroups to a CU
 
 // A workgroup takes sixteen hidden units of a job, 16 rows of A_e and 16 of B_e; its waves share k, wave w the blocks
-// of 128 with index w mod 4, and their sums are joined in LDS in the order of the waves.
-template <int FMT, int ACT, int NT>
-__global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs p) {
+// of 128 with index w mod 4, and their sums are joined in LDS in the order of the waves. More than 32 tokens take another
+// pass over the rows.
+template <int FMT, int ACT>
+__global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerArgs p) {
     __shared__ Jobs jobs;
-    __shared__ float part[kUpWaves][2][NT][256];
-    find_jobs<kUpThreads>(p, blockIdx.x == 0, 16 * NT, jobs);
+    __shared__ __align__(16) char tile[kUpWaves][4096];          // at the end the sums of each wave, [2][2][256]
+    float(*part)[1024] = (float(*)[1024])tile;
+    find_jobs<kUpThreads>(p, blockIdx.x == 0, jobs);
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (blockIdx.x == 0) {
@@ -169,15 +209,16 @@ __global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs p) {
     }
     const int dim = p.dim, blocks = p.hidden / 16, gk = (dim + 127) / 128;
     const int gn = (2 * p.hidden + 127) / 128;
+    const int steps = (gk - wave + kUpWaves - 1) / kUpWaves;      // at most 64, an even number or one more taken
     const uint32_t items = (uint32_t)jobs.total * (uint32_t)blocks;
     const auto xr = make_rsrc(p.x, (uint32_t)p.tokens * (uint32_t)dim * 2u);
     for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
         const uint32_t job = jobs.job[item / (uint32_t)blocks];
         const int j0 = (int)(item % (uint32_t)blocks) * 16;
-        const int e = job_expert(job);
+        const int e = __builtin_amdgcn_readfirstlane(job_expert(job));
         const auto wr = make_rsrc(p.w1 + (int64_t)e * 2 * p.hidden * dim, 2u * (uint32_t)p.hidden * (uint32_t)dim);
         uint32_t wrow[2];
-        wrow[0] = (uint32_t)(j0 + r) * (uint32_t)dim + 16 * g;
+        wrow[0] = (uint32_t)(j0 + (lane >> 3)) * (uint32_t)dim + 16 * (lane & 7);
         wrow[1] = wrow[0] + (uint32_t)p.hidden * (uint32_t)dim;
         // 1 / S of this wave's i-th block in lane i
         float inv[2];
@@ -186,67 +227,91 @@ __global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs p) {
             const int b = wave + lane * kUpWaves;
             inv[q] = b < gk ? 1.0f / p.s1[((int64_t)e * gn + (q * p.hidden + j0) / 128) * gk + b] : 0.0f;
         }
-        for (int c0 = 0; c0 < job_count(job); c0 += 16 * NT) {
-            const int start = job_start(job) + c0, count = job_count(job) - c0;
-            uint32_t xrow[NT];
+        const int all = __builtin_amdgcn_readfirstlane(job_count(job));
+        for (int c0 = 0; c0 < all; c0 += 32) {
+            const int start = job_start(job) + c0, count = all - c0 < 32 ? all - c0 : 32;
+            // NX: instructions that load sixteen tokens, NC: sixteens of tokens, XS: steps that these are loaded ahead
+            const auto run = [&](auto nx, auto nc, auto xs) {
+                constexpr int NX = decltype(nx)::value, NC = decltype(nc)::value, XS = decltype(xs)::value;
+                uint32_t xrow[NC][NX];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int i = n * 16 + r;
-                xrow[n] = i < count ? (jobs.entry[start + i] >> 16) * (uint32_t)dim * 2u + 32 * g : kOutOfRange;
-            }
-            v4f32 acc[2][NT];
+                for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) acc[q][n] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
-            Step<2, NT> step[2];
-            const auto load = [&](Step<2, NT> &s, int i) {
-                const int k0 = (wave + i * kUpWaves) * 128;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const bool in = k0 + 64 * h + 16 * g < dim;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) s.w[q][h] = buf_load16<kNonTemporal>(wr, in ? wrow[q] + k0 + 64 * h : kOutOfRange, 0);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint32_t at = in && xrow[n] != kOutOfRange ? xrow[n] + 2 * (k0 + 64 * h) : kOutOfRange;
-                        s.x[n][2 * h] = buf_load16(xr, at, 0);
-                        s.x[n][2 * h + 1] = buf_load16(xr, at == kOutOfRange ? at : at + 16, 0);
+                    for (int q = 0; q < NX; ++q) {
+                        const int at = 16 * c + 4 * q + g;
+                        xrow[c][q] = at < count ? (jobs.entry[start + at] >> 16) * (uint32_t)dim * 2u + 16 * r : kOutOfRange;
                     }
+                v4f32 acc[NC][2];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) acc[c][0] = acc[c][1] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+                uint4 w[2][2][2], x[XS][4];
+                const auto load_w = [&](uint4 (&to)[2][2], int i) {
+                    const int k0 = (wave + i * kUpWaves) * 128;
+                    const bool in = k0 + 16 * (lane & 7) < dim;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            to[q][h] = buf_load16<kNonTemporal>(wr, in ? wrow[q] : kOutOfRange, (uint32_t)(k0 + 8 * h * dim));
+                };
+                const auto load_x = [&](uint4 (&to)[4], int i, int c) {
+                    const int k0 = (wave + i * kUpWaves) * 128;
+                    const bool in = k0 + 8 * r < dim;
+#pragma unroll
+                    for (int q = 0; q < NX; ++q) to[q] = buf_load16(xr, in ? xrow[c][q] : kOutOfRange, (uint32_t)(2 * k0));
+                };
+                const auto step = [&](uint4 (&from)[2][2], uint4 (&xfrom)[4], int i) {
+                    uint4 wo[2][2];
+                    turn_weights<2>(from, tile[wave], wo);
+                    const float f[2] = {__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv[0]), i)),
+                                        __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv[1]), i))};
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        place_tokens(xfrom, NX, tile[wave]);
+                        if (c + 1 < NC) load_x(xfrom, i, c + 1);
+                        else load_x(xfrom, i + XS, 0);
+                        if (c + 1 == NC) load_w(from, i + 2);        // last: loads come back in their order
+                        multiply<FMT, 2>(wo, tile[wave], f, acc[c]);
+                    }
+                };
+                load_x(x[0], 0, 0);
+                load_w(w[0], 0);
+                if (XS > 1) load_x(x[XS - 1], 1, 0);
+                load_w(w[1], 1);
+                // both steps always: a step behind the last one multiplies zeros. A branch around loads would make every wait
+                // count on the fewest of them
+                for (int i = 0; i < steps; i += 2) {
+                    step(w[0], x[0], i);
+                    step(w[1], x[XS - 1], i + 1);
+                }
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) *(v4f32 *)&part[wave][(2 * c + q) * 256 + r * 16 + 4 * g] = acc[c][q];
                 }
             };
-            const auto use = [&](const Step<2, NT> &s, int i) {
-                const float f[2] = {__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv[0]), i)),
-                                    __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv[1]), i))};
-                multiply<FMT, 2, NT>(s, f, count > 16, acc);
-            };
-            const int steps = (gk - wave + kUpWaves - 1) / kUpWaves;      // at most 64
-            load(step[0], 0);
-            for (int i = 0; i < steps; i += 2) {
-                load(step[1], i + 1);
-                use(step[0], i);
-                load(step[0], i + 2);
-                if (i + 1 < steps) use(step[1], i + 1);
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) *(v4f32 *)&part[wave][q][n][r * 16 + 4 * g] = acc[q][n];
+            using std::integral_constant;
+            const integral_constant<int, 1> one;
+            const integral_constant<int, 2> two;
+            const integral_constant<int, 4> four;
+            if (count <= 4) run(one, one, two);
+            else if (count <= 8) run(two, one, two);
+            else if (count <= 16) run(four, one, two);
+            else run(four, two, one);
             __syncthreads();
             // one hidden unit of one token to a thread
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int i = n * 16 + (int)(threadIdx.x >> 4);
+            for (int c = 0; c * 16 < count; ++c) {
+                const int i = c * 16 + (int)(threadIdx.x >> 4);
                 if (i < count) {
                     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int w = 0; w < kUpWaves; ++w) {
-                        sum[0] += part[w][0][n][threadIdx.x];
-                        sum[1] += part[w][1][n][threadIdx.x];
+                        sum[0] += part[w][c * 512 + threadIdx.x];
+                        sum[1] += part[w][c * 512 + 256 + threadIdx.x];
                     }
                     const float a = act<ACT, false>(sum[0]) * sum[1];
-                    const int c = (int)(jobs.entry[start + i] & 0xFFFF);
-                    p.a[(int64_t)c * p.hidden + j0 + (threadIdx.x & 15)] = (uint16_t)Eight<uint16_t>::two(a, 0.0f);
+                    const int to = (int)(jobs.entry[start + i] & 0xFFFF);
+                    p.a[(int64_t)to * p.hidden + j0 + (threadIdx.x & 15)] = (uint16_t)Eight<uint16_t>::two(a, 0.0f);
                 }
             }
             __syncthreads();
@@ -256,111 +321,179 @@ __global__ __launch_bounds__(kUpThreads, 4) void layer_up_kernel(LayerArgs p) {
 
 constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves;
 
-// A workgroup owns sixteen columns of y. The blocks of 128 hidden units of all jobs form one run of steps, cut into
-// eight equal parts; each wave goes through its part and adds every job's products, weighted, to its own sums of all
-// tokens in LDS, and the eight are joined in the order of the waves: nothing is exchanged between workgroups.
-template <int FMT, int NT>
-__global__ __launch_bounds__(kDownThreads, 4) void layer_down_kernel(LayerArgs p) {
-    extern __shared__ float sums[];                   // [waves][tokens][16], then the list
+// A workgroup owns 16 RT columns of y. The blocks of 128 KB hidden units of all pieces form one run of steps, cut into
+// eight equal parts; each wave goes through its part and adds every expert's products, weighted, to its own sums of all
+// tokens in LDS, and the eight are joined in the order of the waves: nothing is exchanged between workgroups. The pieces of
+// an expert take turns at each block, so its weights are in the L2 for all but the first. One workgroup fills a CU, so its
+// waves have the registers to load D steps ahead.
+template <int FMT, int RT, int KB>
+__global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p) {
+    constexpr int COLS = 16 * RT, D = 2;
+    static_assert(KB * RT <= 2, "a wave's LDS holds two tiles of a weight");
+    extern __shared__ float sums[];                   // [waves][tokens][COLS], then the list
+    __shared__ __align__(16) char tile[kDownWaves][4096];
     const int n = p.tokens * p.top_k, total = *p.job_count;
-    uint32_t *entry = (uint32_t *)(sums + kDownWaves * p.tokens * 16);
+    uint32_t *entry = (uint32_t *)(sums + kDownWaves * p.tokens * COLS);
     float *weight = (float *)(entry + n);
-    uint32_t *job_list = (uint32_t *)(weight + n);
+    uint32_t *piece_list = (uint32_t *)(weight + n);
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    float *mine = sums + wave * p.tokens * 16;
-    for (int i = lane; i < p.tokens * 16; i += 64) mine[i] = 0.0f;
+    float *mine = sums + wave * p.tokens * COLS;
+    for (int i = lane; i < p.tokens * COLS; i += 64) mine[i] = 0.0f;
     for (int i = threadIdx.x; i < n; i += kDownThreads) {       // what is behind the list's end is not used
         entry[i] = p.entries[i];
         weight[i] = p.entry_weights[i];
-        job_list[i] = p.jobs[i];
+        piece_list[i] = p.jobs[i];
     }
     __syncthreads();
-    const int hidden = p.hidden, gk = (hidden + 127) / 128, gn = (p.dim + 127) / 128, d0 = (int)blockIdx.x * 16;
+    const int hidden = p.hidden, gs = (hidden + 127) / 128, gk = (gs + KB - 1) / KB, gn = (p.dim + 127) / 128;
+    const int d0 = (int)blockIdx.x * COLS;
     const int64_t units = (int64_t)total * gk;
     const int lo = (int)(units * wave / kDownWaves), hi = (int)(units * (wave + 1) / kDownWaves);
     const auto ar = make_rsrc(p.a, (uint32_t)n * (uint32_t)hidden * 2u);
-    const uint32_t wrow = (uint32_t)(d0 + r) * (uint32_t)hidden + 16 * g;
-    v4f32 acc[1][NT];
+    uint32_t wrow[RT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[0][i] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < RT; ++t)                      // columns behind the last one: no loads
+        wrow[t] = d0 + 16 * t < p.dim ? (uint32_t)(d0 + 16 * t + (lane >> 3)) * (uint32_t)hidden + 16 * (lane & 7) : kOutOfRange;
+    const auto piece_at = [&](int j) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)piece_list[j < total ? j : total - 1]); };
 
-    // the loads run ahead of the products, so each side keeps its own place in the run
-    int ljob = gk > 0 ? lo / gk : 0, lblock = lo - ljob * gk, ujob = ljob, ublock = lblock;
-    uint32_t arow[NT];
-    __amdgpu_buffer_rsrc_t wr;
-    const float *scale;
-    const auto place = [&](int j) {
-        const uint32_t job = (uint32_t)__builtin_amdgcn_readfirstlane((int)job_list[j < total ? j : 0]);
-        const int e = job_expert(job);
-        wr = make_rsrc(p.w2 + (int64_t)e * p.dim * hidden, (uint32_t)p.dim * (uint32_t)hidden);
-        scale = p.s2 + ((int64_t)e * gn + d0 / 128) * gk;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int at = i * 16 + r;
-            arow[i] = at < job_count(job) ? (entry[job_start(job) + at] & 0xFFFF) * (uint32_t)hidden * 2u + 32 * g : kOutOfRange;
-        }
+    // Where a step is in the run: the expert's first piece and their number, the block, the piece.
+    struct Place {
+        int base, pieces, block, piece;
     };
-    Step<1, NT> step[2];
-    float inv[2];
-    const auto load = [&](Step<1, NT> &s, float &f, int unit) {
-        const int k0 = lblock * 128;
-        const bool on = unit < hi;
-        f = scale[lblock];
+    const auto next = [&](Place &at) {                // whether the expert is another one now
+        if (++at.piece < at.pieces) return false;
+        at.piece = 0;
+        if (++at.block < gk) return false;
+        at.block = 0;
+        at.base += at.pieces;
+        at.pieces = piece_total(piece_at(at.base));
+        return true;
+    };
+    // NX: instructions that load sixteen tokens, enough for each piece of this wave. Loads run D steps ahead of the products,
+    // each side with a place of its own, and each step issues the same ones (behind the end: none from memory), so a wait
+    // counts on all of them. They come back in their order: activations loaded later than the next weights would hold those up.
+    const auto run = [&](auto instructions) {
+        constexpr int NX = decltype(instructions)::value;
+        const uint32_t first = piece_at(lo / gk);
+        Place pw;
+        pw.base = lo / gk - piece_number(first);
+        pw.pieces = piece_total(first);
+        pw.block = (lo - pw.base * gk) / pw.pieces;
+        pw.piece = (lo - pw.base * gk) % pw.pieces;
+        Place px = pw, pu = pw;
+        __amdgpu_buffer_rsrc_t wr, sr;
+        const auto place_w = [&]() {
+            const int e = job_expert(piece_at(pw.base));
+            wr = make_rsrc(p.w2 + (int64_t)e * p.dim * hidden, (uint32_t)p.dim * (uint32_t)hidden);
+            sr = make_rsrc(p.s2 + ((int64_t)e * gn + d0 / 128) * gs, (uint32_t)gs * 4u);
+        };
+        uint32_t arow[NX];
+        const auto place_x = [&]() {
+            const uint32_t piece = piece_at(px.base + px.piece);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const bool in = on && k0 + 64 * h + 16 * g < hidden;
-            s.w[0][h] = buf_load16<kNonTemporal>(wr, in ? wrow + k0 + 64 * h : kOutOfRange, 0);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const uint32_t at = in && arow[i] != kOutOfRange ? arow[i] + 2 * (k0 + 64 * h) : kOutOfRange;
-                s.x[i][2 * h] = buf_load16(ar, at, 0);
-                s.x[i][2 * h + 1] = buf_load16(ar, at == kOutOfRange ? at : at + 16, 0);
+            for (int q = 0; q < NX; ++q) {
+                const int at = 4 * q + g;
+                const uint32_t row = entry[job_start(piece) + (at < job_count(piece) ? at : 0)] & 0xFFFF;
+                arow[q] = at < job_count(piece) ? row * (uint32_t)hidden * 2u + 16 * r : kOutOfRange;
             }
-        }
-        if (++lblock == gk) {
-            lblock = 0;
-            place(++ljob);
-        }
-    };
-    const auto use = [&](const Step<1, NT> &s, float f, int unit) {
-        const uint32_t job = (uint32_t)__builtin_amdgcn_readfirstlane((int)job_list[ujob]);
-        const float one[1] = {1.0f / f};
-        multiply<FMT, 1, NT>(s, one, job_count(job) > 16, acc);
-        if (++ublock == gk || unit + 1 == hi) {
+        };
+        uint4 w[D][KB * RT][2], x[D][KB][4];
+        float scale_of[D][KB];
+        v4f32 acc[RT];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int at = i * 16 + r;
-                if (at < job_count(job)) {
-                    const int k = job_start(job) + at;
-                    v4f32 *to = (v4f32 *)(mine + (entry[k] >> 16) * 16 + 4 * g);
-                    v4f32 v = *to;
+        for (int t = 0; t < RT; ++t) acc[t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+        const auto load_w = [&](uint4 (&to)[KB * RT][2], float (&f)[KB], int unit) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(weight[k], acc[0][i][q], v[q]);
-                    *to = v;
+            for (int b = 0; b < KB; ++b) {
+                const int block = pw.block * KB + b, k0 = block * 128;
+                const bool in = unit < hi && k0 + 16 * (lane & 7) < hidden;
+                // 16 RT columns lie in one block of 128. A vector load: a scalar one would have every wait for LDS wait for it too
+                f[b] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sr, 0, (block < gs ? block : 0) * 4, kCached));
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        to[b * RT + t][h] = buf_load16<kNonTemporal>(wr, in ? wrow[t] : kOutOfRange, (uint32_t)(k0 + 8 * h * hidden));
+            }
+            if (next(pw)) place_w();
+        };
+        const auto load_x = [&](uint4 (&to)[KB][4], int unit) {
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                const int k0 = (px.block * KB + b) * 128;
+                const bool in = unit < hi && k0 + 8 * r < hidden;
+#pragma unroll
+                for (int q = 0; q < NX; ++q) to[b][q] = buf_load16(ar, in ? arow[q] : kOutOfRange, (uint32_t)(2 * k0));
+            }
+            if (next(px) || px.pieces > 1) place_x();
+        };
+        const auto step = [&](uint4 (&wfrom)[KB * RT][2], uint4 (&xfrom)[KB][4], float (&f)[KB], int unit) {
+            uint4 wo[KB * RT][2];
+            turn_weights<KB * RT>(wfrom, tile[wave], wo);
+            float inv[KB][RT];
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) inv[b][t] = unit < hi ? 1.0f / f[b] : 0.0f;
+            place_tokens(xfrom[0], NX, tile[wave]);
+            if constexpr (KB > 1) {
+                multiply<FMT, RT>(wo, tile[wave], inv[0], acc);
+                place_tokens(xfrom[KB - 1], NX, tile[wave]);
+            }
+            load_x(xfrom, unit + D);
+            load_w(wfrom, f, unit + D);
+            multiply<FMT, RT, (KB - 1) * RT>(wo, tile[wave], inv[KB - 1], acc);
+            if (unit < hi && (pu.pieces > 1 || pu.block + 1 == gk || unit + 1 == hi)) {
+                const uint32_t piece = piece_at(pu.base + pu.piece);
+                if (r < job_count(piece)) {
+                    const int k = job_start(piece) + r;
+                    const float f = weight[k];
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        v4f32 *to = (v4f32 *)(mine + (entry[k] >> 16) * COLS + 16 * t + 4 * g);
+                        v4f32 v = *to;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(f, acc[t][q], v[q]);
+                        *to = v;
+                    }
                 }
-                acc[0][i] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int t = 0; t < RT; ++t) acc[t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
             }
-            ublock = 0;
-            ++ujob;
+            next(pu);
+        };
+        place_w();
+        place_x();
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            load_x(x[d], lo + d);
+            load_w(w[d], scale_of[d], lo + d);
+        }
+        for (int u = lo; u < hi; u += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) step(w[d], x[d], scale_of[d], u + d);
         }
     };
     if (lo < hi) {
-        place(ljob);
-        load(step[0], inv[0], lo);
-        for (int u = lo; u < hi; u += 2) {
-            load(step[1], inv[1], u + 1);
-            use(step[0], inv[0], u);
-            load(step[0], inv[0], u + 2);
-            if (u + 1 < hi) use(step[1], inv[1], u + 1);
+        int most = 0;
+        for (int j = lo / gk; j <= (hi - 1) / gk; ++j) {       // and the other pieces of the first and last expert
+            const uint32_t piece = piece_at(j);
+            most = piece_total(piece) > 1 ? 16 : most > job_count(piece) ? most : job_count(piece);
+            if (most == 16) break;
         }
+        using std::integral_constant;
+        if (most <= 4) run(integral_constant<int, 1>{});
+        else if (most <= 8) run(integral_constant<int, 2>{});
+        else run(integral_constant<int, 4>{});
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.tokens * 16; i += kDownThreads) {
+    for (int i = threadIdx.x; i < p.tokens * COLS; i += kDownThreads) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kDownWaves; ++w) s += sums[w * p.tokens * 16 + i];
-        p.y[(int64_t)(i >> 4) * p.dim + d0 + (i & 15)] = (uint16_t)Eight<uint16_t>::two(s, 0.0f);
+        for (int w = 0; w < kDownWaves; ++w) s += sums[w * p.tokens * COLS + i];
+        const int col = d0 + i % COLS;
+        if (col < p.dim) p.y[(int64_t)(i / COLS) * p.dim + col] = (uint16_t)Eight<uint16_t>::two(s, 0.0f);
     }
 }
 
@@ -368,20 +501,23 @@ int launched() { return hipGetLastError() == hipSuccess ? QF8_OK : QF8_ERR_HIP; 
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-template <int FMT, int ACT, int NT>
-int launch_layer_kernels(const LayerArgs &p, hipStream_t s) {
-    const int n = p.tokens * p.top_k;
-    const int64_t jobs = n < p.experts ? n : p.experts, most = 256 * 4;      // four workgroups to a CU
-    const int64_t items = p.hidden > 0 ? jobs * (p.hidden / 16) : 1;
-    hipLaunchKernelGGL((layer_up_kernel<FMT, ACT, NT>), dim3((unsigned)(items < most ? items : most)), dim3(kUpThreads), 0, s, p);
-    if (launched() != QF8_OK) return QF8_ERR_HIP;
-    const size_t lds = (size_t)kDownWaves * p.tokens * 64 + (size_t)n * 12;
-    hipLaunchKernelGGL((layer_down_kernel<FMT, NT>), dim3((unsigned)(p.dim / 16)), dim3(kDownThreads), lds, s, p);
+template <int FMT, int RT, int KB>
+int launch_down(const LayerArgs &p, hipStream_t s) {
+    const size_t lds = (size_t)kDownWaves * p.tokens * 64 * RT + (size_t)p.tokens * p.top_k * 12;
+    hipLaunchKernelGGL((layer_down_kernel<FMT, RT, KB>), dim3((unsigned)((p.dim + 16 * RT - 1) / (16 * RT))), dim3(kDownThreads), lds, s, p);
     return launched();
 }
+
 template <int FMT, int ACT>
-int launch_layer_tokens(const LayerArgs &p, hipStream_t s) {
-    return p.tokens <= 16 ? launch_layer_kernels<FMT, ACT, 1>(p, s) : launch_layer_kernels<FMT, ACT, 2>(p, s);
+int launch_layer_kernels(const LayerArgs &p, hipStream_t s) {
+    const int n = p.tokens * p.top_k;
+    const int64_t jobs = n < p.experts ? n : p.experts, most = 256 * kUpGroups;
+    const int64_t items = p.hidden > 0 ? jobs * (p.hidden / 16) : 1;
+    hipLaunchKernelGGL((layer_up_kernel<FMT, ACT>), dim3((unsigned)(items < most ? items : most)), dim3(kUpThreads), 0, s, p);
+    if (launched() != QF8_OK) return QF8_ERR_HIP;
+    // Sixteen columns to a workgroup as long as that is one to a CU, else 32. us, 16 / 32: 64 tokens of 7168, hidden 2048
+    // 189 / 169 (the activations are read half as often). With sixteen, a step takes two blocks: 1 token of 4096 16.1 / 14.9
+    return p.dim / 16 <= 256 ? launch_down<FMT, 1, 2>(p, s) : launch_down<FMT, 2, 1>(p, s);
 }
 
 }  // namespace
@@ -405,8 +541,8 @@ int launch_layer(const LayerArgs &args, int fmt, int act, void *ws, hipStream_t 
     at += up16(n * 4);
     p.job_count = (int *)at;
     if (fmt == QF8_E4M3)
-        return act == QF8_ACT_SILU ? launch_layer_tokens<kE4M3, QF8_ACT_SILU>(p, s) : launch_layer_tokens<kE4M3, QF8_ACT_GELU>(p, s);
-    return act == QF8_ACT_SILU ? launch_layer_tokens<kE5M2, QF8_ACT_SILU>(p, s) : launch_layer_tokens<kE5M2, QF8_ACT_GELU>(p, s);
+        return act == QF8_ACT_SILU ? launch_layer_kernels<kE4M3, QF8_ACT_SILU>(p, s) : launch_layer_kernels<kE4M3, QF8_ACT_GELU>(p, s);
+    return act == QF8_ACT_SILU ? launch_layer_kernels<kE5M2, QF8_ACT_SILU>(p, s) : launch_layer_kernels<kE5M2, QF8_ACT_GELU>(p, s);
 }
 
 }  // namespace qf8

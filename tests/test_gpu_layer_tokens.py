@@ -59,7 +59,8 @@ def check(y, x, w1, s1, w2, s2, ids, weights, fmt, act):
 @pytest.mark.parametrize("tokens,dim,hidden,experts,top_k", [
     (1, 16, 16, 1, 1), (1, 128, 128, 8, 2), (1, 4096, 512, 16, 8), (2, 144, 80, 5, 5), (13, 528, 208, 40, 6), (16, 512, 256, 4, 2),
     (17, 512, 256, 4, 2), (33, 272, 400, 3, 1), (64, 384, 256, 8, 8), (64, 1040, 128, 1, 1), (64, 256, 144, 64, 16), (5, 32, 2064, 7, 3),
-    (64, 128, 128, 130, 8), (3, 8208, 16, 4, 2)])
+    (64, 128, 128, 130, 8), (3, 8208, 16, 4, 2),
+    (64, 4112, 144, 20, 16)])
 @pytest.mark.parametrize("fmt", [qf8.E4M3, qf8.E5M2])
 def test_layer(tokens, dim, hidden, experts, top_k, fmt):
     act = ACTS[tokens % 2]
