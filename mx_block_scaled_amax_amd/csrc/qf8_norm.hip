@@ -5,7 +5,8 @@
 //   y = h R w                          fp32; S = F8max / max|y| over 128 neighbours, q = sat_rne8(fl32(y S))
 //
 // A row stays in registers from its load to its codes, so each input is read and each output written once:
-// HBM is the bound. A group of 128 is sixteen lanes with eight values each, so its maximum is four DPP steps;
+// HBM is the bound (8192 rows of 7168 BF16 with residual 70 us, 5.9 TB/s; 16384 of 4096 75 us, 6.3; a copy of 2 GiB 4.95).
+// Loads are non-temporal, stores are not (70 us; all cached 78, all non-temporal 73). A group of 128 is sixteen lanes with eight values each, so its maximum is four DPP steps;
 // the row's sum takes one more exchange through LDS where several waves share a row.
 #include <type_traits>
 
@@ -46,11 +47,11 @@ __device__ __forceinline__ float rstd_of_large(const float (&h)[V][8], float *re
     return (float)(1.0 / sqrt(mean + (double)eps));
 }
 
-template <typename TW>
-__device__ __forceinline__ void weights8(const void *w, int col, float *v) {
-    Eight<TW> e;
-    e.load((const TW *)w + col);
-    e.values(v);
+// The workgroup's threads that share a row, and the row, the same for the whole wave.
+template <int T>
+__device__ __forceinline__ int64_t first_row() {
+    constexpr int R = T < 256 ? 256 / T : 1;
+    return (int64_t)blockIdx.x * R + (T < 256 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0);
 }
 
 // T threads to a row, V pieces of eight columns to a thread: cols <= 8 T V. TR: type of the residual (RES) and of h.
@@ -59,24 +60,21 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
     constexpr int R = T < 256 ? 256 / T : 1;
     __shared__ float red[2][T < 256 ? 1 : T / 64];
     const int t = threadIdx.x % T, cols = (int)p.cols;
-    for (int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / T; row < p.rows; row += (int64_t)gridDim.x * R) {
-        const int64_t at = row * cols;
+    for (int64_t row = first_row<T>(); row < p.rows; row += (int64_t)gridDim.x * R) {
+        const auto xr = row_of<TX>(p.x, row, cols);
         Eight<TX> xe[V];
         Eight<TR> re[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int col = (v * T + t) * 8;
-            xe[v].zero();
-            if constexpr (RES) re[v].zero();
-            if (col < cols) {
-                xe[v].stream((const TX *)p.x + at + col);
-                if constexpr (RES) re[v].stream((const TR *)p.residual + at + col);
-            }
+        for (int v = 0; v < V; ++v) xe[v].template from<kNonTemporal>(xr, (v * T + t) * 8);
+        if constexpr (RES) {
+            const auto rr = row_of<TR>(p.residual, row, cols);
+#pragma unroll
+            for (int v = 0; v < V; ++v) re[v].template from<kNonTemporal>(rr, (v * T + t) * 8);
         }
         float h[V][8], ss = 0.0f;
+        const auto hr = row_of<TR>(p.h, row, cols);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int col = (v * T + t) * 8;
             xe[v].values(h[v]);
             if constexpr (RES) {
                 float r[8];
@@ -84,7 +82,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[v][i] += r[i];
                 re[v].round(h[v]);
-                if (col < cols) re[v].store((TR *)p.h + at + col);
+                re[v].template to<kCached>(hr, (v * T + t) * 8);
                 re[v].values(h[v]);
             }
 #pragma unroll
@@ -94,31 +92,35 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
         float rstd = 1.0f / sqrtf(ss / (float)cols + p.eps);
         if (!(ss < __builtin_inff())) rstd = rstd_of_large<T, V>(h, red[1], cols, p.eps);
         if (p.rstd && t == 0) p.rstd[row] = rstd;
+        const auto yr = row_of<TX>(p.y, row, cols, p.y != nullptr);
+        const auto qr = row_of<uint8_t>(p.q, row, cols, p.q != nullptr);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int col = (v * T + t) * 8;
             float w[8], y[8];
-            if (col < cols) {
-                if (p.w_fp32) weights8<float>(p.weight, col, w);
-                else weights8<uint16_t>(p.weight, col, w);
+            if (p.w_fp32) {
+                Eight<float> e;
+                e.from<kCached>(row_of<float>(p.weight, 0, cols), col);
+                e.values(w);
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = 0.0f;
+                Eight<uint16_t> e;
+                e.from<kCached>(row_of<uint16_t>(p.weight, 0, cols), col);
+                e.values(w);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = col < cols ? h[v][i] * rstd * w[i] : 0.0f;
             const uint32_t amax = group_amax(y);
             const bool first = (threadIdx.x & 15) == 0 && col < cols;
             if (p.nonfinite && first && amax >= 0x7F800000u) *p.nonfinite = 1;
-            if (p.y && col < cols) {
+            if (p.y) {
                 Eight<TX> e;
                 e.round(y);
-                e.store((TX *)p.y + at + col);
+                e.template to<kCached>(yr, col);
             }
             if (p.q) {
                 const float s = group_scale(amax, p.fmt, p.pow2);
                 const uint2 c = group_codes(y, s, p.fmt);
-                if (col < cols) *(uint2 *)(p.q + at + col) = c;
+                buf_store8<kCached>(qr, col, 0, c.x, c.y);
                 if (first) p.scales[row * p.gcols + (col >> 7)] = s;
             }
         }
@@ -130,92 +132,115 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
 //
 // With n = h R and g = dy w:  dh = R (g - n mean_c(g n)) + dres,  dw = sum over the rows of dy n.
 // A workgroup takes every gridDim.x-th row and keeps its columns' share of dw in registers; the shares are joined
-// in the order of the workgroups by a second kernel, so the same call gives the same bits.
+// in the order of the workgroups by a second kernel, so the same call gives the same bits. HBM is the bound: 8192 rows of
+// 4096 BF16 with dres 48.9 us, 5.5 TB/s, 4.4 of them the joining.
+// The next row's loads are under way while this one's sum is joined.
 template <typename TX, typename TH, int T, int V>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_backward_kernel(NormArgs p) {
     constexpr int R = T < 256 ? 256 / T : 1;
     __shared__ float red[2][T < 256 ? 1 : T / 64];
     const int t = threadIdx.x % T, cols = (int)p.cols;
-    const int64_t group = (int64_t)blockIdx.x * R + threadIdx.x / T;
+    const int64_t group = first_row<T>(), stride = (int64_t)gridDim.x * R;
     float dw[V][8], w[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int col = (v * T + t) * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[v][i] = w[v][i] = 0.0f;
-        if (col < cols) {
-            if (p.w_fp32) weights8<float>(p.weight, col, w[v]);
-            else weights8<uint16_t>(p.weight, col, w[v]);
+        for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
+        if (p.w_fp32) {
+            Eight<float> e;
+            e.from<kCached>(row_of<float>(p.weight, 0, cols), (v * T + t) * 8);
+            e.values(w[v]);
+        } else {
+            Eight<uint16_t> e;
+            e.from<kCached>(row_of<uint16_t>(p.weight, 0, cols), (v * T + t) * 8);
+            e.values(w[v]);
         }
     }
+    Eight<TX> de[V];
+    Eight<TH> he[V], se[V];
+    float rstd;
+    const auto load = [&](int64_t row) {
+        const bool there = row < p.rows;
+        const auto dr = row_of<TX>(p.dy, row, cols, there);
+        const auto hr = row_of<TH>(p.hin, row, cols, there);
+        const auto sr = row_of<TH>(p.dres, row, cols, there && p.dres != nullptr);
+        const auto rr = make_rsrc(p.rstd_in + row, there ? 4u : 0u);
+        rstd = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rr, 0, 0, kCached));
+#pragma unroll
+        for (int v = 0; v < V; ++v) de[v].template from<kNonTemporal>(dr, (v * T + t) * 8);
+#pragma unroll
+        for (int v = 0; v < V; ++v) he[v].template from<kNonTemporal>(hr, (v * T + t) * 8);
+#pragma unroll
+        for (int v = 0; v < V; ++v) se[v].template from<kNonTemporal>(sr, (v * T + t) * 8);
+    };
+    load(group);
     int turn = 0;
-    for (int64_t row = group; row < p.rows; row += (int64_t)gridDim.x * R, turn ^= 1) {
-        const int64_t at = row * cols;
-        Eight<TX> de[V];
-        Eight<TH> he[V], se[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int col = (v * T + t) * 8;
-            de[v].zero(); he[v].zero(); se[v].zero();
-            if (col < cols) {
-                de[v].stream((const TX *)p.dy + at + col);
-                he[v].stream((const TH *)p.hin + at + col);
-                if (p.dres) se[v].stream((const TH *)p.dres + at + col);
-            }
-        }
-        const float rstd = p.rstd_in[row];
+    for (int64_t row = group; row < p.rows; row += stride, turn ^= 1) {
         float s = 0.0f;
+        Eight<TX> d0[V];
+        Eight<TH> h0[V], s0[V];
+        const float r = rstd;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            d0[v] = de[v]; h0[v] = he[v]; s0[v] = se[v];
             float d[8], n[8];
-            de[v].values(d);
-            he[v].values(n);
+            d0[v].values(d);
+            h0[v].values(n);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                n[i] *= rstd;
+                n[i] *= r;
                 s = __builtin_fmaf(d[i] * w[v][i], n[i], s);
                 dw[v][i] = __builtin_fmaf(d[i], n[i], dw[v][i]);
             }
         }
+        load(row + stride);
         const float mean = sum_row<T>(s, red[turn]) / (float)cols;
+        const auto out = row_of<TH>(p.dx, row, cols);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int col = (v * T + t) * 8;
             float d[8], n[8], o[8];
-            de[v].values(d);
-            he[v].values(n);
-            se[v].values(o);
+            d0[v].values(d);
+            h0[v].values(n);
+            s0[v].values(o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] += rstd * (d[i] * w[v][i] - n[i] * rstd * mean);
-            if (col < cols) {
-                Eight<TH> e;
-                e.round(o);
-                e.store_stream((TH *)p.dx + at + col);
-            }
+            for (int i = 0; i < 8; ++i) o[i] += r * (d[i] * w[v][i] - n[i] * r * mean);
+            Eight<TH> e;
+            e.round(o);
+            e.template to<kCached>(out, (v * T + t) * 8);
         }
     }
     if (p.partial) {
+        const auto to = row_of<float>(p.partial, group, cols);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int col = (v * T + t) * 8;
             Eight<float> e;
             e.round(dw[v]);
-            if (col < cols) e.store(p.partial + group * cols + col);
+            e.to<kCached>(to, (v * T + t) * 8);
         }
     }
 }
 
-// dw[c] = sum of parts rows of partial, 64 columns to a workgroup: four runs of rows, joined in their order.
+// dw[c] = sum of parts rows of partial, 16 columns to a workgroup: 64 runs of rows (a lane's group of four columns
+// reads whole 64-byte pieces), joined in their order.
 __global__ __launch_bounds__(256) void column_sum_kernel(const float *partial, int64_t parts, int cols, float *dw) {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
-    const int64_t per = (parts + 3) / 4, lo = wave * per, hi = lo + per < parts ? lo + per : parts;
-    float s = 0.0f;
+    __shared__ float red[64][16];
+    const int quad = threadIdx.x & 3, run = threadIdx.x >> 2, col = blockIdx.x * 16 + quad * 4;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (col < cols)
-        for (int64_t i = lo; i < hi; ++i) s += partial[i * cols + col];
-    red[wave][lane] = s;
+#pragma unroll 8
+        for (int64_t i = run; i < parts; i += 64) {
+            const float4 v = *(const float4 *)(partial + i * cols + col);
+            s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[run][quad * 4 + i] = s[i];
     __syncthreads();
-    if (wave == 0 && col < cols) dw[col] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if (threadIdx.x < 16 && blockIdx.x * 16 + (int)threadIdx.x < cols) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) t += red[i][threadIdx.x];
+        dw[blockIdx.x * 16 + threadIdx.x] = t;
+    }
 }
 
 int launched() { return hipGetLastError() == hipSuccess ? QF8_OK : QF8_ERR_HIP; }
@@ -232,13 +257,19 @@ int launch_norm_types(const NormArgs &p, hipStream_t s) {
         return launched();
     };
     using std::integral_constant;
+    // Threads and pieces of a row. us of the kernel, BF16: 7168 columns, 8192 rows 256 x 4 70, 512 x 2 73, 1024 x 1 100;
+    // 64 rows 5.7, 4.5, 4.3; 1 row 4.6, 3.5, 3.3. 2048 columns, 16384 rows 256 x 1 41, 64 x 4 42; 64 rows 3.2, 5.2. 16384
+    // columns, 2048 rows 512 x 4 47, 1024 x 2 51; 16 rows 5.8, 5.3
+    const bool few = p.rows <= 512;
 #define QF8_GO(T, V) return go(integral_constant<int, T>{}, integral_constant<int, V>{})
     if (p.cols <= 512) QF8_GO(64, 1);
     if (p.cols <= 1024) QF8_GO(64, 2);
     if (p.cols <= 2048) QF8_GO(256, 1);
     if (p.cols <= 4096) QF8_GO(256, 2);
+    if (p.cols <= 8192 && few) QF8_GO(512, 2);
     if (p.cols <= 8192) QF8_GO(256, 4);
-    QF8_GO(1024, 2);
+    if (few) QF8_GO(1024, 2);
+    QF8_GO(512, 4);
 #undef QF8_GO
 }
 
@@ -251,20 +282,22 @@ int launch_norm_backward_types(const NormArgs &p, hipStream_t s) {
         return launched();
     };
     using std::integral_constant;
+    // Few values to a thread, so that the next row's loads find registers. us, 8192 rows of 4096: 512 x 1 44.8, 256 x 2 44.5
 #define QF8_GO(T, V) return go(integral_constant<int, T>{}, integral_constant<int, V>{})
     if (p.cols <= 512) QF8_GO(64, 1);
     if (p.cols <= 1024) QF8_GO(64, 2);
     if (p.cols <= 2048) QF8_GO(256, 1);
-    if (p.cols <= 4096) QF8_GO(256, 2);
-    if (p.cols <= 8192) QF8_GO(256, 4);
+    if (p.cols <= 4096) QF8_GO(512, 1);
+    if (p.cols <= 8192) QF8_GO(1024, 1);
     QF8_GO(1024, 2);
 #undef QF8_GO
 }
 
 }  // namespace
 
+// us with the joining kernel, 8192 rows of 4096: 512 groups 48.9, 768 51.9, 2048 62
 int64_t norm_backward_groups(int64_t rows, int64_t cols) {
-    const int64_t r = cols <= 1024 ? 4 : 1, most = 1024;      // rows that a workgroup takes at once
+    const int64_t r = cols <= 1024 ? 4 : 1, most = 512;      // rows that a workgroup takes at once
     const int64_t groups = (rows + r - 1) / r * r;
     return groups < most ? groups : most;
 }
@@ -287,7 +320,7 @@ int launch_norm_backward(const NormArgs &p, int dtype, int h_dtype, float *dw, h
             r = bf ? launch_norm_backward_types<uint16_t, float>(p, s) : launch_norm_backward_types<float, float>(p, s);
     }
     if (r != QF8_OK || !dw) return r;
-    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((p.cols + 63) / 64)), dim3(256), 0, s, p.partial,
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((p.cols + 15) / 16)), dim3(256), 0, s, p.partial,
                        p.rows > 0 ? norm_backward_groups(p.rows, p.cols) : 0, (int)p.cols, dw);
     return launched();
 }

@@ -23,6 +23,8 @@ template <> struct Eight<uint16_t> {
     __device__ __forceinline__ void round(const float *v) {
         a = make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7]));
     }
+    template <int CP> __device__ __forceinline__ void from(__amdgpu_buffer_rsrc_t r, int col) { a = buf_load16<CP>(r, col * 2, 0); }
+    template <int CP> __device__ __forceinline__ void to(__amdgpu_buffer_rsrc_t r, int col) const { buf_store16<CP>(r, col * 2, 0, a); }
     __device__ __forceinline__ void store(uint16_t *p) const { *(uint4 *)p = a; }
     __device__ __forceinline__ void store_stream(uint16_t *p) const { st_stream((uint4 *)p, a); }
 };
@@ -39,9 +41,23 @@ template <> struct Eight<float> {
         a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
         b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     }
+    template <int CP> __device__ __forceinline__ void from(__amdgpu_buffer_rsrc_t r, int col) {
+        a = buf_load16<CP>(r, col * 4, 0);
+        b = buf_load16<CP>(r, col * 4 + 16, 0);
+    }
+    template <int CP> __device__ __forceinline__ void to(__amdgpu_buffer_rsrc_t r, int col) const {
+        buf_store16<CP>(r, col * 4, 0, a);
+        buf_store16<CP>(r, col * 4 + 16, 0, b);
+    }
     __device__ __forceinline__ void store(float *p) const { ((uint4 *)p)[0] = a; ((uint4 *)p)[1] = b; }
     __device__ __forceinline__ void store_stream(float *p) const { st_stream((uint4 *)p, a); st_stream((uint4 *)p + 1, b); }
 };
+
+// A row of a tensor as a buffer: what lies behind its columns reads as zeros and is not written. No row: no columns.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void *base, int64_t row, int cols, bool there = true) {
+    return make_rsrc((const T *)base + row * cols, there ? (uint32_t)cols * (uint32_t)sizeof(T) : 0u);
+}
 
 // Sum over the wave, the same bits in every lane (all lanes active): each step adds two partners' equal sums.
 __device__ __forceinline__ float sum_wave(float v) {
