@@ -12,7 +12,6 @@ row). Outputs are ``torch.uint8`` tensors of raw fp8 / E8M0 bytes.
 """
 import array
 import collections
-import contextlib
 import ctypes
 import functools
 import os
@@ -781,15 +780,20 @@ def combine_experts_backward(dy, x, weights, slots, rows, dx=None, dweights=None
 
 # ---- around the expert layer ---------------------------------------------------------------------
 
-_current_device = torch.cuda.current_device
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on(device):
-    """The kernels run on the current device: the tensors' one for the time of a call."""
-    return _NOTHING if device == _current_device() else torch.cuda.device(device)
+def _run(name, device, *args):
+    """The call with the tensors' device as the current one: the kernels run there."""
+    f = getattr(_lib or _load(), name)
+    if device == _current_device():
+        status = f(*args)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args)
+    if status != 0:
+        raise QF8Error(status, name)
 
-
-_NOTHING = contextlib.nullcontext()
 
 NormResult = collections.namedtuple("NormResult", "q scales h y rstd")
 
@@ -828,11 +832,9 @@ def rms_norm_quantize(x, weight, fmt, residual=None, eps=1e-6, pow2_scales=False
         y = _place(y, (rows, cols), x.dtype, x, "y", stream)
     if want_rstd or rstd is not None:
         rstd = _place(rstd, (rows,), torch.float32, x, "rstd", stream)
-    with _on(device):
-        _check(_load().rms_norm_quantize(x.data_ptr(), dtype, _address(residual), r_dtype, weight.data_ptr(), w_dtype, rows,
-                                         cols, eps, 0 if fmt is None else fmt, FLAG_POW2_SCALES if pow2_scales else 0,
-                                         _address(q), _address(scales), _address(h), _address(y), _address(rstd),
-                                         _flag(nonfinite, device), _stream_of(stream, x)), "rms_norm_quantize")
+    _run("rms_norm_quantize", device, x.data_ptr(), dtype, _address(residual), r_dtype, weight.data_ptr(), w_dtype,
+         rows, cols, eps, 0 if fmt is None else fmt, FLAG_POW2_SCALES if pow2_scales else 0, _address(q),
+         _address(scales), _address(h), _address(y), _address(rstd), _flag(nonfinite, device), _stream_of(stream, x))
     return NormResult(q, scales, x if residual is None else h, y, rstd)
 
 
@@ -853,11 +855,9 @@ def rms_norm_backward(dy, h, rstd, weight, dres=None, want_dweight=True, dx=None
     if want_dweight or dweight is not None:
         dweight = _place(dweight, (cols,), torch.float32, dy, "dweight", stream)
         ws = _workspace(ws, dy, stream, "rms_norm_backward_workspace_bytes", rows, cols)
-    with _on(device):
-        _check(_load().rms_norm_backward(dy.data_ptr(), dtype, h.data_ptr(), h_dtype, rstd.data_ptr(), weight.data_ptr(),
-                                         w_dtype, _address(dres), rows, cols, dx.data_ptr(), _address(dweight),
-                                         _address(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                                         _stream_of(stream, dy)), "rms_norm_backward")
+    _run("rms_norm_backward", device, dy.data_ptr(), dtype, h.data_ptr(), h_dtype, rstd.data_ptr(),
+         weight.data_ptr(), w_dtype, _address(dres), rows, cols, dx.data_ptr(), _address(dweight), _address(ws),
+         0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, dy))
     return dx, dweight
 
 
@@ -882,10 +882,9 @@ def gated_act_quantize(x, fmt, act=ACT_SILU, pow2_scales=False, want_y=False, q=
         raise ValueError("q and scales need a format")
     if want_y or y is not None or fmt is None:
         y = _place(y, (rows, cols), x.dtype, x, "y", stream)
-    with _on(device):
-        _check(_load().gated_act_quantize(x.data_ptr(), dtype, rows, cols, act, 0 if fmt is None else fmt,
-                                          FLAG_POW2_SCALES if pow2_scales else 0, _address(q), _address(scales), _address(y),
-                                          _flag(nonfinite, device), _stream_of(stream, x)), "gated_act_quantize")
+    _run("gated_act_quantize", device, x.data_ptr(), dtype, rows, cols, act, 0 if fmt is None else fmt,
+         FLAG_POW2_SCALES if pow2_scales else 0, _address(q), _address(scales), _address(y), _flag(nonfinite, device),
+         _stream_of(stream, x))
     return q, scales, y
 
 
@@ -905,10 +904,9 @@ def gated_act_backward(dy, x, fmt, act=ACT_SILU, pow2_scales=False, want_dx=Fals
         raise ValueError("q and scales need a format")
     if want_dx or dx is not None or fmt is None:
         dx = _place(dx, (rows, 2 * cols), x.dtype, x, "dx", stream)
-    with _on(device):
-        _check(_load().gated_act_backward(dy.data_ptr(), x.data_ptr(), dtype, rows, cols, act, 0 if fmt is None else fmt,
-                                          FLAG_POW2_SCALES if pow2_scales else 0, _address(q), _address(scales),
-                                          _address(dx), _flag(nonfinite, device), _stream_of(stream, x)), "gated_act_backward")
+    _run("gated_act_backward", device, dy.data_ptr(), x.data_ptr(), dtype, rows, cols, act,
+         0 if fmt is None else fmt, FLAG_POW2_SCALES if pow2_scales else 0, _address(q), _address(scales), _address(dx),
+         _flag(nonfinite, device), _stream_of(stream, x))
     return q, scales, dx
 
 
@@ -932,37 +930,43 @@ def expert_layer_tokens(x, w1, s1, w2, s2, ids, weights, fmt, act=ACT_SILU, y=No
     _need(weights, "weights", torch.float32, (tokens, top_k), device)
     y = _place(y, (tokens, dim), torch.bfloat16, x, "y", stream)
     ws = _workspace(ws, x, stream, "expert_layer_tokens_workspace_bytes", tokens, top_k, hidden)
-    with _on(device):
-        _check(_load().expert_layer_tokens(x.data_ptr(), tokens, dim, w1.data_ptr(), s1.data_ptr(), w2.data_ptr(),
-                                           s2.data_ptr(), experts, hidden, fmt, act, ids.data_ptr(), weights.data_ptr(),
-                                           top_k, y.data_ptr(), _address(ws),
-                                           0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, x)),
-               "expert_layer_tokens")
+    _run("expert_layer_tokens", device, x.data_ptr(), tokens, dim, w1.data_ptr(), s1.data_ptr(), w2.data_ptr(),
+         s2.data_ptr(), experts, hidden, fmt, act, ids.data_ptr(), weights.data_ptr(), top_k, y.data_ptr(),
+         _address(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, x))
     return y
 
 
-def _clip(grads, out, max_norm, norm, nonfinite, ws, stream, what):
-    grads = list(grads)
+def _clip(grads, out, max_norm, norm, nonfinite, ws, stream):
     if not grads:
         raise ValueError("no gradients given")
     like = grads[0]
-    entries = array.array("q")
-    device = None
-    for i, g in enumerate(grads):
-        code = _in_code(g, f"grads[{i}]")
-        if not g.is_cuda or not g.is_contiguous() or g.get_device() != device:
+    entries = []
+    bf16, fp32, device = torch.bfloat16, torch.float32, None
+    for i, g in enumerate(grads):                        # a right call: a few attributes to a tensor
+        try:
+            dtype = g.dtype
+            if g.get_device() != device or not g.is_contiguous() or (dtype is not bf16 and dtype is not fp32):
+                raise AttributeError
+        except AttributeError:
+            _in_code(g, f"grads[{i}]")
             _need(g, f"grads[{i}]", g.dtype, g.shape, device)       # the first tensor's device is that of all
             device = g.get_device()
         at = g.data_ptr()
-        to = 0
-        if out is not None:
+        if out is None:
+            to = 0
+        elif out is grads:
+            to = at
+        else:
             o = out[i]
-            if o is g:
-                to = at
-            else:
-                _need(o, f"out[{i}]", g.dtype, g.shape, device)
-                to = o.data_ptr()
-        entries.extend((at, to, g.numel(), code))
+            try:
+                if (o.dtype is not dtype or o.get_device() != device or not o.is_contiguous() or o.dim() != 1 or g.dim() != 1
+                        or o.numel() != g.numel()):
+                    raise AttributeError
+            except AttributeError:
+                _need(o, f"out[{i}]", dtype, g.shape, device)
+            to = o.data_ptr()
+        entries += (at, to, g.numel(), 0 if dtype is bf16 else 1)
+    entries = array.array("q", entries)
     norm = _place(norm, (1,), torch.float32, like, "norm", stream)
     lib, where, count = _load(), entries.buffer_info()[0], len(grads)
     need = lib.clip_grads_workspace_bytes(where, count)
@@ -970,16 +974,15 @@ def _clip(grads, out, max_norm, norm, nonfinite, ws, stream, what):
         _same_device(_dev_tensor(ws, "ws"), "ws", device)
     else:
         ws = _fresh(like, (need,), torch.uint8, stream)
-    with _on(device):
-        _check(lib.clip_grads(where, count, max_norm, norm.data_ptr(), _flag(nonfinite, device), ws.data_ptr(),
-                              ws.numel() * ws.element_size(), _stream_of(stream, like)), what)
+    _run("clip_grads", device, where, count, max_norm, norm.data_ptr(), _flag(nonfinite, device), ws.data_ptr(),
+         ws.numel() * ws.element_size(), _stream_of(stream, like))
     return norm
 
 
 def grad_norm(grads, norm=None, nonfinite=None, ws=None, stream=None):
     """sqrt of the sum of all squares of the tensors grads (BF16 or FP32, any shapes, contiguous), summed in fp64: a
     float32 tensor of one element."""
-    return _clip(grads, None, float("inf"), norm, nonfinite, ws, stream, "grad_norm")
+    return _clip(list(grads), None, float("inf"), norm, nonfinite, ws, stream)
 
 
 def clip_grads(grads, max_norm, out=None, norm=None, nonfinite=None, ws=None, stream=None):
@@ -993,4 +996,4 @@ def clip_grads(grads, max_norm, out=None, norm=None, nonfinite=None, ws=None, st
         out = list(out)
         if len(out) != len(grads):
             raise ValueError(f"out must have {len(grads)} tensors, got {len(out)}")
-    return _clip(grads, out, max_norm, norm, nonfinite, ws, stream, "clip_grads")
+    return _clip(grads, out, max_norm, norm, nonfinite, ws, stream)

@@ -1,9 +1,10 @@
 // qf8_act.h -- the activations of a gated layer: act(a) = a s, with
 //   SiLU  s = sigmoid(a);   GELU (tanh form)  s = (1 + tanh(z / 2)) / 2 = sigmoid(z), z = 2 sqrt(2 / pi) (a + 0.044715 a^3)
 //   act'(a) = s + a s (1 - s) z', z' the slope of the sigmoid's argument (SiLU: 1)
-// Where the result is rounded to BF16 or FP8 the sigmoid takes the hardware's exp2 and reciprocal: its argument's
-// rounding costs |z| 2^-24 of e^-z, below 2^-17 down to where the sigmoid falls below 2^-126 and is 0 (|act| below
-// 2^-119); 2^-9 and 2^-4 are the roundings after it. EXACT (FP32 results): the library's exp and the exact division.
+// The sigmoid takes the hardware's exp2 and reciprocal (an ulp each). Where the result is rounded to BF16 or FP8, exp2's
+// argument is one product: its rounding costs |z| 2^-24 of e^-z, below 2^-17 down to where the sigmoid falls below 2^-126 and
+// is 0 (|act| below 2^-119); 2^-9 and 2^-4 are the roundings after it. EXACT (FP32 results): the product's rounding error is
+// carried along.
 #pragma once
 #include "qf8_device.h"
 #include "../../include/qf8.h"
@@ -12,8 +13,13 @@ namespace qf8 {
 
 template <bool EXACT>
 __device__ __forceinline__ float sigmoid(float z) {
-    if constexpr (EXACT) return 1.0f / (1.0f + expf(-z));
-    else return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+    constexpr float kLog2E = 1.44269504088896341f, kRest = (float)(1.4426950408889634074 - (double)kLog2E);
+    if constexpr (EXACT) z = __builtin_amdgcn_fmed3f(z, -200.0f, 200.0f);      // 0 or 1 from here on, and no Inf - Inf below
+    const float t = z * -kLog2E;
+    float e = __builtin_amdgcn_exp2f(t);
+    if constexpr (EXACT)                              // 2^rest = 1 + rest ln 2, the rest below 2^-17
+        e *= __builtin_fmaf(__builtin_fmaf(z, -kRest, __builtin_fmaf(z, -kLog2E, -t)), 0.693147180559945f, 1.0f);
+    return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 constexpr float kTwoRootTwoOverPi = 1.59576912160573071f, kCube = 0.044715f;

@@ -670,15 +670,17 @@ int gate(const void *dy, const void *x, int dtype, int64_t rows, int64_t cols, i
     return qf8::launch_gate(p, dtype, act, backward, as_stream(stream));
 }
 
-// -1: refused
-int64_t clip_workspace(const qf8_grad *grads, int count) {
+// Bytes of the sums, and the values of one of them; -1: refused.
+int64_t clip_workspace(const qf8_grad *grads, int count, int64_t *chunk) {
     if (count < 0 || count > 1 << 20 || (count > 0 && !grads)) return -1;
-    int64_t chunks = 0;
+    int64_t total = 0, sums = 0;
     for (int i = 0; i < count; ++i) {
         if (grads[i].n < 0 || grads[i].n >= (int64_t)1 << 36) return -1;
-        chunks += qf8::clip_chunks(grads[i].n);
+        total += grads[i].n;
     }
-    return (chunks * 8 + 15) / 16 * 16 + 16;
+    *chunk = qf8::clip_chunk(total);
+    for (int i = 0; i < count; ++i) sums += (grads[i].n + *chunk - 1) / *chunk;
+    return (sums * 8 + 15) / 16 * 16 + 16;
 }
 }  // namespace
 
@@ -772,14 +774,16 @@ qf8_status expert_layer_tokens(const void *x, int64_t tokens, int64_t dim, const
 }
 
 size_t clip_grads_workspace_bytes(const qf8_grad *grads, int count) {
-    const int64_t need = clip_workspace(grads, count);
+    int64_t chunk;
+    const int64_t need = clip_workspace(grads, count, &chunk);
     return need < 0 ? 0 : (size_t)need;
 }
 
 qf8_status clip_grads(const qf8_grad *grads, int count, float max_norm, float *norm, int32_t *nonfinite, void *ws,
                       size_t ws_bytes, void *stream) {
     if (count > 0 && !grads) return QF8_ERR_NULL;
-    const int64_t need = clip_workspace(grads, count);
+    int64_t chunk = 0;
+    const int64_t need = clip_workspace(grads, count, &chunk);
     if (need < 0 || !(max_norm > 0.0f)) return QF8_ERR_SHAPE;
     int written = 0, held = 0;
     for (int i = 0; i < count; ++i) {
@@ -796,7 +800,7 @@ qf8_status clip_grads(const qf8_grad *grads, int count, float max_norm, float *n
     if (!norm && written == 0 && !nonfinite) return QF8_OK;
     if (!ws || ws_bytes < (size_t)need) return QF8_ERR_WORKSPACE;
     if (!aligned(ws, 16) || !aligned(norm, 4) || !aligned(nonfinite, 4)) return QF8_ERR_ALIGN;
-    return status_of(qf8::launch_clip(grads, count, max_norm, written > 0, norm, (float *)ws, (double *)((char *)ws + 16),
+    return status_of(qf8::launch_clip(grads, count, chunk, max_norm, written > 0, norm, (float *)ws, (double *)((char *)ws + 16),
                                       nonfinite, as_stream(stream)));
 }
 

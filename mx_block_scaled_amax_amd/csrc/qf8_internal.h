@@ -199,16 +199,17 @@ int launch_layer(const LayerArgs &p, int fmt, int act, void *ws, hipStream_t s);
 
 // Norm over many tensors, and scaling to a largest norm. The tensors of a launch travel in its arguments.
 constexpr int kClipTensors = 128;
-constexpr int64_t kMaxClipGrid = (int64_t)1 << 23;       // threads of a launch are counted in 32 bits
 struct ClipBatch {
     const void *g[kClipTensors];
     void *out[kClipTensors];
     int64_t size[kClipTensors];  // values * 2 + (FP32)
-    uint32_t first[kClipTensors];
+    uint32_t first[kClipTensors];        // first chunk
+    int64_t chunk;               // values of a workgroup
     int count;
 };
-int64_t clip_chunks(int64_t n);
-int launch_clip(const qf8_grad *grads, int count, float max_norm, int write, float *norm, float *factor, double *partial,
-                int32_t *nonfinite, hipStream_t s);
+// Values of a workgroup for this many in all: some thousands of workgroups, so that one can join their sums.
+int64_t clip_chunk(int64_t total);
+int launch_clip(const qf8_grad *grads, int count, int64_t chunk, float max_norm, int write, float *norm, float *factor,
+                double *partial, int32_t *nonfinite, hipStream_t s);
 
 }  // namespace qf8

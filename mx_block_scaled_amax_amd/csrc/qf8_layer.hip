@@ -41,8 +41,8 @@ struct Jobs {
     int total, entries;
 };
 
-// All threads of the workgroup; ends with a barrier. The order of an expert's entries is this workgroup's own: what
-// leaves it (activations) is placed by choice. A token that names an expert twice has one entry, at its first choice.
+// All threads of the workgroup; ends with a barrier. The order of an expert's entries is this workgroup's and this run's
+// own: activations are placed by choice, and each is a result of its own. A token that names an expert twice has one entry, at its first choice.
 // cut: the pieces go to p.jobs, their number to p.job_count.
 template <int THREADS>
 __device__ void find_jobs(const LayerArgs &p, bool cut, Jobs &s) {
@@ -198,13 +198,16 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (blockIdx.x == 0) {
+        // the entries of an expert in the order of the choices, so that the second kernel's sums have one order too
         for (int i = threadIdx.x; i < jobs.entries; i += kUpThreads) {
-            const int c = (int)(jobs.entry[i] & 0xFFFF), t0 = (int)(jobs.entry[i] >> 16) * p.top_k;
+            const int c = (int)(jobs.entry[i] & 0xFFFF), t0 = (int)(jobs.entry[i] >> 16) * p.top_k, e = jobs.id[c];
+            int k = jobs.start[e], before = 0;        // the end of the expert's entries
+            for (; k > 0 && jobs.id[jobs.entry[k - 1] & 0xFFFF] == e; --k) before += (int)(jobs.entry[k - 1] & 0xFFFF) < c;
             float w = p.weights[c];
             for (int j = c + 1; j < t0 + p.top_k; ++j)
-                if (jobs.id[j] == jobs.id[c]) w += p.weights[j];
-            p.entries[i] = jobs.entry[i];
-            p.entry_weights[i] = w;
+                if (jobs.id[j] == e) w += p.weights[j];
+            p.entries[k + before] = jobs.entry[i];
+            p.entry_weights[k + before] = w;
         }
     }
     const int dim = p.dim, blocks = p.hidden / 16, gk = (dim + 127) / 128;

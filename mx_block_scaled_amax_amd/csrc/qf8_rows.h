@@ -5,12 +5,11 @@
 
 namespace qf8 {
 
-// Eight values: one 16-byte piece of BF16, two of FP32.
+// Eight values: one 16-byte piece of BF16, two of FP32. CP: cache policy of BF16's.
 template <typename T> struct Eight;
 template <> struct Eight<uint16_t> {
     uint4 a;
     __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const uint16_t *p) { a = *(const uint4 *)p; }
     __device__ __forceinline__ void stream(const uint16_t *p) { a = ld_stream((const uint4 *)p); }
     __device__ __forceinline__ void values(float *v) const {
         v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
@@ -25,14 +24,15 @@ template <> struct Eight<uint16_t> {
     }
     template <int CP> __device__ __forceinline__ void from(__amdgpu_buffer_rsrc_t r, int col) { a = buf_load16<CP>(r, col * 2, 0); }
     template <int CP> __device__ __forceinline__ void to(__amdgpu_buffer_rsrc_t r, int col) const { buf_store16<CP>(r, col * 2, 0, a); }
-    __device__ __forceinline__ void store(uint16_t *p) const { *(uint4 *)p = a; }
     __device__ __forceinline__ void store_stream(uint16_t *p) const { st_stream((uint4 *)p, a); }
 };
+// Each of the two pieces fills half of its lines, so loads and stores are cached: non-temporal ones take a line twice. us,
+// cached / not: gated activation of FP32 to FP32, 8192 x 2048, 36.7 / 43.0, its gradients 60.6 / 64.8, norm 8192 x 4096 with
+// FP32 residual 65.3 / 67.2.
 template <> struct Eight<float> {
     uint4 a, b;
     __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const float *p) { a = ((const uint4 *)p)[0]; b = ((const uint4 *)p)[1]; }
-    __device__ __forceinline__ void stream(const float *p) { a = ld_stream((const uint4 *)p); b = ld_stream((const uint4 *)p + 1); }
+    __device__ __forceinline__ void stream(const float *p) { a = ((const uint4 *)p)[0]; b = ((const uint4 *)p)[1]; }
     __device__ __forceinline__ void values(float *v) const {
         v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
         v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
@@ -42,15 +42,14 @@ template <> struct Eight<float> {
         b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     }
     template <int CP> __device__ __forceinline__ void from(__amdgpu_buffer_rsrc_t r, int col) {
-        a = buf_load16<CP>(r, col * 4, 0);
-        b = buf_load16<CP>(r, col * 4 + 16, 0);
+        a = buf_load16<kCached>(r, col * 4, 0);
+        b = buf_load16<kCached>(r, col * 4 + 16, 0);
     }
     template <int CP> __device__ __forceinline__ void to(__amdgpu_buffer_rsrc_t r, int col) const {
-        buf_store16<CP>(r, col * 4, 0, a);
-        buf_store16<CP>(r, col * 4 + 16, 0, b);
+        buf_store16<kCached>(r, col * 4, 0, a);
+        buf_store16<kCached>(r, col * 4 + 16, 0, b);
     }
-    __device__ __forceinline__ void store(float *p) const { ((uint4 *)p)[0] = a; ((uint4 *)p)[1] = b; }
-    __device__ __forceinline__ void store_stream(float *p) const { st_stream((uint4 *)p, a); st_stream((uint4 *)p + 1, b); }
+    __device__ __forceinline__ void store_stream(float *p) const { ((uint4 *)p)[0] = a; ((uint4 *)p)[1] = b; }
 };
 
 // A row of a tensor as a buffer: what lies behind its columns reads as zeros and is not written. No row: no columns.

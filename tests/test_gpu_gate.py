@@ -1,7 +1,7 @@
 """The gated activation and its gradients against the definition in 64 bits.
 
 Tolerances. BF16 inputs: the sigmoid's argument z is rounded a few times, which costs |z| 2^-22 of e^-z, below 2^-15.5
-where the result is no subnormal; its slope's two terms, up to |dy b|, are off by 2^-17 of that. FP32 inputs: expf and the exact division,
+where the result is no subnormal; its slope's two terms, up to |dy b|, are off by 2^-17 of that. FP32 inputs: exp2's argument in two parts,
 2^-20 for SiLU; GELU's argument costs |z| 2^-22 there too. Then the type's half step, or a code's (E4M3 2^-4, at least 2^-10; E5M2
 2^-3, 2^-17). With FP32 input the codes are quantize_block's of the values bit for bit."""
 import math

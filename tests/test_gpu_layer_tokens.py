@@ -83,6 +83,15 @@ def test_choices_of_any_kind():
         check(qf8.expert_layer_tokens(*args, qf8.E4M3), *args, qf8.E4M3, qf8.ACT_SILU)
 
 
+def test_the_same_bits_again():
+    """Experts with several pieces of tokens, whose choices lie far apart: the order of the sums is the same in every run."""
+    for top_k, experts in ((16, 20), (8, 8), (3, 3)):
+        args = made(64, 512, 272, experts, top_k, qf8.E4M3, seed=experts)
+        want = qf8.expert_layer_tokens(*args, qf8.E4M3)
+        for _ in range(20):
+            assert torch.equal(want, qf8.expert_layer_tokens(*args, qf8.E4M3))
+
+
 def test_most_experts():
     ids = (torch.arange(64 * 16, device="cuda", dtype=torch.int32) % 1024).view(64, 16).contiguous()
     args = made(64, 128, 32, 1024, 16, qf8.E4M3, seed=3, ids=ids)
