@@ -115,7 +115,7 @@ def _load():
         "rms_norm_backward": (i32, [vp, i32, vp, i32, vp, vp, i32, vp, i64, i64, vp, vp, vp, sz, vp]),
         "gated_act_quantize": (i32, [vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp]),
         "gated_act_backward": (i32, [vp, vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp]),
-        "expert_layer_tokens_workspace_bytes": (sz, [i64, i32, i64]),
+        "expert_layer_tokens_workspace_bytes": (sz, [i64, i32, i32, i64, i64]),
         "expert_layer_tokens": (i32, [vp, i64, i64, vp, vp, vp, vp, i32, i64, i32, i32, vp, vp, i32, vp, vp, sz, vp]),
         "clip_grads_workspace_bytes": (sz, [vp, i32]),
         "clip_grads": (i32, [vp, i32, ctypes.c_float, vp, vp, vp, sz, vp]),
@@ -929,7 +929,7 @@ def expert_layer_tokens(x, w1, s1, w2, s2, ids, weights, fmt, act=ACT_SILU, y=No
         raise ValueError(f"ids must have {tokens} rows, got {t}")
     _need(weights, "weights", torch.float32, (tokens, top_k), device)
     y = _place(y, (tokens, dim), torch.bfloat16, x, "y", stream)
-    ws = _workspace(ws, x, stream, "expert_layer_tokens_workspace_bytes", tokens, top_k, hidden)
+    ws = _workspace(ws, x, stream, "expert_layer_tokens_workspace_bytes", tokens, top_k, experts, dim, hidden)
     _run("expert_layer_tokens", device, x.data_ptr(), tokens, dim, w1.data_ptr(), s1.data_ptr(), w2.data_ptr(),
          s2.data_ptr(), experts, hidden, fmt, act, ids.data_ptr(), weights.data_ptr(), top_k, y.data_ptr(),
          _address(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream_of(stream, x))

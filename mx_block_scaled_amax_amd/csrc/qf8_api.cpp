@@ -743,13 +743,14 @@ qf8_status gated_act_backward(const void *dy, const void *x, qf8_dtype dtype, in
     return status_of(gate(dy, x, dtype, rows, cols, act, fmt, flags, q, scales, dx, nonfinite, 1, stream));
 }
 
-static bool layer_dims_ok(int64_t tokens, int top_k, int64_t hidden) {
+static bool layer_dims_ok(int64_t tokens, int top_k, int experts, int64_t dim, int64_t hidden) {
+    const auto side_ok = [](int64_t n) { return n >= 0 && n % 16 == 0 && n <= qf8::kMaxLayerDim; };
     return tokens >= 0 && tokens <= qf8::kLayerTokens && top_k >= 1 && top_k <= qf8::kMaxTopK &&
-           tokens * top_k <= qf8::kLayerChoices && hidden >= 0 && hidden % 16 == 0 && hidden <= qf8::kMaxLayerDim;
+           tokens * top_k <= qf8::kLayerChoices && experts >= 1 && experts <= qf8::kMaxExperts && side_ok(dim) && side_ok(hidden);
 }
 
-size_t expert_layer_tokens_workspace_bytes(int64_t tokens, int top_k, int64_t hidden) {
-    return layer_dims_ok(tokens, top_k, hidden) ? qf8::layer_workspace(tokens, top_k, hidden) : 0;
+size_t expert_layer_tokens_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t dim, int64_t hidden) {
+    return layer_dims_ok(tokens, top_k, experts, dim, hidden) ? qf8::layer_workspace(tokens, top_k, experts, dim, hidden) : 0;
 }
 
 qf8_status expert_layer_tokens(const void *x, int64_t tokens, int64_t dim, const uint8_t *w1, const float *s1,
@@ -757,12 +758,10 @@ qf8_status expert_layer_tokens(const void *x, int64_t tokens, int64_t dim, const
                                const int32_t *ids, const float *weights, int top_k, void *y, void *ws, size_t ws_bytes,
                                void *stream) {
     if (!fmt_ok(fmt) || !act_ok(act)) return QF8_ERR_ENUM;
-    if (!layer_dims_ok(tokens, top_k, hidden) || dim < 0 || dim % 16 != 0 || dim > qf8::kMaxLayerDim || experts < 1 ||
-        experts > qf8::kMaxExperts)
-        return QF8_ERR_SHAPE;
+    if (!layer_dims_ok(tokens, top_k, experts, dim, hidden)) return QF8_ERR_SHAPE;
     if (tokens == 0 || dim == 0) return QF8_OK;
     if (!x || !ids || !weights || !y || (hidden > 0 && (!w1 || !s1 || !w2 || !s2))) return QF8_ERR_NULL;
-    if (!ws || ws_bytes < qf8::layer_workspace(tokens, top_k, hidden)) return QF8_ERR_WORKSPACE;
+    if (!ws || ws_bytes < qf8::layer_workspace(tokens, top_k, experts, dim, hidden)) return QF8_ERR_WORKSPACE;
     if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(y, 16) || !aligned(ws, 16) || !aligned(s1, 4) ||
         !aligned(s2, 4) || !aligned(ids, 4) || !aligned(weights, 4))
         return QF8_ERR_ALIGN;

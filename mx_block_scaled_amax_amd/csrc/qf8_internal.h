@@ -193,8 +193,11 @@ struct LayerArgs {
     uint32_t *jobs, *entries;
     float *entry_weights;
     int *job_count;
+    int *arrivals;               // shares of y's columns that are done, and the shares [columns][parts][tokens][32]
+    float *partial;
+    int parts, columns;
 };
-size_t layer_workspace(int64_t tokens, int top_k, int64_t hidden);
+size_t layer_workspace(int64_t tokens, int top_k, int experts, int64_t dim, int64_t hidden);
 int launch_layer(const LayerArgs &p, int fmt, int act, void *ws, hipStream_t s);
 
 // Norm over many tensors, and scaling to a largest norm. The tensors of a launch travel in its arguments.

@@ -6,7 +6,10 @@
 // Each chosen expert's weights are read once, which is the bound: a weight's byte takes part in as many products as
 // its expert has tokens, about eight, where the matrix cores would need hundreds. Codes are exact in BF16, so they
 // are converted beside the loads and multiplied with BF16 activations (16x16x32 products: sixteen rows of a weight
-// times up to sixteen tokens); a 128x128 block's sums meet 1/S in fp32. The activations are not quantized.
+// times up to sixteen tokens); a 128x128 block's sums meet 1/S in fp32. The activations are not quantized; those between
+// the products are rounded to BF16 as the second one's operand, which costs what rounding y does (2^-9).
+// us of the two kernels: 64 tokens of 7168, 8 of 64 experts, hidden 2048 310 + 172 (6.1 and 5.5 TB/s; a loop of loads alone
+// reaches 7.1), 1 token of 4096 29 + 16, of which a launch and the list of jobs take 5 each.
 //
 // Every workgroup of the first kernel sorts the choices by expert on its own (in LDS, at most 1024 of them); the first
 // one leaves the list, cut into pieces of up to sixteen tokens of an expert, in the workspace for the second kernel.
@@ -158,11 +161,11 @@ __device__ __forceinline__ void place_tokens(const uint4 (&x)[4], int instructio
         if (q < instructions) *(uint4 *)(tile + chunk256(4 * q + g, r)) = x[q];
 }
 
-// Products of turned weights, tiles T0 on, with placed tokens, one half of the 128 values of k after the other (the fence keeps the
+// Products of turned weights with placed tokens, one half of the 128 values of k after the other (the fence keeps the
 // second half's operands out of the registers meanwhile). Tokens behind the last one are what LDS held: their columns are
 // not used.
-template <int FMT, int RT, int T0 = 0, int N>
-__device__ __forceinline__ void multiply(const uint4 (&w)[N][2], const char *tile, const float (&inv)[RT], v4f32 (&acc)[RT]) {
+template <int FMT, int RT>
+__device__ __forceinline__ void multiply(const uint4 (&w)[RT][2], const char *tile, const float (&inv)[RT], v4f32 (&acc)[RT]) {
     const int lane = lane_here(), r = lane & 15, g = lane >> 4;
     v4f32 sum[RT];
 #pragma unroll
@@ -173,8 +176,8 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[N][2], const char *til
         const v8bf16 x1 = *(const v8bf16 *)(tile + chunk256(r, 8 * h + 2 * g + 1));
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FMT>(w[T0 + t][h].x, w[T0 + t][h].y), x0, sum[t], 0, 0, 0);
-            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FMT>(w[T0 + t][h].z, w[T0 + t][h].w), x1, sum[t], 0, 0, 0);
+            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FMT>(w[t][h].x, w[t][h].y), x0, sum[t], 0, 0, 0);
+            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FMT>(w[t][h].z, w[t][h].w), x1, sum[t], 0, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -184,12 +187,14 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[N][2], const char *til
         for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(sum[t][i], inv[t], acc[t][i]);
 }
 
+// Weights are read past the caches where rows are whole lines; where they are not, neighbouring rows share lines, and cached
+// loads take them once: 13 tokens of 2064, 40 experts, hidden 720 53 -> 46 us.
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64, kUpGroups = 3;      // workgroups to a CU
 
 // A workgroup takes sixteen hidden units of a job, 16 rows of A_e and 16 of B_e; its waves share k, wave w the blocks
 // of 128 with index w mod 4, and their sums are joined in LDS in the order of the waves. More than 32 tokens take another
 // pass over the rows.
-template <int FMT, int ACT>
+template <int FMT, int ACT, int CP>
 __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerArgs p) {
     __shared__ Jobs jobs;
     __shared__ __align__(16) char tile[kUpWaves][4096];          // at the end the sums of each wave, [2][2][256]
@@ -198,6 +203,8 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (blockIdx.x == 0) {
+        if (p.parts > 1)
+            for (int i = threadIdx.x; i < p.columns; i += kUpThreads) p.arrivals[i] = 0;
         // the entries of an expert in the order of the choices, so that the second kernel's sums have one order too
         for (int i = threadIdx.x; i < jobs.entries; i += kUpThreads) {
             const int c = (int)(jobs.entry[i] & 0xFFFF), t0 = (int)(jobs.entry[i] >> 16) * p.top_k, e = jobs.id[c];
@@ -255,7 +262,7 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            to[q][h] = buf_load16<kNonTemporal>(wr, in ? wrow[q] : kOutOfRange, (uint32_t)(k0 + 8 * h * dim));
+                            to[q][h] = buf_load16<CP>(wr, in ? wrow[q] : kOutOfRange, (uint32_t)(k0 + 8 * h * dim));
                 };
                 const auto load_x = [&](uint4 (&to)[4], int i, int c) {
                     const int k0 = (wave + i * kUpWaves) * 128;
@@ -322,21 +329,21 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
     }
 }
 
-constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves;
+// A workgroup owns 32 columns of y and one of p.parts equal shares of the products: the blocks of 128 hidden units of all
+// pieces form one run of steps, cut into 8 p.parts parts. Each wave goes through its part and adds every expert's products,
+// weighted, to its own sums of all tokens in LDS; the eight are joined in the order of the waves. With several shares the
+// workgroup that comes last joins those of its columns, in their order. The pieces of an expert take turns at each block,
+// so its weights are in the L2 for all but the first. One workgroup fills a CU.
+constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves, kDownTiles = 2, kDownCols = 16 * kDownTiles;
 
-// A workgroup owns 16 RT columns of y. The blocks of 128 KB hidden units of all pieces form one run of steps, cut into
-// eight equal parts; each wave goes through its part and adds every expert's products, weighted, to its own sums of all
-// tokens in LDS, and the eight are joined in the order of the waves: nothing is exchanged between workgroups. The pieces of
-// an expert take turns at each block, so its weights are in the L2 for all but the first. One workgroup fills a CU, so its
-// waves have the registers to load D steps ahead.
-template <int FMT, int RT, int KB>
+template <int FMT, int CP>
 __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p) {
-    constexpr int COLS = 16 * RT, D = 2;
-    static_assert(KB * RT <= 2, "a wave's LDS holds two tiles of a weight");
+    constexpr int W = kDownWaves, RT = kDownTiles, COLS = kDownCols, D = 2;
     extern __shared__ float sums[];                   // [waves][tokens][COLS], then the list
-    __shared__ __align__(16) char tile[kDownWaves][4096];
+    __shared__ __align__(16) char tile[W][4096];
+    __shared__ int arrived;
     const int n = p.tokens * p.top_k, total = *p.job_count;
-    uint32_t *entry = (uint32_t *)(sums + kDownWaves * p.tokens * COLS);
+    uint32_t *entry = (uint32_t *)(sums + W * p.tokens * COLS);
     float *weight = (float *)(entry + n);
     uint32_t *piece_list = (uint32_t *)(weight + n);
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -349,10 +356,10 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
         piece_list[i] = p.jobs[i];
     }
     __syncthreads();
-    const int hidden = p.hidden, gs = (hidden + 127) / 128, gk = (gs + KB - 1) / KB, gn = (p.dim + 127) / 128;
-    const int d0 = (int)blockIdx.x * COLS;
+    const int hidden = p.hidden, gk = (hidden + 127) / 128, gn = (p.dim + 127) / 128;
+    const int column = (int)blockIdx.x / p.parts, share = (int)blockIdx.x % p.parts, d0 = column * COLS;
     const int64_t units = (int64_t)total * gk;
-    const int lo = (int)(units * wave / kDownWaves), hi = (int)(units * (wave + 1) / kDownWaves);
+    const int lo = (int)(units * (share * W + wave) / (p.parts * W)), hi = (int)(units * (share * W + wave + 1) / (p.parts * W));
     const auto ar = make_rsrc(p.a, (uint32_t)n * (uint32_t)hidden * 2u);
     uint32_t wrow[RT];
 #pragma unroll
@@ -389,7 +396,7 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
         const auto place_w = [&]() {
             const int e = job_expert(piece_at(pw.base));
             wr = make_rsrc(p.w2 + (int64_t)e * p.dim * hidden, (uint32_t)p.dim * (uint32_t)hidden);
-            sr = make_rsrc(p.s2 + ((int64_t)e * gn + d0 / 128) * gs, (uint32_t)gs * 4u);
+            sr = make_rsrc(p.s2 + ((int64_t)e * gn + d0 / 128) * gk, (uint32_t)gk * 4u);
         };
         uint32_t arow[NX];
         const auto place_x = [&]() {
@@ -401,52 +408,40 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
                 arow[q] = at < job_count(piece) ? row * (uint32_t)hidden * 2u + 16 * r : kOutOfRange;
             }
         };
-        uint4 w[D][KB * RT][2], x[D][KB][4];
-        float scale_of[D][KB];
+        uint4 w[D][RT][2], x[D][4];
+        float scale_of[D];
         v4f32 acc[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
-        const auto load_w = [&](uint4 (&to)[KB * RT][2], float (&f)[KB], int unit) {
+        const auto load_w = [&](uint4 (&to)[RT][2], float &f, int unit) {
+            const int k0 = pw.block * 128;
+            const bool in = unit < hi && k0 + 16 * (lane & 7) < hidden;
+            // 32 columns lie in one block of 128. A vector load: a scalar one would have every wait for LDS wait for it too
+            f = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sr, 0, pw.block * 4, kCached));
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                const int block = pw.block * KB + b, k0 = block * 128;
-                const bool in = unit < hi && k0 + 16 * (lane & 7) < hidden;
-                // 16 RT columns lie in one block of 128. A vector load: a scalar one would have every wait for LDS wait for it too
-                f[b] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sr, 0, (block < gs ? block : 0) * 4, kCached));
+            for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        to[b * RT + t][h] = buf_load16<kNonTemporal>(wr, in ? wrow[t] : kOutOfRange, (uint32_t)(k0 + 8 * h * hidden));
-            }
+                for (int h = 0; h < 2; ++h)
+                    to[t][h] = buf_load16<CP>(wr, in ? wrow[t] : kOutOfRange, (uint32_t)(k0 + 8 * h * hidden));
             if (next(pw)) place_w();
         };
-        const auto load_x = [&](uint4 (&to)[KB][4], int unit) {
+        const auto load_x = [&](uint4 (&to)[4], int unit) {
+            const int k0 = px.block * 128;
+            const bool in = unit < hi && k0 + 8 * r < hidden;
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                const int k0 = (px.block * KB + b) * 128;
-                const bool in = unit < hi && k0 + 8 * r < hidden;
-#pragma unroll
-                for (int q = 0; q < NX; ++q) to[b][q] = buf_load16(ar, in ? arow[q] : kOutOfRange, (uint32_t)(2 * k0));
-            }
+            for (int q = 0; q < NX; ++q) to[q] = buf_load16(ar, in ? arow[q] : kOutOfRange, (uint32_t)(2 * k0));
             if (next(px) || px.pieces > 1) place_x();
         };
-        const auto step = [&](uint4 (&wfrom)[KB * RT][2], uint4 (&xfrom)[KB][4], float (&f)[KB], int unit) {
-            uint4 wo[KB * RT][2];
-            turn_weights<KB * RT>(wfrom, tile[wave], wo);
-            float inv[KB][RT];
+        const auto step = [&](uint4 (&wfrom)[RT][2], uint4 (&xfrom)[4], float &f, int unit) {
+            uint4 wo[RT][2];
+            turn_weights<RT>(wfrom, tile[wave], wo);
+            place_tokens(xfrom, NX, tile[wave]);
+            float inv[RT];
 #pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int t = 0; t < RT; ++t) inv[b][t] = unit < hi ? 1.0f / f[b] : 0.0f;
-            place_tokens(xfrom[0], NX, tile[wave]);
-            if constexpr (KB > 1) {
-                multiply<FMT, RT>(wo, tile[wave], inv[0], acc);
-                place_tokens(xfrom[KB - 1], NX, tile[wave]);
-            }
+            for (int t = 0; t < RT; ++t) inv[t] = unit < hi ? 1.0f / f : 0.0f;
             load_x(xfrom, unit + D);
             load_w(wfrom, f, unit + D);
-            multiply<FMT, RT, (KB - 1) * RT>(wo, tile[wave], inv[KB - 1], acc);
+            multiply<FMT, RT>(wo, tile[wave], inv, acc);
             if (unit < hi && (pu.pieces > 1 || pu.block + 1 == gk || unit + 1 == hi)) {
                 const uint32_t piece = piece_at(pu.base + pu.piece);
                 if (r < job_count(piece)) {
@@ -491,10 +486,29 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
         else run(integral_constant<int, 4>{});
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < p.tokens * COLS; i += kDownThreads) {
+    const int values = p.tokens * COLS;
+    float *part = p.partial + (int64_t)blockIdx.x * values;
+    for (int i = threadIdx.x; i < values; i += kDownThreads) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kDownWaves; ++w) s += sums[w * p.tokens * COLS + i];
+        for (int v = 0; v < W; ++v) s += sums[v * values + i];
+        const int col = d0 + i % COLS;
+        if (p.parts > 1) __hip_atomic_store(&part[i], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        else if (col < p.dim) p.y[(int64_t)(i / COLS) * p.dim + col] = (uint16_t)Eight<uint16_t>::two(s, 0.0f);
+    }
+    if (p.parts == 1) return;
+    // The shares are written, then counted; whoever counts the last one reads them all. (The first kernel cleared the counts.)
+    // Every access to a share is one of the device's scope, which passes the XCDs' L2; a fence would write back and
+    // invalidate a whole L2 for each workgroup (15 to 25 us).
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) arrived = __hip_atomic_fetch_add(&p.arrivals[column], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != p.parts - 1) return;
+    for (int i = threadIdx.x; i < values; i += kDownThreads) {
+        float s = 0.0f;
+        for (int v = 0; v < p.parts; ++v)
+            s += __hip_atomic_load(&p.partial[(int64_t)(column * p.parts + v) * values + i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         const int col = d0 + i % COLS;
         if (col < p.dim) p.y[(int64_t)(i / COLS) * p.dim + col] = (uint16_t)Eight<uint16_t>::two(s, 0.0f);
     }
@@ -502,32 +516,50 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
 
 int launched() { return hipGetLastError() == hipSuccess ? QF8_OK : QF8_ERR_HIP; }
 
-size_t up16(size_t n) { return (n + 15) / 16 * 16; }
-
-template <int FMT, int RT, int KB>
-int launch_down(const LayerArgs &p, hipStream_t s) {
-    const size_t lds = (size_t)kDownWaves * p.tokens * 64 * RT + (size_t)p.tokens * p.top_k * 12;
-    hipLaunchKernelGGL((layer_down_kernel<FMT, RT, KB>), dim3((unsigned)((p.dim + 16 * RT - 1) / (16 * RT))), dim3(kDownThreads), lds, s, p);
-    return launched();
+// Shares of the second kernel's columns: the fewest that fill three quarters of the CUs in every round of workgroups (or the
+// most of them), with two steps at least for each wave that may have some. us, one share / this: 13 tokens of 2048, hidden 768
+// 19.4 / 14.8 (4 shares), 64 of 4096, hidden 2048 115 / 107 (2), 64 of 4112, hidden 2000 211 / 175 (3).
+int down_parts(int64_t tokens, int top_k, int experts, int64_t dim, int64_t hidden) {
+    const int64_t columns = (dim + kDownCols - 1) / kDownCols, n = tokens * top_k;
+    const int64_t steps = (n < experts ? n : experts) * ((hidden + 127) / 128), most = steps / (2 * kDownWaves);
+    int best = 1;
+    int64_t filled = 0;                               // of 1024
+    for (int p = 1; p <= 16 && p <= most; ++p) {
+        const int64_t groups = columns * p, f = groups * 1024 / ((groups + 255) / 256 * 256);
+        if (f > filled) {
+            best = p;
+            filled = f;
+        }
+        if (f >= 768) break;
+    }
+    return best;
 }
+
+size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 template <int FMT, int ACT>
 int launch_layer_kernels(const LayerArgs &p, hipStream_t s) {
     const int n = p.tokens * p.top_k;
     const int64_t jobs = n < p.experts ? n : p.experts, most = 256 * kUpGroups;
     const int64_t items = p.hidden > 0 ? jobs * (p.hidden / 16) : 1;
-    hipLaunchKernelGGL((layer_up_kernel<FMT, ACT>), dim3((unsigned)(items < most ? items : most)), dim3(kUpThreads), 0, s, p);
+    const dim3 grid((unsigned)(items < most ? items : most));
+    if (p.dim % 128 == 0) hipLaunchKernelGGL((layer_up_kernel<FMT, ACT, kNonTemporal>), grid, dim3(kUpThreads), 0, s, p);
+    else hipLaunchKernelGGL((layer_up_kernel<FMT, ACT, kCached>), grid, dim3(kUpThreads), 0, s, p);
     if (launched() != QF8_OK) return QF8_ERR_HIP;
-    // Sixteen columns to a workgroup as long as that is one to a CU, else 32. us, 16 / 32: 64 tokens of 7168, hidden 2048
-    // 189 / 169 (the activations are read half as often). With sixteen, a step takes two blocks: 1 token of 4096 16.1 / 14.9
-    return p.dim / 16 <= 256 ? launch_down<FMT, 1, 2>(p, s) : launch_down<FMT, 2, 1>(p, s);
+    const size_t lds = (size_t)kDownWaves * p.tokens * kDownCols * 4 + (size_t)n * 12;
+    const dim3 columns((unsigned)(p.columns * p.parts));
+    if (p.hidden % 128 == 0) hipLaunchKernelGGL((layer_down_kernel<FMT, kNonTemporal>), columns, dim3(kDownThreads), lds, s, p);
+    else hipLaunchKernelGGL((layer_down_kernel<FMT, kCached>), columns, dim3(kDownThreads), lds, s, p);
+    return launched();
 }
 
 }  // namespace
 
-size_t layer_workspace(int64_t tokens, int top_k, int64_t hidden) {
-    const size_t n = (size_t)tokens * top_k;
-    return up16(n * hidden * 2) + up16(kMaxJobs * 4) + 2 * up16(n * 4) + 16;
+size_t layer_workspace(int64_t tokens, int top_k, int experts, int64_t dim, int64_t hidden) {
+    const size_t n = (size_t)tokens * top_k, columns = ((size_t)dim + kDownCols - 1) / kDownCols;
+    const size_t parts = down_parts(tokens, top_k, experts, dim, hidden);
+    return up16(n * hidden * 2) + up16(kMaxJobs * 4) + 2 * up16(n * 4) + 16 +
+           (parts > 1 ? up16(columns * 4) + columns * parts * tokens * kDownCols * 4 : 0);
 }
 
 int launch_layer(const LayerArgs &args, int fmt, int act, void *ws, hipStream_t s) {
@@ -543,6 +575,12 @@ int launch_layer(const LayerArgs &args, int fmt, int act, void *ws, hipStream_t 
     p.entry_weights = (float *)at;
     at += up16(n * 4);
     p.job_count = (int *)at;
+    at += 16;
+    p.arrivals = (int *)at;
+    p.columns = (p.dim + kDownCols - 1) / kDownCols;
+    at += up16((size_t)p.columns * 4);
+    p.partial = (float *)at;
+    p.parts = down_parts(p.tokens, p.top_k, p.experts, p.dim, p.hidden);
     if (fmt == QF8_E4M3)
         return act == QF8_ACT_SILU ? launch_layer_kernels<kE4M3, QF8_ACT_SILU>(p, s) : launch_layer_kernels<kE4M3, QF8_ACT_GELU>(p, s);
     return act == QF8_ACT_SILU ? launch_layer_kernels<kE5M2, QF8_ACT_SILU>(p, s) : launch_layer_kernels<kE5M2, QF8_ACT_GELU>(p, s);

@@ -74,8 +74,8 @@ def test_gate_refusals(back):
 def test_layer_refusals():
     def f(x=F, t=4, d=256, w1=F, s1=F, w2=F, s2=F, e=8, h=128, fmt=0, act=0, ids=F, w=F, k=2, y=F, ws=F, wsb=1 << 40):
         return lib().expert_layer_tokens(x, t, d, w1, s1, w2, s2, e, h, fmt, act, ids, w, k, y, ws, wsb, None)
-    need = lib().expert_layer_tokens_workspace_bytes(4, 2, 128)
-    assert need >= 4 * 2 * 128 * 2 and lib().expert_layer_tokens_workspace_bytes(65, 2, 128) == 0
+    need = lib().expert_layer_tokens_workspace_bytes(4, 2, 8, 256, 128)
+    assert need >= 4 * 2 * 128 * 2 and lib().expert_layer_tokens_workspace_bytes(65, 2, 8, 256, 128) == 0
     assert f(fmt=2) == ENUM and f(act=2) == ENUM
     assert f(t=-1) == SHAPE and f(t=65) == SHAPE and f(d=264) == SHAPE and f(d=32784) == SHAPE and f(h=136) == SHAPE
     assert f(h=32784) == SHAPE and f(e=0) == SHAPE and f(e=1025) == SHAPE and f(k=0) == SHAPE and f(k=65) == SHAPE
