@@ -461,12 +461,12 @@ qf8_status combine_experts_backward(const void *dy, const void *x, qf8_dtype dty
  * Root-mean-square norm of a residual stream, its result in FP8 codes with 1x128 scales:
  *   h = rnd(x + residual) in the residual's type (h = x without a residual),
  *   R = 1 / sqrt(mean_c h^2 + eps),   y = h R weight,   codes and scales of y as quantize_block gives them.
- * Sums are fp32 in a fixed order (a row whose squares overflow fp32 is summed again, scaled); y is rounded to FP8
- * from fp32, not by way of BF16. x [rows][cols] of dtype; residual (nullable) and h [rows][cols] of residual_dtype,
+ * Sums are fp32 in a fixed order, whatever the number of rows (a row whose squares overflow fp32 is summed again, scaled); y is
+ * rounded to FP8 from fp32, not by way of BF16. x [rows][cols] of dtype; residual (nullable) and h [rows][cols] of residual_dtype,
  * h required with a residual and allowed to be the residual itself; weight [cols] of weight_dtype. q [rows][cols] and scales
  * [rows][ceil(cols/128)]: both or neither; y (nullable) [rows][cols] of dtype; at least one of q and y. rstd
  * (nullable): R, [rows] fp32, for the backward pass. nonfinite (nullable) is set where y holds Inf or NaN.
- * flags: QF8_FLAG_POW2_SCALES. cols % 8 == 0, cols <= 16384; 0 < eps < infinity. Tensors 16-byte aligned, scales
+ * flags: QF8_FLAG_POW2_SCALES. cols % 8 == 0, cols <= 16384; eps a normal positive fp32. Tensors 16-byte aligned, scales
  * and rstd 4-byte; no other output overlaps an input. */
 qf8_status rms_norm_quantize(const void *x, qf8_dtype dtype, const void *residual, qf8_dtype residual_dtype,
                              const void *weight, qf8_dtype weight_dtype, int64_t rows, int64_t cols, float eps, qf8_fmt fmt,
@@ -487,7 +487,7 @@ qf8_status rms_norm_backward(const void *dy, qf8_dtype dtype, const void *h, qf8
 /* Gated activation of a product's two halves: y = act(a) * b for x = [a | b], x [rows][2 cols], in fp32. Codes q
  * [rows][cols] with 1x128 scales [rows][ceil(cols/128)] (both or neither) and y (nullable) [rows][cols] of dtype; at least
  * one of the two. act: SiLU, a sigmoid(a), or the tanh form of GELU, a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2.
- * cols % 8 == 0; rows * ceil(cols/128) < 2^31. flags: QF8_FLAG_POW2_SCALES. nonfinite (nullable) is set where y holds
+ * cols % 8 == 0; rows * ceil(cols/128) < 2^28. flags: QF8_FLAG_POW2_SCALES. nonfinite (nullable) is set where y holds
  * Inf or NaN (a = -Inf gives NaN). */
 typedef enum qf8_act { QF8_ACT_SILU = 0, QF8_ACT_GELU = 1 } qf8_act;
 
@@ -523,7 +523,7 @@ qf8_status expert_layer_tokens(const void *x, int64_t tokens, int64_t dim, const
  * values of the same type to out, which may be g itself; with out NULL in every entry (or in none) only the norm is
  * computed. N is summed in fp64 in a fixed order. norm (nullable): N as one fp32. Where N is Inf or NaN the factor is 1
  * and nonfinite (nullable) is set. max_norm > 0. Tensors at the alignment of their type (those at 16 bytes are
- * read faster); out overlaps no g but its own. count <= 2^20, n < 2^36.
+ * read faster); out overlaps no g but its own, so no tensor is given twice. count <= 2^20, n < 2^36.
  * ws: clip_grads_workspace_bytes() bytes, 16-byte aligned, no initialisation. */
 typedef struct qf8_grad {
     const void *g;

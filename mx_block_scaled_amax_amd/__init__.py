@@ -966,6 +966,10 @@ def _clip(grads, out, max_norm, norm, nonfinite, ws, stream):
                 _need(o, f"out[{i}]", dtype, g.shape, device)
             to = o.data_ptr()
         entries += (at, to, g.numel(), 0 if dtype is bf16 else 1)
+    if out is not None:
+        written = [to for to, n in zip(entries[1::4], entries[2::4]) if n]
+        if len(set(written)) != len(written):
+            raise ValueError("a tensor is given twice: it would be scaled twice")
     entries = array.array("q", entries)
     norm = _place(norm, (1,), torch.float32, like, "norm", stream)
     lib, where, count = _load(), entries.buffer_info()[0], len(grads)

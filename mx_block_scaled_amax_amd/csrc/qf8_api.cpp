@@ -646,7 +646,7 @@ int check_gate(const void *dy, const void *x, int dtype, int64_t rows, int64_t c
                const uint8_t *q, const float *scales, const void *y, const int32_t *nonfinite, int backward) {
     if (!dtype_ok(dtype) || !act_ok(act) || (q && !fmt_ok(fmt)) || (flags & ~QF8_FLAG_POW2_SCALES)) return QF8_ERR_ENUM;
     if (rows < 0 || cols < 0 || cols % 8 != 0 || cols >= (int64_t)1 << 30 || rows >= (int64_t)1 << 31 ||
-        rows * ((cols + 127) / 128) >= (int64_t)1 << 31)
+        rows * ((cols + 127) / 128) >= kMaxLaunchThreads / 16)     // up to eight threads to a group, in whole workgroups
         return QF8_ERR_SHAPE;
     if (backward && q && cols % 128 != 0) return QF8_ERR_SHAPE;
     if (rows * cols == 0) return QF8_OK;
@@ -693,7 +693,7 @@ qf8_status rms_norm_quantize(const void *x, qf8_dtype dtype, const void *residua
     if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || (residual && !dtype_ok(residual_dtype)) || (q && !fmt_ok(fmt)) ||
         (flags & ~QF8_FLAG_POW2_SCALES))
         return QF8_ERR_ENUM;
-    if (!norm_dims_ok(rows, cols) || !(eps > 0.0f) || !(eps <= 3.40282346638528859812e+38f)) return QF8_ERR_SHAPE;
+    if (!norm_dims_ok(rows, cols) || !(eps >= 1.17549435e-38f) || !(eps <= 3.40282346638528859812e+38f)) return QF8_ERR_SHAPE;
     if (rows * cols == 0) return QF8_OK;
     if (!x || !weight || !q != !scales || (!q && !y) || (residual && !h)) return QF8_ERR_NULL;
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(q, 16) || !aligned(h, 16) ||

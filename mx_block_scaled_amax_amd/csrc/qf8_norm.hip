@@ -16,34 +16,38 @@
 namespace qf8 {
 namespace {
 
-// Sum over the T threads of a row, the same bits in each of them. red: T / 64 floats that no thread still reads
-// from an earlier call.
-template <int T>
-__device__ __forceinline__ float sum_row(float v, float *red) {
-    v = sum_wave(v);
-    if constexpr (T > 64) {
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.0f;
+// Sum over the T threads of a row and their C shares each, the same bits in each thread. red: C T / 64 floats that no thread
+// still reads from an earlier call. T threads with C shares sum as C T threads do: a thread's share c is that of thread c T + t.
+template <int T, int C>
+__device__ __forceinline__ float sum_row(const float (&v)[C], float *red) {
+    float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < T / 64; ++w) v += red[w];
+    for (int c = 0; c < C; ++c) {
+        s = sum_wave(v[c]);
+        if (T > 64 && (threadIdx.x & 63) == 0) red[(c * T + (int)threadIdx.x) >> 6] = s;
     }
-    return v;
+    if constexpr (T > 64) {
+        __syncthreads();
+        s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < C * T / 64; ++w) s += red[w];
+    }
+    return s;
 }
 
 // A row of squares whose fp32 sum overflows: the sum of (h 2^-72)^2, at most 2^14 (2^128 2^-72)^2 = 2^126, and
 // the root in fp64. Inf and NaN among the values come through as R = 0 or NaN.
-template <int T, int V>
+template <int T, int V, int C>
 __device__ __forceinline__ float rstd_of_large(const float (&h)[V][8], float *red, int cols, float eps) {
-    float ss = 0.0f;
+    float ss[C] = {};
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float s = h[v][i] * 0x1p-72f;
-            ss = __builtin_fmaf(s, s, ss);
+            ss[v % C] = __builtin_fmaf(s, s, ss[v % C]);
         }
-    const double mean = (double)sum_row<T>(ss, red) * 0x1p144 / cols;
+    const double mean = (double)sum_row<T, C>(ss, red) * 0x1p144 / cols;
     return (float)(1.0 / sqrt(mean + (double)eps));
 }
 
@@ -55,10 +59,11 @@ __device__ __forceinline__ int64_t first_row() {
 }
 
 // T threads to a row, V pieces of eight columns to a thread: cols <= 8 T V. TR: type of the residual (RES) and of h.
-template <typename TX, typename TR, bool RES, int T, int V>
+// C: shares of a thread's sum, so that a row's bits do not hang on the number of rows.
+template <typename TX, typename TR, bool RES, int T, int V, int C>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p) {
     constexpr int R = T < 256 ? 256 / T : 1;
-    __shared__ float red[2][T < 256 ? 1 : T / 64];
+    __shared__ float red[2][T < 256 ? 1 : C * T / 64];
     const int t = threadIdx.x % T, cols = (int)p.cols;
     for (int64_t row = first_row<T>(); row < p.rows; row += (int64_t)gridDim.x * R) {
         const auto xr = row_of<TX>(p.x, row, cols);
@@ -71,7 +76,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
 #pragma unroll
             for (int v = 0; v < V; ++v) re[v].template from<kNonTemporal>(rr, (v * T + t) * 8);
         }
-        float h[V][8], ss = 0.0f;
+        float h[V][8], share[C] = {};
         const auto hr = row_of<TR>(p.h, row, cols);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -86,11 +91,11 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
                 re[v].values(h[v]);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(h[v][i], h[v][i], ss);
+            for (int i = 0; i < 8; ++i) share[v % C] = __builtin_fmaf(h[v][i], h[v][i], share[v % C]);
         }
-        ss = sum_row<T>(ss, red[0]);
+        const float ss = sum_row<T, C>(share, red[0]);
         float rstd = 1.0f / sqrtf(ss / (float)cols + p.eps);
-        if (!(ss < __builtin_inff())) rstd = rstd_of_large<T, V>(h, red[1], cols, p.eps);
+        if (!(ss < __builtin_inff())) rstd = rstd_of_large<T, V, C>(h, red[1], cols, p.eps);
         if (p.rstd && t == 0) p.rstd[row] = rstd;
         const auto yr = row_of<TX>(p.y, row, cols, p.y != nullptr);
         const auto qr = row_of<uint8_t>(p.q, row, cols, p.q != nullptr);
@@ -176,7 +181,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_backward_kernel(No
     load(group);
     int turn = 0;
     for (int64_t row = group; row < p.rows; row += stride, turn ^= 1) {
-        float s = 0.0f;
+        float s[1] = {0.0f};
         Eight<TX> d0[V];
         Eight<TH> h0[V], s0[V];
         const float r = rstd;
@@ -189,12 +194,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_backward_kernel(No
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 n[i] *= r;
-                s = __builtin_fmaf(d[i] * w[v][i], n[i], s);
+                s[0] = __builtin_fmaf(d[i] * w[v][i], n[i], s[0]);
                 dw[v][i] = __builtin_fmaf(d[i], n[i], dw[v][i]);
             }
         }
         load(row + stride);
-        const float mean = sum_row<T>(s, red[turn]) / (float)cols;
+        const float mean = sum_row<T, 1>(s, red[turn]) / (float)cols;
         const auto out = row_of<TH>(p.dx, row, cols);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -249,10 +254,10 @@ constexpr int64_t kMaxNormGrid = (int64_t)1 << 21;       // threads of a launch 
 
 template <typename TX, typename TR, bool RES>
 int launch_norm_types(const NormArgs &p, hipStream_t s) {
-    const auto go = [&](auto t, auto v) {
-        constexpr int T = decltype(t)::value, V = decltype(v)::value, R = T < 256 ? 256 / T : 1;
+    const auto go = [&](auto t, auto v, auto c) {
+        constexpr int T = decltype(t)::value, V = decltype(v)::value, C = decltype(c)::value, R = T < 256 ? 256 / T : 1;
         const int64_t grid = (p.rows + R - 1) / R;
-        hipLaunchKernelGGL((rms_norm_kernel<TX, TR, RES, T, V>), dim3((unsigned)(grid < kMaxNormGrid ? grid : kMaxNormGrid)),
+        hipLaunchKernelGGL((rms_norm_kernel<TX, TR, RES, T, V, C>), dim3((unsigned)(grid < kMaxNormGrid ? grid : kMaxNormGrid)),
                            dim3(T < 256 ? 256 : T), 0, s, p);
         return launched();
     };
@@ -261,15 +266,15 @@ int launch_norm_types(const NormArgs &p, hipStream_t s) {
     // 64 rows 5.7, 4.5, 4.3; 1 row 4.6, 3.5, 3.3. 2048 columns, 16384 rows 256 x 1 41, 64 x 4 42; 64 rows 3.2, 5.2. 16384
     // columns, 2048 rows 512 x 4 47, 1024 x 2 51; 16 rows 5.8, 5.3
     const bool few = p.rows <= 512;
-#define QF8_GO(T, V) return go(integral_constant<int, T>{}, integral_constant<int, V>{})
-    if (p.cols <= 512) QF8_GO(64, 1);
-    if (p.cols <= 1024) QF8_GO(64, 2);
-    if (p.cols <= 2048) QF8_GO(256, 1);
-    if (p.cols <= 4096) QF8_GO(256, 2);
-    if (p.cols <= 8192 && few) QF8_GO(512, 2);
-    if (p.cols <= 8192) QF8_GO(256, 4);
-    if (few) QF8_GO(1024, 2);
-    QF8_GO(512, 4);
+#define QF8_GO(T, V, C) return go(integral_constant<int, T>{}, integral_constant<int, V>{}, integral_constant<int, C>{})
+    if (p.cols <= 512) QF8_GO(64, 1, 1);
+    if (p.cols <= 1024) QF8_GO(64, 2, 1);
+    if (p.cols <= 2048) QF8_GO(256, 1, 1);
+    if (p.cols <= 4096) QF8_GO(256, 2, 1);
+    if (p.cols <= 8192 && few) QF8_GO(512, 2, 1);
+    if (p.cols <= 8192) QF8_GO(256, 4, 2);
+    if (few) QF8_GO(1024, 2, 1);
+    QF8_GO(512, 4, 2);
 #undef QF8_GO
 }
 

@@ -26,7 +26,7 @@ def test_norm_refusals():
     assert norm(dt=2) == ENUM and norm(rdt=-1) == ENUM and norm(wdt=3) == ENUM and norm(fmt=2) == ENUM and norm(flags=2) == ENUM
     assert norm(flags=16) == ENUM
     assert norm(rows=-1) == SHAPE and norm(cols=-8) == SHAPE and norm(cols=260) == SHAPE and norm(cols=16392) == SHAPE
-    assert norm(eps=0.0) == SHAPE and norm(eps=-1.0) == SHAPE and norm(eps=INF) == SHAPE and norm(eps=float("nan")) == SHAPE
+    assert norm(eps=0.0) == SHAPE and norm(eps=-1.0) == SHAPE and norm(eps=INF) == SHAPE and norm(eps=1e-40) == SHAPE and norm(eps=float("nan")) == SHAPE
     assert norm(x=None) == NULL and norm(w=None) == NULL and norm(h=None) == NULL and norm(s=None) == NULL and norm(q=None) == NULL
     assert norm(q=None, s=None) == NULL                      # neither codes nor values
     for name in ("x", "r", "w", "q", "h", "y"):
@@ -63,7 +63,7 @@ def test_gate_refusals(back):
         return gate(back=back, **k)
     assert g(dt=2) == ENUM and g(act=2) == ENUM and g(fmt=5) == ENUM and g(flags=3) == ENUM
     assert g(rows=-1) == SHAPE and g(cols=-8) == SHAPE and g(cols=252) == SHAPE
-    assert g(rows=1 << 30, cols=256) == SHAPE and g(rows=1 << 31, cols=8) == SHAPE and g(rows=1, cols=1 << 30) == SHAPE
+    assert g(rows=1 << 28, cols=256) == SHAPE and g(rows=1 << 30, cols=256) == SHAPE and g(rows=1 << 31, cols=8) == SHAPE and g(rows=1, cols=1 << 30) == SHAPE
     assert g(x=None) == NULL and g(q=None) == NULL and g(s=None) == NULL and g(q=None, s=None) == NULL
     assert g(x=ODD) == ALIGN and g(q=ODD) == ALIGN and g(y=ODD) == ALIGN and g(s=UNEVEN) == ALIGN and g(nf=UNEVEN) == ALIGN
     assert g(rows=0, x=None, q=None, s=None) == OK and g(cols=0, x=None) == OK

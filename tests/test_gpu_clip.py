@@ -113,6 +113,10 @@ def test_refusals():
         qf8.clip_grads([g], 1.0, out=[torch.zeros(8, 8, device="cuda", dtype=BF)])
     with pytest.raises(TypeError):
         qf8.clip_grads([g, torch.zeros(3)], 1.0)
+    with pytest.raises(ValueError):
+        qf8.clip_grads([g, g], 1.0)
+    e = torch.empty(0, device="cuda")
+    assert qf8.clip_grads([e, e], 1.0).item() == 0 and qf8.grad_norm([g, g]).item() == 0
     with pytest.raises(qf8.QF8Error):
         qf8.clip_grads([g], 0.0)
     with pytest.raises(qf8.QF8Error):

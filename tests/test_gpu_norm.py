@@ -72,6 +72,19 @@ def test_forward(rows, cols, x, residual, w):
         assert torch.equal(q, got.q) and torch.equal(s, got.scales)
 
 
+@pytest.mark.parametrize("cols", [1032, 4096, 4104, 7168, 8192, 8200, 16384])
+def test_a_row_by_itself(cols):
+    """A row's bits do not hang on how many rows there are."""
+    a, w, r, _ = made(700, cols, BF, F32, F32, seed=cols)
+    every = qf8.rms_norm_quantize(a, w, qf8.E4M3, residual=r, want_rstd=True)
+    for rows in (slice(0, 1), slice(300, 500), slice(699, 700)):
+        some = qf8.rms_norm_quantize(a[rows].contiguous(), w, qf8.E4M3, residual=r[rows].contiguous(), want_rstd=True)
+        assert torch.equal(some.rstd, every.rstd[rows]) and torch.equal(some.q, every.q[rows]) and torch.equal(some.scales, every.scales[rows])
+    x = (a.float() * 2.0 ** 64).contiguous()                # squares beyond fp32
+    big = qf8.rms_norm_quantize(x, w, None, want_rstd=True).rstd
+    assert torch.equal(big[:3], qf8.rms_norm_quantize(x[:3].contiguous(), w, None, want_rstd=True).rstd)
+
+
 def test_alone_and_in_place():
     a, w, r, _ = made(37, 1544, BF, BF, BF, seed=4)
     every = qf8.rms_norm_quantize(a, w, qf8.E4M3, residual=r, want_y=True, want_rstd=True)
