@@ -8,11 +8,12 @@
 // are converted beside the loads and multiplied with BF16 activations (16x16x32 products: sixteen rows of a weight
 // times up to sixteen tokens); a 128x128 block's sums meet 1/S in fp32. The activations are not quantized; those between
 // the products are rounded to BF16 as the second one's operand, which costs what rounding y does (2^-9).
-// us of the two kernels: 64 tokens of 7168, 8 of 64 experts, hidden 2048 310 + 172 (6.1 and 5.5 TB/s; a loop of loads alone
+// us of the two kernels: 64 tokens of 7168, 8 of 64 experts, hidden 2048 310 + 160 (6.1 and 5.9 TB/s; a loop of loads alone
 // reaches 7.1), 1 token of 4096 29 + 16, of which a launch and the list of jobs take 5 each.
 //
 // Every workgroup of the first kernel sorts the choices by expert on its own (in LDS, at most 1024 of them); the first
-// one leaves the list, cut into pieces of up to sixteen tokens of an expert, in the workspace for the second kernel.
+// one leaves the list, cut into pieces of up to 32 tokens of an expert, those of experts with more than sixteen first, in the
+// workspace for the second kernel.
 #include <type_traits>
 
 #include "qf8_act.h"
@@ -26,7 +27,7 @@ typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
 typedef float v4f32 __attribute__((ext_vector_type(4)));
 
 // ---- jobs ---------------------------------------------------------------------------------------
-// A job in 32 bits: expert (10), first entry (10), entries - 1 (6). A piece of one, up to sixteen entries, has its number
+// A job in 32 bits: expert (10), first entry (10), entries - 1 (6). A piece of one, up to 32 entries, has its number
 // in the job and the number of the job's pieces - 1 too (2 each). An entry: choice t * top_k + j (16) and token.
 constexpr int kMaxJobs = kLayerChoices;              // a job, and a piece, has an entry at least
 __device__ __forceinline__ uint32_t pack_job(int e, int start, int n) { return (uint32_t)(e | start << 10 | (n - 1) << 20); }
@@ -46,7 +47,7 @@ struct Jobs {
 
 // All threads of the workgroup; ends with a barrier. The order of an expert's entries is this workgroup's and this run's
 // own: activations are placed by choice, and each is a result of its own. A token that names an expert twice has one entry, at its first choice.
-// cut: the pieces go to p.jobs, their number to p.job_count.
+// cut: the pieces go to p.jobs, their number and that of the first kind to p.job_count.
 template <int THREADS>
 __device__ void find_jobs(const LayerArgs &p, bool cut, Jobs &s) {
     const int n = p.tokens * p.top_k;
@@ -64,31 +65,43 @@ __device__ void find_jobs(const LayerArgs &p, bool cut, Jobs &s) {
     }
     __syncthreads();
     if (threadIdx.x < 64) {                           // counts -> first entries, and the jobs in the order of the experts
-        int entries = 0, jobs = 0, pieces = 0;
+        int entries = 0, jobs = 0, large = 0, small = 0;       // pieces of experts with more than sixteen entries, and of the others
+        for (int base = 0; cut && base < p.experts; base += 64) {
+            const int c = base + (int)threadIdx.x < p.experts ? s.start[base + threadIdx.x] : 0;
+            small += __popcll(__ballot(c > 16)) + __popcll(__ballot(c > 32));       // where the others begin
+        }
+        if (cut && threadIdx.x == 0) p.job_count[1] = small;
         for (int base = 0; base < p.experts; base += 64) {
             const int e = base + (int)threadIdx.x;
-            const int c = e < p.experts ? s.start[e] : 0, q = (c + 15) / 16;
-            int before = c, qbefore = q;              // inclusive sums over the lanes
+            const int c = e < p.experts ? s.start[e] : 0;
+            int before = c;                           // inclusive sum over the lanes
 #pragma unroll
             for (int off = 1; off < 64; off <<= 1) {
-                const int a = __shfl_up(before, off), b = __shfl_up(qbefore, off);
-                if ((int)threadIdx.x >= off) { before += a; qbefore += b; }
+                const int a = __shfl_up(before, off);
+                if ((int)threadIdx.x >= off) before += a;
             }
-            const uint64_t chosen = __ballot(c > 0);
+            const uint64_t chosen = __ballot(c > 0), first = __ballot(c > 16), second = __ballot(c > 32);
+            const uint64_t below = (1ull << threadIdx.x) - 1;
             const int at = entries + before - c;
             if (e < p.experts) s.start[e] = at;
-            if (c > 0) s.job[jobs + __popcll(chosen & ((1ull << threadIdx.x) - 1))] = pack_job(e, at, c);
-            for (int k = 0; cut && k < q; ++k)
-                p.jobs[pieces + qbefore - q + k] =
-                    pack_job(e, at + k * 16, c - k * 16 < 16 ? c - k * 16 : 16) | (uint32_t)k << 26 | (uint32_t)(q - 1) << 28;
+            if (c > 0) s.job[jobs + __popcll(chosen & below)] = pack_job(e, at, c);
+            if (cut && c > 16) {
+                const int to = large + __popcll(first & below) + __popcll(second & below);
+                const uint32_t pieces = c > 32 ? 1u << 28 : 0u;
+                p.jobs[to] = pack_job(e, at, c > 32 ? 32 : c) | pieces;
+                if (c > 32) p.jobs[to + 1] = pack_job(e, at + 32, c - 32) | pieces | 1u << 26;
+            } else if (cut && c > 0) {
+                p.jobs[small + __popcll(chosen & ~first & below)] = pack_job(e, at, c);
+            }
+            large += __popcll(first) + __popcll(second);
+            small += __popcll(chosen & ~first);
             entries += __shfl(before, 63);
-            pieces += __shfl(qbefore, 63);
             jobs += __popcll(chosen);
         }
         if (threadIdx.x == 0) {
             s.total = jobs;
             s.entries = entries;
-            if (cut) *p.job_count = pieces;
+            if (cut) p.job_count[0] = small;
         }
     }
     __syncthreads();
@@ -240,9 +253,9 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
         const int all = __builtin_amdgcn_readfirstlane(job_count(job));
         for (int c0 = 0; c0 < all; c0 += 32) {
             const int start = job_start(job) + c0, count = all - c0 < 32 ? all - c0 : 32;
-            // NX: instructions that load sixteen tokens, NC: sixteens of tokens, XS: steps that these are loaded ahead
-            const auto run = [&](auto nx, auto nc, auto xs) {
-                constexpr int NX = decltype(nx)::value, NC = decltype(nc)::value, XS = decltype(xs)::value;
+            // NX: instructions that load sixteen tokens, NC: sixteens of tokens
+            const auto run = [&](auto nx, auto nc) {
+                constexpr int NX = decltype(nx)::value, NC = decltype(nc)::value;
                 uint32_t xrow[NC][NX];
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
@@ -254,7 +267,7 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
                 v4f32 acc[NC][2];
 #pragma unroll
                 for (int c = 0; c < NC; ++c) acc[c][0] = acc[c][1] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
-                uint4 w[2][2][2], x[XS][4];
+                uint4 w[2][2][2], x[2][4];
                 const auto load_w = [&](uint4 (&to)[2][2], int i) {
                     const int k0 = (wave + i * kUpWaves) * 128;
                     const bool in = k0 + 16 * (lane & 7) < dim;
@@ -270,29 +283,31 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
 #pragma unroll
                     for (int q = 0; q < NX; ++q) to[q] = buf_load16(xr, in ? xrow[c][q] : kOutOfRange, (uint32_t)(2 * k0));
                 };
-                const auto step = [&](uint4 (&from)[2][2], uint4 (&xfrom)[4], int i) {
+                // one sixteen of tokens: its x of two steps; two: those of the next step
+                const auto step = [&](uint4 (&from)[2][2], int s, int i) {
                     uint4 wo[2][2];
                     turn_weights<2>(from, tile[wave], wo);
                     const float f[2] = {__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv[0]), i)),
                                         __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv[1]), i))};
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
+                        uint4(&xfrom)[4] = x[NC > 1 ? c : s];
                         place_tokens(xfrom, NX, tile[wave]);
-                        if (c + 1 < NC) load_x(xfrom, i, c + 1);
-                        else load_x(xfrom, i + XS, 0);
+                        load_x(xfrom, NC > 1 ? i + 1 : i + 2, c);
                         if (c + 1 == NC) load_w(from, i + 2);        // last: loads come back in their order
                         multiply<FMT, 2>(wo, tile[wave], f, acc[c]);
                     }
                 };
                 load_x(x[0], 0, 0);
+                if (NC > 1) load_x(x[1], 0, NC - 1);
                 load_w(w[0], 0);
-                if (XS > 1) load_x(x[XS - 1], 1, 0);
+                if (NC == 1) load_x(x[1], 1, 0);
                 load_w(w[1], 1);
                 // both steps always: a step behind the last one multiplies zeros. A branch around loads would make every wait
                 // count on the fewest of them
                 for (int i = 0; i < steps; i += 2) {
-                    step(w[0], x[0], i);
-                    step(w[1], x[XS - 1], i + 1);
+                    step(w[0], 0, i);
+                    step(w[1], 1, i + 1);
                 }
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
@@ -304,10 +319,10 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
             const integral_constant<int, 1> one;
             const integral_constant<int, 2> two;
             const integral_constant<int, 4> four;
-            if (count <= 4) run(one, one, two);
-            else if (count <= 8) run(two, one, two);
-            else if (count <= 16) run(four, one, two);
-            else run(four, two, one);
+            if (count <= 4) run(one, one);
+            else if (count <= 8) run(two, one);
+            else if (count <= 16) run(four, one);
+            else run(four, two);
             __syncthreads();
             // one hidden unit of one token to a thread
             for (int c = 0; c * 16 < count; ++c) {
@@ -338,11 +353,11 @@ constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves, kDownTiles = 2, kD
 
 template <int FMT, int CP>
 __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p) {
-    constexpr int W = kDownWaves, RT = kDownTiles, COLS = kDownCols, D = 2;
+    constexpr int W = kDownWaves, RT = kDownTiles, COLS = kDownCols;
     extern __shared__ float sums[];                   // [waves][tokens][COLS], then the list
     __shared__ __align__(16) char tile[W][4096];
     __shared__ int arrived;
-    const int n = p.tokens * p.top_k, total = *p.job_count;
+    const int n = p.tokens * p.top_k, total = p.job_count[0], large = p.job_count[1];
     uint32_t *entry = (uint32_t *)(sums + W * p.tokens * COLS);
     float *weight = (float *)(entry + n);
     uint32_t *piece_list = (uint32_t *)(weight + n);
@@ -358,8 +373,13 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
     __syncthreads();
     const int hidden = p.hidden, gk = (hidden + 127) / 128, gn = (p.dim + 127) / 128;
     const int column = (int)blockIdx.x / p.parts, share = (int)blockIdx.x % p.parts, d0 = column * COLS;
-    const int64_t units = (int64_t)total * gk;
-    const int lo = (int)(units * (share * W + wave) / (p.parts * W)), hi = (int)(units * (share * W + wave + 1) / (p.parts * W));
+    // Equal parts in time: a step of up to 32 tokens counts as one and a half of sixteen. us, 64 tokens of 7168, 8 of 64 experts, as
+    // one / one and a half / two: 487 / 469 / 469 for both kernels, of 4096, 4 of 16 experts 119 / 114 / 114.
+    const auto bound = [&](int part) {
+        const int64_t first = (int64_t)large * gk, at = (first * 3 + ((int64_t)total * gk - first) * 2) * part / (p.parts * W);
+        return (int)(at < first * 3 ? at / 3 : first + (at - first * 3) / 2);
+    };
+    const int lo = bound(share * W + wave), hi = bound(share * W + wave + 1);
     const auto ar = make_rsrc(p.a, (uint32_t)n * (uint32_t)hidden * 2u);
     uint32_t wrow[RT];
 #pragma unroll
@@ -380,11 +400,12 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
         at.pieces = piece_total(piece_at(at.base));
         return true;
     };
-    // NX: instructions that load sixteen tokens, enough for each piece of this wave. Loads run D steps ahead of the products,
-    // each side with a place of its own, and each step issues the same ones (behind the end: none from memory), so a wait
-    // counts on all of them. They come back in their order: activations loaded later than the next weights would hold those up.
-    const auto run = [&](auto instructions) {
-        constexpr int NX = decltype(instructions)::value;
+    // NX: instructions that load sixteen tokens, NC: sixteens of tokens, enough for each piece of this wave. Loads run ahead of
+    // the products, weights two steps and tokens two (NC 2: one), each side with a place of its own, and each step issues the same
+    // ones (behind the end: none from memory), so a wait counts on all of them. They come back in their order: tokens loaded later
+    // than the next weights would hold those up.
+    const auto run = [&](auto instructions, auto sixteens) {
+        constexpr int NX = decltype(instructions)::value, NC = decltype(sixteens)::value;
         const uint32_t first = piece_at(lo / gk);
         Place pw;
         pw.base = lo / gk - piece_number(first);
@@ -398,21 +419,28 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
             wr = make_rsrc(p.w2 + (int64_t)e * p.dim * hidden, (uint32_t)p.dim * (uint32_t)hidden);
             sr = make_rsrc(p.s2 + ((int64_t)e * gn + d0 / 128) * gk, (uint32_t)gk * 4u);
         };
-        uint32_t arow[NX];
+        uint32_t arow[NC][NX];
         const auto place_x = [&]() {
             const uint32_t piece = piece_at(px.base + px.piece);
 #pragma unroll
-            for (int q = 0; q < NX; ++q) {
-                const int at = 4 * q + g;
-                const uint32_t row = entry[job_start(piece) + (at < job_count(piece) ? at : 0)] & 0xFFFF;
-                arow[q] = at < job_count(piece) ? row * (uint32_t)hidden * 2u + 16 * r : kOutOfRange;
-            }
-        };
-        uint4 w[D][RT][2], x[D][4];
-        float scale_of[D];
-        v4f32 acc[RT];
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int q = 0; q < NX; ++q) {
+                    const int at = 16 * c + 4 * q + g;
+                    const uint32_t row = entry[job_start(piece) + (at < job_count(piece) ? at : 0)] & 0xFFFF;
+                    arow[c][q] = at < job_count(piece) ? row * (uint32_t)hidden * 2u + 16 * r : kOutOfRange;
+                }
+        };
+        uint4 w[2][RT][2], x[2][4];
+        float scale_of[2];
+        v4f32 acc[NC][RT];
+        const auto clear = [&]() {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) acc[c][t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+        };
+        clear();
         const auto load_w = [&](uint4 (&to)[RT][2], float &f, int unit) {
             const int k0 = pw.block * 128;
             const bool in = unit < hi && k0 + 16 * (lane & 7) < hidden;
@@ -425,65 +453,75 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
                     to[t][h] = buf_load16<CP>(wr, in ? wrow[t] : kOutOfRange, (uint32_t)(k0 + 8 * h * hidden));
             if (next(pw)) place_w();
         };
-        const auto load_x = [&](uint4 (&to)[4], int unit) {
+        const auto load_x = [&](uint4 (&to)[4], int unit, int c) {
             const int k0 = px.block * 128;
             const bool in = unit < hi && k0 + 8 * r < hidden;
 #pragma unroll
-            for (int q = 0; q < NX; ++q) to[q] = buf_load16(ar, in ? arow[q] : kOutOfRange, (uint32_t)(2 * k0));
-            if (next(px) || px.pieces > 1) place_x();
+            for (int q = 0; q < NX; ++q) to[q] = buf_load16(ar, in ? arow[c][q] : kOutOfRange, (uint32_t)(2 * k0));
+            if (c + 1 == NC && (next(px) || px.pieces > 1)) place_x();
         };
-        const auto step = [&](uint4 (&wfrom)[RT][2], uint4 (&xfrom)[4], float &f, int unit) {
+        const auto step = [&](int s, int unit) {
             uint4 wo[RT][2];
-            turn_weights<RT>(wfrom, tile[wave], wo);
-            place_tokens(xfrom, NX, tile[wave]);
+            turn_weights<RT>(w[s], tile[wave], wo);
             float inv[RT];
 #pragma unroll
-            for (int t = 0; t < RT; ++t) inv[t] = unit < hi ? 1.0f / f : 0.0f;
-            load_x(xfrom, unit + D);
-            load_w(wfrom, f, unit + D);
-            multiply<FMT, RT>(wo, tile[wave], inv, acc);
+            for (int t = 0; t < RT; ++t) inv[t] = unit < hi ? 1.0f / scale_of[s] : 0.0f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                uint4(&from)[4] = x[NC > 1 ? c : s];
+                place_tokens(from, NX, tile[wave]);
+                load_x(from, NC > 1 ? unit + 1 : unit + 2, c);
+                if (c + 1 == NC) load_w(w[s], scale_of[s], unit + 2);
+                multiply<FMT, RT>(wo, tile[wave], inv, acc[c]);
+            }
             if (unit < hi && (pu.pieces > 1 || pu.block + 1 == gk || unit + 1 == hi)) {
                 const uint32_t piece = piece_at(pu.base + pu.piece);
-                if (r < job_count(piece)) {
-                    const int k = job_start(piece) + r;
-                    const float f = weight[k];
 #pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        v4f32 *to = (v4f32 *)(mine + (entry[k] >> 16) * COLS + 16 * t + 4 * g);
-                        v4f32 v = *to;
+                for (int c = 0; c < NC; ++c)
+                    if (16 * c + r < job_count(piece)) {
+                        const int k = job_start(piece) + 16 * c + r;
+                        const float f = weight[k];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(f, acc[t][q], v[q]);
-                        *to = v;
+                        for (int t = 0; t < RT; ++t) {
+                            v4f32 *to = (v4f32 *)(mine + (entry[k] >> 16) * COLS + 16 * t + 4 * g);
+                            v4f32 v = *to;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(f, acc[c][t][q], v[q]);
+                            *to = v;
+                        }
                     }
-                }
-#pragma unroll
-                for (int t = 0; t < RT; ++t) acc[t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+                clear();
             }
             next(pu);
         };
         place_w();
         place_x();
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            load_x(x[d], lo + d);
-            load_w(w[d], scale_of[d], lo + d);
-        }
-        for (int u = lo; u < hi; u += D) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) step(w[d], x[d], scale_of[d], u + d);
+        load_x(x[0], lo, 0);
+        if (NC > 1) load_x(x[1], lo, NC - 1);
+        load_w(w[0], scale_of[0], lo);
+        if (NC == 1) load_x(x[1], lo + 1, 0);
+        load_w(w[1], scale_of[1], lo + 1);
+        for (int u = lo; u < hi; u += 2) {
+            step(0, u);
+            step(1, u + 1);
         }
     };
     if (lo < hi) {
         int most = 0;
-        for (int j = lo / gk; j <= (hi - 1) / gk; ++j) {       // and the other pieces of the first and last expert
+        for (int j = lo / gk; j <= (hi - 1) / gk; ++j) {       // an expert's second piece may have few where its first has 32
             const uint32_t piece = piece_at(j);
-            most = piece_total(piece) > 1 ? 16 : most > job_count(piece) ? most : job_count(piece);
-            if (most == 16) break;
+            const int count = piece_total(piece) > 1 ? 32 : job_count(piece);
+            most = most > count ? most : count;
+            if (most > 16) break;
         }
         using std::integral_constant;
-        if (most <= 4) run(integral_constant<int, 1>{});
-        else if (most <= 8) run(integral_constant<int, 2>{});
-        else run(integral_constant<int, 4>{});
+        const integral_constant<int, 1> one;
+        const integral_constant<int, 2> two;
+        const integral_constant<int, 4> four;
+        if (most <= 4) run(one, one);
+        else if (most <= 8) run(two, one);
+        else if (most <= 16) run(four, one);
+        else run(four, two);
     }
     __syncthreads();
     const int values = p.tokens * COLS;

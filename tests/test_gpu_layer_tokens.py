@@ -77,6 +77,10 @@ def test_choices_of_any_kind():
     y = qf8.expert_layer_tokens(*args, qf8.E4M3)
     check(y, *args, qf8.E4M3, qf8.ACT_SILU)
     assert bool((y[2] == 0).all()) and bool((y[4] == 0).all())
+    for counts in ([64], [33, 31], [32, 16, 16], [17, 47], [1, 2, 3, 40, 18]):       # pieces of one and two sixteens, and second pieces
+        ids = torch.cat([torch.full((c,), e, dtype=torch.int32) for e, c in enumerate(counts)])[torch.randperm(sum(counts))].cuda()[:, None].contiguous()
+        args = made(sum(counts), 272, 400, 6, 1, qf8.E4M3, seed=sum(counts), ids=ids)
+        check(qf8.expert_layer_tokens(*args, qf8.E4M3), *args, qf8.E4M3, qf8.ACT_SILU)
     for expert in (0, 5, 7):
         ids = torch.full((40, 2), expert, dtype=torch.int32, device="cuda")
         args = made(40, 256, 192, 6, 2, qf8.E4M3, seed=2, ids=ids)
