@@ -14,7 +14,8 @@ namespace qf8 {
 template <bool EXACT>
 __device__ __forceinline__ float sigmoid(float z) {
     constexpr float kLog2E = 1.44269504088896341f, kRest = (float)(1.4426950408889634074 - (double)kLog2E);
-    if constexpr (EXACT) z = __builtin_amdgcn_fmed3f(z, -200.0f, 200.0f);      // 0 or 1 from here on, and no Inf - Inf below
+    // 0 or 1 beyond, and no Inf - Inf below; NaN stays
+    if constexpr (EXACT) z = z != z ? z : __builtin_amdgcn_fmed3f(z, -200.0f, 200.0f);
     const float t = z * -kLog2E;
     float e = __builtin_amdgcn_exp2f(t);
     if constexpr (EXACT)                              // 2^rest = 1 + rest ln 2, the rest below 2^-17

@@ -137,6 +137,13 @@ def test_ends_of_the_range(act, dtype):
         flag.zero_()
         qf8.gated_act_quantize(z, qf8.E4M3, act=act, nonfinite=flag)
         assert flag.item() == 1
+        flag.zero_()
+        dx = qf8.gated_act_backward(torch.ones(3, 128, device="cuda", dtype=dtype), z, None, act=act, want_dx=True, nonfinite=flag)[2]
+        if bad != bad:
+            assert bool(dx[0, [5, 133]].isnan().all())
+        rest = torch.ones(3, 256, dtype=torch.bool, device="cuda")
+        rest[0, [5, 133]] = False
+        assert flag.item() == 1 and bool(dx[rest].isfinite().all())
 
 
 def test_sizes_of_nothing_and_refusals():
