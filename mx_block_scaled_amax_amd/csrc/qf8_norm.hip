@@ -6,8 +6,9 @@
 //
 // A row stays in registers from its load to its codes, so each input is read and each output written once:
 // HBM is the bound (8192 rows of 7168 BF16 with residual 70 us, 5.9 TB/s; 16384 of 4096 75 us, 6.3; a copy of 2 GiB 4.95).
-// Loads are non-temporal, stores are not (70 us; all cached 78, all non-temporal 73). A group of 128 is sixteen lanes with eight values each, so its maximum is four DPP steps;
-// the row's sum takes one more exchange through LDS where several waves share a row.
+// Loads are non-temporal, stores are not (70 us; all cached 78, all non-temporal 73). A group of 128 is sixteen lanes with
+// eight values each, so its maximum is four DPP steps; the row's sum takes one more exchange through LDS where several waves
+// share a row.
 #include <type_traits>
 
 #include "qf8_internal.h"
