@@ -288,14 +288,15 @@ int launch_norm_backward_types(const NormArgs &p, hipStream_t s) {
         return launched();
     };
     using std::integral_constant;
-    // Few values to a thread, so that the next row's loads find registers. us, 8192 rows of 4096: 512 x 1 44.8, 256 x 2 44.5
+    // Few values to a thread, so that the next row's loads find registers. us, 8192 rows of 4096: 512 x 1 44.8, 256 x 2 44.5;
+    // 4096 of 16384 512 x 4 91, 1024 x 2 102, of 12296 with h in FP32 (some registers in scratch) 175, 206
 #define QF8_GO(T, V) return go(integral_constant<int, T>{}, integral_constant<int, V>{})
     if (p.cols <= 512) QF8_GO(64, 1);
     if (p.cols <= 1024) QF8_GO(64, 2);
     if (p.cols <= 2048) QF8_GO(256, 1);
     if (p.cols <= 4096) QF8_GO(512, 1);
     if (p.cols <= 8192) QF8_GO(1024, 1);
-    QF8_GO(1024, 2);
+    QF8_GO(512, 4);
 #undef QF8_GO
 }
 
