@@ -59,6 +59,14 @@ __device__ __forceinline__ int64_t first_row() {
     return (int64_t)blockIdx.x * R + (T < 256 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0);
 }
 
+// Whether piece v of the whole wave lies behind the columns. Its loads are idle ones all the same (a branch around loads would
+// make waits count on the fewest of them), the work on it is left out. us with that work / without it, no residual: 8192 rows of
+// 5120 40.8 / 35.6, 16384 of 2056 42.3 / 38.6, 333 of 4104 5.0 / 4.7, whole pieces the same; gradients, 8192 of 4104 59.8 / 53.5.
+template <int T>
+__device__ __forceinline__ bool behind(int v, int cols) {
+    return __builtin_amdgcn_readfirstlane((v * T + (int)(threadIdx.x % T)) * 8) >= cols;
+}
+
 // T threads to a row, V pieces of eight columns to a thread: cols <= 8 T V. TR: type of the residual (RES) and of h.
 // C: shares of a thread's sum, so that a row's bits do not hang on the number of rows.
 template <typename TX, typename TR, bool RES, int T, int V, int C>
@@ -82,6 +90,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             xe[v].values(h[v]);
+            if (v > 0 && behind<T>(v, cols)) continue;
             if constexpr (RES) {
                 float r[8];
                 re[v].values(r);
@@ -103,6 +112,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int col = (v * T + t) * 8;
+            if (v > 0 && behind<T>(v, cols)) break;
             float w[8], y[8];
             if (p.w_fp32) {
                 Eight<float> e;
@@ -114,8 +124,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
                 e.values(w);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = col < cols ? h[v][i] * rstd * w[i] : 0.0f;
-            const uint32_t amax = group_amax(y);
+            for (int i = 0; i < 8; ++i) y[i] = h[v][i] * rstd * w[i];
+            const uint32_t amax = group_amax(y, col < cols);       // behind the columns 0 times R, which may be NaN
             const bool first = (threadIdx.x & 15) == 0 && col < cols;
             if (p.nonfinite && first && amax >= 0x7F800000u) *p.nonfinite = 1;
             if (p.y) {
@@ -189,6 +199,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_backward_kernel(No
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             d0[v] = de[v]; h0[v] = he[v]; s0[v] = se[v];
+            if (behind<T>(v, cols)) continue;
             float d[8], n[8];
             d0[v].values(d);
             h0[v].values(n);
@@ -204,6 +215,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_backward_kernel(No
         const auto out = row_of<TH>(p.dx, row, cols);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            if (behind<T>(v, cols)) break;
             float d[8], n[8], o[8];
             d0[v].values(d);
             h0[v].values(n);
@@ -215,7 +227,22 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_backward_kernel(No
             e.template to<kCached>(out, (v * T + t) * 8);
         }
     }
-    if (p.partial) {
+    if constexpr (R > 1) {                            // a wave has a share of its own: joined first, in the order of the waves
+        __shared__ __align__(16) float share[R][V * T * 8];
+        if (!p.partial) return;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; i += 4)
+                *(float4 *)&share[threadIdx.x / T][(v * T + t) * 8 + i] = make_float4(dw[v][i], dw[v][i + 1], dw[v][i + 2], dw[v][i + 3]);
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += 256) {
+            float sum = share[0][c];
+#pragma unroll
+            for (int i = 1; i < R; ++i) sum += share[i][c];
+            p.partial[(int64_t)blockIdx.x * cols + c] = sum;
+        }
+    } else if (p.partial) {
         const auto to = row_of<float>(p.partial, group, cols);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -282,14 +309,14 @@ int launch_norm_types(const NormArgs &p, hipStream_t s) {
 template <typename TX, typename TH>
 int launch_norm_backward_types(const NormArgs &p, hipStream_t s) {
     const auto go = [&](auto t, auto v) {
-        constexpr int T = decltype(t)::value, V = decltype(v)::value, R = T < 256 ? 256 / T : 1;
-        const int64_t grid = norm_backward_groups(p.rows, p.cols) / R;
+        constexpr int T = decltype(t)::value, V = decltype(v)::value;
+        const int64_t grid = norm_backward_groups(p.rows, p.cols);
         hipLaunchKernelGGL((rms_norm_backward_kernel<TX, TH, T, V>), dim3((unsigned)grid), dim3(T < 256 ? 256 : T), 0, s, p);
         return launched();
     };
     using std::integral_constant;
     // Few values to a thread, so that the next row's loads find registers. us, 8192 rows of 4096: 512 x 1 44.8, 256 x 2 44.5;
-    // 4096 of 16384 512 x 4 91, 1024 x 2 102, of 12296 with h in FP32 (some registers in scratch) 175, 206
+    // 4096 of 16384 512 x 4 94, 1024 x 2 102, of 12296 with h in FP32 (some registers in scratch) 175, 206
 #define QF8_GO(T, V) return go(integral_constant<int, T>{}, integral_constant<int, V>{})
     if (p.cols <= 512) QF8_GO(64, 1);
     if (p.cols <= 1024) QF8_GO(64, 2);
@@ -302,10 +329,11 @@ int launch_norm_backward_types(const NormArgs &p, hipStream_t s) {
 
 }  // namespace
 
-// us with the joining kernel, 8192 rows of 4096: 512 groups 48.9, 768 51.9, 2048 62
+// us with the joining kernel, 8192 rows of 4096: 512 groups 48.9, 768 51.9, 2048 62; without it, 65536 of 512 (four rows at
+// once) 512 groups 45.6, 1024 45.3, 2048 48.1, 128 124
 int64_t norm_backward_groups(int64_t rows, int64_t cols) {
-    const int64_t r = cols <= 1024 ? 4 : 1, most = 512;      // rows that a workgroup takes at once
-    const int64_t groups = (rows + r - 1) / r * r;
+    const int64_t r = cols <= 1024 ? 4 : 1, most = 512;      // r: rows that a workgroup takes at once
+    const int64_t groups = (rows + r - 1) / r;
     return groups < most ? groups : most;
 }
 

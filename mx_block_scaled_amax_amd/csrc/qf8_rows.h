@@ -69,12 +69,12 @@ __device__ __forceinline__ float sum_wave(float v) {
     return v;
 }
 
-// |amax| bits of a 1x128 group: sixteen lanes of a DPP row, eight values each. NaN sorts above every value.
-__device__ __forceinline__ uint32_t group_amax(const float *y) {
+// |amax| bits of a 1x128 group: sixteen lanes of a DPP row, eight values each of those that have some. NaN sorts above every value.
+__device__ __forceinline__ uint32_t group_amax(const float *y, bool there = true) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = umax(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-    return max_row16(m);
+    return max_row16(there ? m : 0);
 }
 // The group's scale and this lane's eight codes.
 __device__ __forceinline__ float group_scale(uint32_t amax, int fmt, int pow2) {

@@ -124,7 +124,7 @@ def test_ends_of_the_range(cols):
     assert flag.item() == 0
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 8), (1, 4096), (3, 136), (4100, 128), (1030, 1032), (17, 2048), (1500, 4096),
+@pytest.mark.parametrize("rows,cols", [(1, 8), (1, 4096), (3, 136), (4100, 128), (2101, 1000), (1030, 1032), (17, 2048), (1500, 4096),
                                        (5, 7168), (2, 8200), (1029, 16384)])
 @pytest.mark.parametrize("dy,h,w,dres", [(BF, BF, BF, True), (BF, F32, F32, False), (F32, BF, F32, False), (F32, F32, BF, True)])
 def test_backward(rows, cols, dy, h, w, dres):
