@@ -704,6 +704,7 @@ qf8_status rms_norm_quantize(const void *x, qf8_dtype dtype, const void *residua
     p.nonfinite = nonfinite;
     p.rows = rows; p.cols = cols; p.gcols = (cols + 127) / 128;
     p.eps = eps;
+    p.inv_cols = 1.0f / (float)cols;
     p.w_fp32 = weight_dtype == QF8_IN_FP32;
     p.fmt = fmt; p.pow2 = flags & QF8_FLAG_POW2_SCALES;
     return status_of(qf8::launch_norm(p, dtype, residual_dtype, as_stream(stream)));
@@ -729,6 +730,7 @@ qf8_status rms_norm_backward(const void *dy, qf8_dtype dtype, const void *h, qf8
     p.dy = dy; p.hin = h; p.rstd_in = rstd; p.weight = weight; p.dres = dres; p.dx = dx;
     p.partial = dweight ? (float *)ws : nullptr;
     p.rows = rows; p.cols = cols;
+    p.inv_cols = 1.0f / (float)cols;
     p.w_fp32 = weight_dtype == QF8_IN_FP32;
     return status_of(qf8::launch_norm_backward(p, dtype, h_dtype, dweight, as_stream(stream)));
 }

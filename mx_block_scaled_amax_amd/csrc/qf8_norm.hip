@@ -104,7 +104,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
             for (int i = 0; i < 8; ++i) share[v % C] = __builtin_fmaf(h[v][i], h[v][i], share[v % C]);
         }
         const float ss = sum_row<T, C>(share, red[0]);
-        float rstd = 1.0f / sqrtf(ss / (float)cols + p.eps);
+        // the hardware's root, an ulp, and a product for the mean. us, IEEE divisions and root / this, no residual: 1 row of 7168
+        // 3.1 / 2.9, 16384 of 2056 39.4 / 37.5
+        float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_cols, p.eps));
         if (!(ss < __builtin_inff())) rstd = rstd_of_large<T, V, C>(h, red[1], cols, p.eps);
         if (p.rstd && t == 0) p.rstd[row] = rstd;
         const auto yr = row_of<TX>(p.y, row, cols, p.y != nullptr);
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_backward_kernel(No
             }
         }
         load(row + stride);
-        const float mean = sum_row<T, 1>(s, red[turn]) / (float)cols;
+        const float mean = sum_row<T, 1>(s, red[turn]) * p.inv_cols;
         const auto out = row_of<TH>(p.dx, row, cols);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
