@@ -501,11 +501,12 @@ qf8_status gated_act_backward(const void *dy, const void *x, qf8_dtype dtype, in
                               qf8_fmt fmt, int flags, uint8_t *q, float *scales, void *dx, int32_t *nonfinite, void *stream);
 
 /* A whole expert layer with gated activation for a few tokens, in two kernels:
- *   y[t] = sum_j weights[t][j] W2[e] a,  a = rnd_bf16(act(A x[t]) * (B x[t])),  W1[e] = [A; B],  e = ids[t][j].
+ *   y[t] = sum_j weights[t][j] W2[e] a,  a = act(A x[t]) * (B x[t]),  W1[e] = [A; B],  e = ids[t][j].
  * x and y [tokens][dim] BF16. w1: codes [experts][2 hidden][dim] with 128x128 scales s1
  * [experts][ceil(2 hidden/128)][ceil(dim/128)]; w2: codes [experts][dim][hidden], s2 [experts][ceil(dim/128)]
- * [ceil(hidden/128)], both of fmt as quantize_block writes them. The activations are not quantized: products of BF16
- * with the codes' exact values, fp32 sums, y rounded once. ids, weights [tokens][top_k] as route_experts gives them; an
+ * [ceil(hidden/128)], both of fmt as quantize_block writes them. The activations are not quantized: products of 16-bit
+ * values with the codes' exact values, fp32 sums, y rounded once; a has 11 bits (FP16 under powers of two), down to 2^-28 of the
+ * largest of its 128 neighbours, and below that it is off by 2^-39 of it. ids, weights [tokens][top_k] as route_experts gives them; an
  * id outside [0, experts) adds nothing, one that a token has twice counts with the sum of its weights. The same
  * call gives the same bits. tokens <= 64, tokens * top_k <= 1024, experts <= 1024, top_k <= 64; dim, hidden
  * multiples of 16 and <= 32768. Tensors and ws 16-byte aligned, scales, ids and weights 4-byte; y overlaps no input.

@@ -189,7 +189,8 @@ struct LayerArgs {
     const float *weights;
     uint16_t *y;
     int tokens, top_k, experts, dim, hidden;
-    uint16_t *a;                 // workspace: activations [choice][hidden], and the list of jobs
+    uint16_t *a;                 // workspace: activations [choice][hidden], their scales by sixteen, and the list of jobs
+    uint8_t *a_scales;
     uint32_t *jobs, *entries;
     float *entry_weights;
     int *job_count;

@@ -1,14 +1,15 @@
 // qf8_layer.hip -- a whole expert layer with gated activation for a few tokens, in two kernels.
 //
-//   a[t][e] = rnd_bf16(act(A_e x[t]) * (B_e x[t])),  W1[e] = [A_e; B_e]      the first kernel
+//   a[t][e] = act(A_e x[t]) * (B_e x[t]),  W1[e] = [A_e; B_e]                the first kernel
 //   y[t]    = rnd_bf16(sum_e wt[t][e] W2[e] a[t][e])                          the second
 //
 // Each chosen expert's weights are read once, which is the bound: a weight's byte takes part in as many products as
-// its expert has tokens, about eight, where the matrix cores would need hundreds. Codes are exact in BF16, so they
-// are converted beside the loads and multiplied with BF16 activations (16x16x32 products: sixteen rows of a weight
-// times up to sixteen tokens); a 128x128 block's sums meet 1/S in fp32. The activations are not quantized; those between
-// the products are rounded to BF16 as the second one's operand, which costs what rounding y does (2^-9).
-// us of the two kernels: 64 tokens of 7168, 8 of 64 experts, hidden 2048 310 + 160 (6.1 and 5.9 TB/s; a loop of loads alone
+// its expert has tokens, about eight, where the matrix cores would need hundreds. Codes are exact in BF16 and in FP16, so they
+// are converted beside the loads and multiplied with 16-bit activations (16x16x32 products: sixteen rows of a weight
+// times up to sixteen tokens); a 128x128 block's sums meet 1/S in fp32. The activations are not quantized: x is BF16, and those
+// between the products are FP16 times a power of two for sixteen neighbours, 2^-11 off, an eighth of what rounding y is (BF16 has
+// them off by as much as y, for 4% less time with 64 tokens of 7168, 8 of 64 experts; two BF16 pieces take 8% more).
+// us of the two kernels: 64 tokens of 7168, 8 of 64 experts, hidden 2048 312 + 174 (6.1 and 5.4 TB/s; a loop of loads alone
 // reaches 7.1), 1 token of 4096 29 + 16, of which a launch and the list of jobs take 5 each.
 //
 // Every workgroup of the first kernel sorts the choices by expert on its own (in LDS, at most 1024 of them); the first
@@ -24,6 +25,8 @@ namespace qf8 {
 namespace {
 
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
+typedef _Float16 v2f16 __attribute__((ext_vector_type(2)));
+typedef _Float16 v8f16 __attribute__((ext_vector_type(8)));
 typedef float v4f32 __attribute__((ext_vector_type(4)));
 
 // ---- jobs ---------------------------------------------------------------------------------------
@@ -116,23 +119,51 @@ __device__ void find_jobs(const LayerArgs &p, bool cut, Jobs &s) {
 
 // ---- products -----------------------------------------------------------------------------------
 
-// Sixteen codes of a row (k ascending) -> two operands of eight BF16 values, exactly.
-template <int FMT>
-__device__ __forceinline__ v8bf16 operand(uint32_t lo, uint32_t hi) {
-    v2bf16 p[4];
-    if constexpr (FMT == kE4M3) {
-        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-    } else {
-        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false);
-        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true);
-        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false);
-        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true);
+// Eight codes of a row (k ascending) -> an operand of eight values, exactly, and products of operands. Bf16: of x. Fp16: of the
+// activations between the products.
+struct Bf16 {
+    typedef v8bf16 Operand;
+    template <int FMT> static __device__ __forceinline__ Operand of(uint32_t lo, uint32_t hi) {
+        v2bf16 p[4];
+        if constexpr (FMT == kE4M3) {
+            p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+            p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+            p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+            p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+        } else {
+            p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false);
+            p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true);
+            p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false);
+            p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true);
+        }
+        return Operand{p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y};
     }
-    return v8bf16{p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y};
-}
+    static __device__ __forceinline__ v4f32 product(Operand a, Operand b, v4f32 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+};
+struct Fp16 {
+    typedef v8f16 Operand;
+    template <int FMT> static __device__ __forceinline__ Operand of(uint32_t lo, uint32_t hi) {
+        v2f16 p[4];
+        if constexpr (FMT == kE4M3) {
+            p[0] = __builtin_bit_cast(v2f16, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+            p[1] = __builtin_bit_cast(v2f16, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+            p[2] = __builtin_bit_cast(v2f16, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+            p[3] = __builtin_bit_cast(v2f16, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+        } else {
+            p[0] = __builtin_bit_cast(v2f16, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(lo, 1.0f, false));
+            p[1] = __builtin_bit_cast(v2f16, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(lo, 1.0f, true));
+            p[2] = __builtin_bit_cast(v2f16, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(hi, 1.0f, false));
+            p[3] = __builtin_bit_cast(v2f16, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(hi, 1.0f, true));
+        }
+        return Operand{p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y};
+    }
+    static __device__ __forceinline__ v4f32 product(Operand a, Operand b, v4f32 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+};
+
+// An activation between the products is v 2^(E - kScaleBias), v FP16 and E a byte for sixteen neighbours: the exponent field of
+// their largest magnitude, which v holds in [2^14, 2^15), or kLeastScale (2^-126) if that is more.
+constexpr uint32_t kScaleBias = 127 + 14, kLeastScale = 15;
+__device__ __forceinline__ float scale_value(uint32_t e) { return __uint_as_float((umax(e, kLeastScale) + 127 - kScaleBias) << 23); }
 
 // 128 values of k for RT tiles of sixteen rows of a weight and up to sixteen tokens. Both are loaded in whole lines, a
 // weight eight rows to an instruction (lane l: chunk l % 8 of row l / 8), the tokens four (chunk l % 16 of token l / 16, as
@@ -146,7 +177,8 @@ __device__ __forceinline__ v8bf16 operand(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ int chunk128(int r, int c) { return r * 128 + ((c ^ (r >> 1)) & 7) * 16; }
 __device__ __forceinline__ int chunk256(int r, int c) { return r * 256 + ((c ^ r) & 15) * 16; }
 
-// The lane, computed where it is used: addresses that hang on it stay out of the registers of the loops around.
+// The lane, computed where it is used: addresses that hang on it stay out of the registers of the loops around (the first
+// kernel, whose three workgroups to a CU leave 168 to a thread; the second has registers for them).
 __device__ __forceinline__ int lane_here() {
     int lane = (int)(threadIdx.x & 63);
     asm volatile("" : "+v"(lane));
@@ -156,8 +188,8 @@ __device__ __forceinline__ int lane_here() {
 // Loaded rows into the products' layout, over the same LDS one after the other (a wave's LDS operations keep their
 // order); the registers they come from can be loaded again then.
 template <int RT>
-__device__ __forceinline__ void turn_weights(const uint4 (&w)[RT][2], char *tile, uint4 (&o)[RT][2]) {
-    const int lane = lane_here(), r = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void turn_weights(const uint4 (&w)[RT][2], char *tile, uint4 (&o)[RT][2], int lane) {
+    const int r = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -167,37 +199,53 @@ __device__ __forceinline__ void turn_weights(const uint4 (&w)[RT][2], char *tile
 #pragma unroll
         for (int h = 0; h < 2; ++h) o[t][h] = *(const uint4 *)(tile + t * 2048 + chunk128(r, g + 4 * h));
 }
-__device__ __forceinline__ void place_tokens(const uint4 (&x)[4], int instructions, char *tile) {
-    const int lane = lane_here(), r = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void place_tokens(const uint4 (&x)[4], int instructions, char *tile, int lane) {
+    const int r = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
         if (q < instructions) *(uint4 *)(tile + chunk256(4 * q + g, r)) = x[q];
 }
 
+// The scales of 128 activations of a token, a byte for each sixteen: the values move to the largest of them (what falls below
+// FP16 there is below 2^-39 of the largest value). by[h]: the factor of the lane's k in half h; returns the token's scale.
+__device__ __forceinline__ float find_scales(uint2 e, int g, _Float16 (&by)[2]) {
+    const v2u16 a = __builtin_bit_cast(v2u16, e.x & 0x00FF00FFu), b = __builtin_bit_cast(v2u16, (e.x >> 8) & 0x00FF00FFu);
+    const v2u16 c = __builtin_bit_cast(v2u16, e.y & 0x00FF00FFu), d = __builtin_bit_cast(v2u16, (e.y >> 8) & 0x00FF00FFu);
+    const v2u16 m = __builtin_elementwise_max(__builtin_elementwise_max(a, b), __builtin_elementwise_max(c, d));
+    const uint32_t most = umax(m.x, m.y);
+    by[0] = __builtin_ldexpf16((_Float16)1.0f, (int)(e.x >> 8 * g & 255) - (int)most);
+    by[1] = __builtin_ldexpf16((_Float16)1.0f, (int)(e.y >> 8 * g & 255) - (int)most);
+    return scale_value(most);
+}
+
 // Products of turned weights with placed tokens, one half of the 128 values of k after the other (the fence keeps the
 // second half's operands out of the registers meanwhile). Tokens behind the last one are what LDS held: their columns are
-// not used.
-template <int FMT, int RT>
-__device__ __forceinline__ void multiply(const uint4 (&w)[RT][2], const char *tile, const float (&inv)[RT], v4f32 (&acc)[RT]) {
-    const int lane = lane_here(), r = lane & 15, g = lane >> 4;
+// not used. f: the factor of each tile's sums, for this lane's token; by: factors of the token's values (Fp16).
+template <typename T, int FMT, int RT>
+__device__ __forceinline__ void multiply(const uint4 (&w)[RT][2], const char *tile, const float (&f)[RT], v4f32 (&acc)[RT], int lane, const _Float16 (&by)[2] = {}) {
+    const int r = lane & 15, g = lane >> 4;
     v4f32 sum[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) sum[t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const v8bf16 x0 = *(const v8bf16 *)(tile + chunk256(r, 8 * h + 2 * g));
-        const v8bf16 x1 = *(const v8bf16 *)(tile + chunk256(r, 8 * h + 2 * g + 1));
+        typename T::Operand x0 = *(const typename T::Operand *)(tile + chunk256(r, 8 * h + 2 * g));
+        typename T::Operand x1 = *(const typename T::Operand *)(tile + chunk256(r, 8 * h + 2 * g + 1));
+        if constexpr (std::is_same<T, Fp16>::value) {
+            x0 *= by[h];
+            x1 *= by[h];
+        }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FMT>(w[t][h].x, w[t][h].y), x0, sum[t], 0, 0, 0);
-            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(operand<FMT>(w[t][h].z, w[t][h].w), x1, sum[t], 0, 0, 0);
+            sum[t] = T::product(T::template of<FMT>(w[t][h].x, w[t][h].y), x0, sum[t]);
+            sum[t] = T::product(T::template of<FMT>(w[t][h].z, w[t][h].w), x1, sum[t]);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(sum[t][i], inv[t], acc[t][i]);
+        for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(sum[t][i], f[t], acc[t][i]);
 }
 
 // Weights are read past the caches where rows are whole lines; where they are not, neighbouring rows share lines, and cached
@@ -286,16 +334,16 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
                 // one sixteen of tokens: its x of two steps; two: those of the next step
                 const auto step = [&](uint4 (&from)[2][2], int s, int i) {
                     uint4 wo[2][2];
-                    turn_weights<2>(from, tile[wave], wo);
+                    turn_weights<2>(from, tile[wave], wo, lane_here());
                     const float f[2] = {__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv[0]), i)),
                                         __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv[1]), i))};
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         uint4(&xfrom)[4] = x[NC > 1 ? c : s];
-                        place_tokens(xfrom, NX, tile[wave]);
+                        place_tokens(xfrom, NX, tile[wave], lane_here());
                         load_x(xfrom, NC > 1 ? i + 1 : i + 2, c);
                         if (c + 1 == NC) load_w(from, i + 2);        // last: loads come back in their order
-                        multiply<FMT, 2>(wo, tile[wave], f, acc[c]);
+                        multiply<Bf16, FMT, 2>(wo, tile[wave], f, acc[c], lane_here());
                     }
                 };
                 load_x(x[0], 0, 0);
@@ -336,7 +384,12 @@ __global__ __launch_bounds__(kUpThreads, kUpGroups) void layer_up_kernel(LayerAr
                     }
                     const float a = act<ACT, false>(sum[0]) * sum[1];
                     const int to = (int)(jobs.entry[start + i] & 0xFFFF);
-                    p.a[(int64_t)to * p.hidden + j0 + (threadIdx.x & 15)] = (uint16_t)Eight<uint16_t>::two(a, 0.0f);
+                    const uint32_t scale = umax(max_row16(__float_as_uint(a) & 0x7FFFFFFFu) >> 23, kLeastScale);
+                    const float down = __uint_as_float((127 + kScaleBias - scale) << 23);
+                    p.a[(int64_t)to * p.hidden + j0 + (threadIdx.x & 15)] = __builtin_bit_cast(uint16_t, (_Float16)(a * down));
+                    // the last sixteen also write the zeros that fill the row to whole 128s
+                    const int u = (int)(threadIdx.x & 15), at = j0 / 16 + u, bytes = (p.hidden + 127) / 128 * 8;
+                    if (u == 0 || (j0 + 16 == p.hidden && at < bytes)) p.a_scales[(int64_t)to * bytes + at] = u == 0 ? (uint8_t)scale : 0;
                 }
             }
             __syncthreads();
@@ -373,14 +426,15 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
     __syncthreads();
     const int hidden = p.hidden, gk = (hidden + 127) / 128, gn = (p.dim + 127) / 128;
     const int column = (int)blockIdx.x / p.parts, share = (int)blockIdx.x % p.parts, d0 = column * COLS;
-    // Equal parts in time: a step of up to 32 tokens counts as one and a half of sixteen. us, 64 tokens of 7168, 8 of 64 experts, as
-    // one / one and a half / two: 487 / 469 / 469 for both kernels, of 4096, 4 of 16 experts 119 / 114 / 114.
+    // Equal parts in time: a step of up to 32 tokens counts as two of sixteen. us of both kernels, as one and a half / two: 64
+    // tokens of 7168, 8 of 64 experts 489 / 488, 40 tokens 445 / 441, 64 of 4096, 4 of 16 experts 118 / 116.5.
     const auto bound = [&](int part) {
-        const int64_t first = (int64_t)large * gk, at = (first * 3 + ((int64_t)total * gk - first) * 2) * part / (p.parts * W);
-        return (int)(at < first * 3 ? at / 3 : first + (at - first * 3) / 2);
+        const int64_t first = (int64_t)large * gk, at = (first * 2 + ((int64_t)total * gk - first)) * part / (p.parts * W);
+        return (int)(at < first * 2 ? at / 2 : at - first);
     };
     const int lo = bound(share * W + wave), hi = bound(share * W + wave + 1);
     const auto ar = make_rsrc(p.a, (uint32_t)n * (uint32_t)hidden * 2u);
+    const auto er = make_rsrc(p.a_scales, (uint32_t)n * (uint32_t)gk * 8u);
     uint32_t wrow[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t)                      // columns behind the last one: no loads
@@ -419,19 +473,22 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
             wr = make_rsrc(p.w2 + (int64_t)e * p.dim * hidden, (uint32_t)p.dim * (uint32_t)hidden);
             sr = make_rsrc(p.s2 + ((int64_t)e * gn + d0 / 128) * gk, (uint32_t)gk * 4u);
         };
-        uint32_t arow[NC][NX];
+        uint32_t arow[NC][NX], erow[NC];
         const auto place_x = [&]() {
             const uint32_t piece = piece_at(px.base + px.piece);
+            const auto row_at = [&](int at, uint32_t bytes, uint32_t more) {
+                const uint32_t row = entry[job_start(piece) + (at < job_count(piece) ? at : 0)] & 0xFFFF;
+                return at < job_count(piece) ? row * bytes + more : kOutOfRange;
+            };
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+            for (int c = 0; c < NC; ++c) {
+                erow[c] = row_at(16 * c + r, (uint32_t)gk * 8u, 0);
 #pragma unroll
-                for (int q = 0; q < NX; ++q) {
-                    const int at = 16 * c + 4 * q + g;
-                    const uint32_t row = entry[job_start(piece) + (at < job_count(piece) ? at : 0)] & 0xFFFF;
-                    arow[c][q] = at < job_count(piece) ? row * (uint32_t)hidden * 2u + 16 * r : kOutOfRange;
-                }
+                for (int q = 0; q < NX; ++q) arow[c][q] = row_at(16 * c + 4 * q + g, (uint32_t)hidden * 2u, 16 * r);
+            }
         };
         uint4 w[2][RT][2], x[2][4];
+        uint2 ex[2];
         float scale_of[2];
         v4f32 acc[NC][RT];
         const auto clear = [&]() {
@@ -453,26 +510,37 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
                     to[t][h] = buf_load16<CP>(wr, in ? wrow[t] : kOutOfRange, (uint32_t)(k0 + 8 * h * hidden));
             if (next(pw)) place_w();
         };
-        const auto load_x = [&](uint4 (&to)[4], int unit, int c) {
+        const auto load_x = [&](int s, int unit, int c) {
             const int k0 = px.block * 128;
             const bool in = unit < hi && k0 + 8 * r < hidden;
 #pragma unroll
-            for (int q = 0; q < NX; ++q) to[q] = buf_load16(ar, in ? arow[c][q] : kOutOfRange, (uint32_t)(2 * k0));
+            for (int q = 0; q < NX; ++q) x[s][q] = buf_load16(ar, in ? arow[c][q] : kOutOfRange, (uint32_t)(2 * k0));
+            const v2u32 e = __builtin_amdgcn_raw_buffer_load_b64(er, (int)(unit < hi ? erow[c] : kOutOfRange), k0 >> 4, kCached);
+            ex[s] = make_uint2(e.x, e.y);
             if (c + 1 == NC && (next(px) || px.pieces > 1)) place_x();
         };
         const auto step = [&](int s, int unit) {
             uint4 wo[RT][2];
-            turn_weights<RT>(w[s], tile[wave], wo);
+            turn_weights<RT>(w[s], tile[wave], wo, lane);
             float inv[RT];
 #pragma unroll
             for (int t = 0; t < RT; ++t) inv[t] = unit < hi ? 1.0f / scale_of[s] : 0.0f;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                uint4(&from)[4] = x[NC > 1 ? c : s];
-                place_tokens(from, NX, tile[wave]);
+                const int from = NC > 1 ? c : s;
+                place_tokens(x[from], NX, tile[wave], lane);
+                const uint2 e = ex[from];
                 load_x(from, NC > 1 ? unit + 1 : unit + 2, c);
                 if (c + 1 == NC) load_w(w[s], scale_of[s], unit + 2);
-                multiply<FMT, RT>(wo, tile[wave], inv, acc[c]);
+                _Float16 by[2];
+                const float scale = find_scales(e, g, by);
+                float f[RT];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {        // the largest value for Inf (a sum of 0 stays 0), NaN stays
+                    f[t] = inv[t] * scale;
+                    f[t] = f[t] > 3.40282346638528859812e+38f ? 3.40282346638528859812e+38f : f[t];
+                }
+                multiply<Fp16, FMT, RT>(wo, tile[wave], f, acc[c], lane, by);
             }
             if (unit < hi && (pu.pieces > 1 || pu.block + 1 == gk || unit + 1 == hi)) {
                 const uint32_t piece = piece_at(pu.base + pu.piece);
@@ -496,10 +564,10 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
         };
         place_w();
         place_x();
-        load_x(x[0], lo, 0);
-        if (NC > 1) load_x(x[1], lo, NC - 1);
+        load_x(0, lo, 0);
+        if (NC > 1) load_x(1, lo, NC - 1);
         load_w(w[0], scale_of[0], lo);
-        if (NC == 1) load_x(x[1], lo + 1, 0);
+        if (NC == 1) load_x(1, lo + 1, 0);
         load_w(w[1], scale_of[1], lo + 1);
         for (int u = lo; u < hi; u += 2) {
             step(0, u);
@@ -596,7 +664,7 @@ int launch_layer_kernels(const LayerArgs &p, hipStream_t s) {
 size_t layer_workspace(int64_t tokens, int top_k, int experts, int64_t dim, int64_t hidden) {
     const size_t n = (size_t)tokens * top_k, columns = ((size_t)dim + kDownCols - 1) / kDownCols;
     const size_t parts = down_parts(tokens, top_k, experts, dim, hidden);
-    return up16(n * hidden * 2) + up16(kMaxJobs * 4) + 2 * up16(n * 4) + 16 +
+    return up16(n * hidden * 2) + up16(n * ((hidden + 127) / 128 * 8)) + up16(kMaxJobs * 4) + 2 * up16(n * 4) + 16 +
            (parts > 1 ? up16(columns * 4) + columns * parts * tokens * kDownCols * 4 : 0);
 }
 
@@ -606,6 +674,8 @@ int launch_layer(const LayerArgs &args, int fmt, int act, void *ws, hipStream_t 
     char *at = (char *)ws;
     p.a = (uint16_t *)at;
     at += up16(n * p.hidden * 2);
+    p.a_scales = (uint8_t *)at;
+    at += up16(n * ((p.hidden + 127) / 128 * 8));
     p.jobs = (uint32_t *)at;
     at += up16(kMaxJobs * 4);
     p.entries = (uint32_t *)at;
