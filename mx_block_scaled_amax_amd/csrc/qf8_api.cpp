@@ -705,6 +705,7 @@ qf8_status rms_norm_quantize(const void *x, qf8_dtype dtype, const void *residua
     p.rows = rows; p.cols = cols; p.gcols = (cols + 127) / 128;
     p.eps = eps;
     p.inv_cols = 1.0f / (float)cols;
+    p.inv_cols_rest = (float)(1.0 / (double)cols - (double)p.inv_cols);
     p.w_fp32 = weight_dtype == QF8_IN_FP32;
     p.fmt = fmt; p.pow2 = flags & QF8_FLAG_POW2_SCALES;
     return status_of(qf8::launch_norm(p, dtype, residual_dtype, as_stream(stream)));

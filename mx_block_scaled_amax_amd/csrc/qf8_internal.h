@@ -159,7 +159,7 @@ struct NormArgs {
     void *dx;
     float *partial;              // [norm_backward_groups][cols]
     int64_t rows, cols, gcols;
-    float eps, inv_cols;         // inv_cols: 1 / cols
+    float eps, inv_cols, inv_cols_rest;  // 1 / cols in two parts
     int w_fp32, fmt, pow2;
 };
 int launch_norm(const NormArgs &p, int dtype, int residual_dtype, hipStream_t s);

@@ -36,6 +36,13 @@ __device__ __forceinline__ float sum_row(const float (&v)[C], float *red) {
     return s;
 }
 
+// 1 / sqrt(v), v normal: the hardware's root, an ulp off, and a step r + r (1 - v r^2) / 2 with v r in two parts, which leaves
+// half an ulp.
+__device__ __forceinline__ float rsqrt_rounded(float v) {
+    const float r = __builtin_amdgcn_rsqf(v), t = v * r, rest = __builtin_fmaf(v, r, -t);
+    return __builtin_fmaf(0.5f * r, __builtin_fmaf(-rest, r, __builtin_fmaf(-t, r, 1.0f)), r);
+}
+
 // A row of squares whose fp32 sum overflows: the sum of (h 2^-72)^2, at most 2^14 (2^128 2^-72)^2 = 2^126, and
 // the root in fp64. Inf and NaN among the values come through as R = 0 or NaN.
 template <int T, int V, int C>
@@ -104,9 +111,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
             for (int i = 0; i < 8; ++i) share[v % C] = __builtin_fmaf(h[v][i], h[v][i], share[v % C]);
         }
         const float ss = sum_row<T, C>(share, red[0]);
-        // the hardware's root, an ulp, and a product for the mean. us, IEEE divisions and root / this, no residual: 1 row of 7168
-        // 3.1 / 2.9, 16384 of 2056 39.4 / 37.5
-        float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_cols, p.eps));
+        // the mean as a product with 1 / cols in two parts, rounded once with eps. us, one part and the hardware's root
+        // alone / this, no residual: 1 row of 7168 3.0 / 3.1, 16384 of 2056 37.9 / 38.4 (IEEE divisions and root 39.4)
+        float rstd = rsqrt_rounded(__builtin_fmaf(ss, p.inv_cols, __builtin_fmaf(ss, p.inv_cols_rest, p.eps)));
         if (!(ss < __builtin_inff())) rstd = rstd_of_large<T, V, C>(h, red[1], cols, p.eps);
         if (p.rstd && t == 0) p.rstd[row] = rstd;
         const auto yr = row_of<TX>(p.y, row, cols, p.y != nullptr);
