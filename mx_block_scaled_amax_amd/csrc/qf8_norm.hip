@@ -43,7 +43,7 @@ __device__ __forceinline__ float rsqrt_rounded(float v) {
     return __builtin_fmaf(0.5f * r, __builtin_fmaf(-rest, r, __builtin_fmaf(-t, r, 1.0f)), r);
 }
 
-// A row of squares whose fp32 sum overflows: the sum of (h 2^-72)^2, at most 2^14 (2^128 2^-72)^2 = 2^126, and
+// A row of squares whose fp32 sum, or mean with eps, overflows: the sum of (h 2^-72)^2, at most 2^14 (2^128 2^-72)^2 = 2^126, and
 // the root in fp64. Inf and NaN among the values come through as R = 0 or NaN.
 template <int T, int V, int C>
 __device__ __forceinline__ float rstd_of_large(const float (&h)[V][8], float *red, int cols, float eps) {
@@ -113,8 +113,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
         const float ss = sum_row<T, C>(share, red[0]);
         // the mean as a product with 1 / cols in two parts, rounded once with eps. us, one part and the hardware's root
         // alone / this, no residual: 1 row of 7168 3.0 / 3.1, 16384 of 2056 37.9 / 38.4 (IEEE divisions and root 39.4)
-        float rstd = rsqrt_rounded(__builtin_fmaf(ss, p.inv_cols, __builtin_fmaf(ss, p.inv_cols_rest, p.eps)));
-        if (!(ss < __builtin_inff())) rstd = rstd_of_large<T, V, C>(h, red[1], cols, p.eps);
+        const float mean = __builtin_fmaf(ss, p.inv_cols, __builtin_fmaf(ss, p.inv_cols_rest, p.eps));
+        float rstd = rsqrt_rounded(mean);
+        if (!(mean < __builtin_inff())) rstd = rstd_of_large<T, V, C>(h, red[1], cols, p.eps);
         if (p.rstd && t == 0) p.rstd[row] = rstd;
         const auto yr = row_of<TX>(p.y, row, cols, p.y != nullptr);
         const auto qr = row_of<uint8_t>(p.q, row, cols, p.q != nullptr);

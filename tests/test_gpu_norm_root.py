@@ -21,3 +21,17 @@ def test_root(rows, cols):
         eps = float(torch.tensor(eps, dtype=torch.float32))
         want = (x.double().square().sum(1) / cols + eps).rsqrt()
         assert float(((got - want).abs() / want).max()) <= tol * (1 + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("cols,value", [(8, 6.3e18), (264, 1.1e18), (264, 1e19), (16384, 1.0)])
+def test_mean_and_eps_beyond_fp32(cols, value):
+    """The largest eps: the mean with it overflows fp32 where the sum of squares does not, or does, or is nothing beside it. R is rounded
+    once from fp64, or half an ulp from its fp32 argument: 2^-23; y has two more roundings, and its subnormals half a step 2^-150."""
+    eps = torch.finfo(torch.float32).max
+    x = torch.full((3, cols), value, device="cuda")
+    x[1] *= -0.5
+    got = qf8.rms_norm_quantize(x, torch.ones(cols, device="cuda"), None, eps=eps, want_rstd=True)
+    want = (x.double().square().mean(1) + eps).rsqrt()
+    assert bool(((got.rstd.double() - want).abs() <= 2.0 ** -23 * (1 + 2.0 ** -18) * want).all())
+    y = x.double() * want[:, None]
+    assert bool(((got.y.double() - y).abs() <= 2.0 ** -22 * y.abs() + 2.0 ** -150).all())
