@@ -519,7 +519,7 @@ qf8_status expert_layer_tokens(const void *x, int64_t tokens, int64_t dim, const
                                void *stream);
 
 /* Norm over all gradients of a step, and the gradients scaled down to a largest norm:
- *   N = sqrt(sum g^2),  c = min(1, max_norm / (N + 1e-6)),  out = rnd(g fl32(c)).
+ *   N = sqrt(sum g^2),  c = min(1, max_norm / (N + 1e-6)) in fp64,  out = rnd(g fl32(c)).
  * grads: count host entries (read before the call returns); each tensor has n >= 0 values of its dtype at g and writes n
  * values of the same type to out, which may be g itself; with out NULL in every entry (or in none) only the norm is
  * computed. N is summed in fp64 in a fixed order. norm (nullable): N as one fp32. Where N is Inf or NaN the factor is 1
@@ -535,7 +535,7 @@ typedef struct qf8_grad {
 } qf8_grad;
 
 size_t clip_grads_workspace_bytes(const qf8_grad *grads, int count);
-qf8_status clip_grads(const qf8_grad *grads, int count, float max_norm, float *norm, int32_t *nonfinite, void *ws,
+qf8_status clip_grads(const qf8_grad *grads, int count, double max_norm, float *norm, int32_t *nonfinite, void *ws,
                       size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus

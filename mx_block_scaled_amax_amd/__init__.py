@@ -118,7 +118,7 @@ def _load():
         "expert_layer_tokens_workspace_bytes": (sz, [i64, i32, i32, i64, i64]),
         "expert_layer_tokens": (i32, [vp, i64, i64, vp, vp, vp, vp, i32, i64, i32, i32, vp, vp, i32, vp, vp, sz, vp]),
         "clip_grads_workspace_bytes": (sz, [vp, i32]),
-        "clip_grads": (i32, [vp, i32, ctypes.c_float, vp, vp, vp, sz, vp]),
+        "clip_grads": (i32, [vp, i32, ctypes.c_double, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(lib, name)

@@ -781,12 +781,12 @@ size_t clip_grads_workspace_bytes(const qf8_grad *grads, int count) {
     return need < 0 ? 0 : (size_t)need;
 }
 
-qf8_status clip_grads(const qf8_grad *grads, int count, float max_norm, float *norm, int32_t *nonfinite, void *ws,
+qf8_status clip_grads(const qf8_grad *grads, int count, double max_norm, float *norm, int32_t *nonfinite, void *ws,
                       size_t ws_bytes, void *stream) {
     if (count > 0 && !grads) return QF8_ERR_NULL;
     int64_t chunk = 0;
     const int64_t need = clip_workspace(grads, count, &chunk);
-    if (need < 0 || !(max_norm > 0.0f)) return QF8_ERR_SHAPE;
+    if (need < 0 || !(max_norm > 0.0)) return QF8_ERR_SHAPE;
     int written = 0, held = 0;
     for (int i = 0; i < count; ++i) {
         const qf8_grad &g = grads[i];

@@ -141,7 +141,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_squares_kernel(ClipBatch b,
 }
 
 // N and c from the partial sums.
-__global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(const double *partial, int64_t n, float max_norm, float *norm,
+__global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(const double *partial, int64_t n, double max_norm, float *norm,
                                                                  float *factor, int32_t *nonfinite) {
     __shared__ double red[4];
     double s = 0.0;
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(const double *p
         const double total = sqrt(s);
         const bool finite = s < __builtin_inf();
         if (norm) *norm = (float)total;
-        const double c = (double)max_norm / (total + 1e-6);
+        const double c = max_norm / (total + 1e-6);
         *factor = finite && c < 1.0 ? (float)c : 1.0f;
         if (nonfinite && !finite) *nonfinite = 1;
     }
@@ -227,7 +227,7 @@ int64_t clip_chunk(int64_t total) {
     return chunk > kClipTrip ? chunk : kClipTrip;
 }
 
-int launch_clip(const qf8_grad *grads, int count, int64_t chunk, float max_norm, int write, float *norm, float *factor, double *partial,
+int launch_clip(const qf8_grad *grads, int count, int64_t chunk, double max_norm, int write, float *norm, float *factor, double *partial,
                 int32_t *nonfinite, hipStream_t s) {
     ClipBatch b;
     b.chunk = chunk;

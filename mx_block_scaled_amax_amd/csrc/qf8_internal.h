@@ -213,7 +213,7 @@ struct ClipBatch {
 };
 // Values of a workgroup for this many in all: some thousands of workgroups, so that one can join their sums.
 int64_t clip_chunk(int64_t total);
-int launch_clip(const qf8_grad *grads, int count, int64_t chunk, float max_norm, int write, float *norm, float *factor,
+int launch_clip(const qf8_grad *grads, int count, int64_t chunk, double max_norm, int write, float *norm, float *factor,
                 double *partial, int32_t *nonfinite, hipStream_t s);
 
 }  // namespace qf8
