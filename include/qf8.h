@@ -522,8 +522,9 @@ qf8_status expert_layer_tokens(const void *x, int64_t tokens, int64_t dim, const
  *   N = sqrt(sum g^2),  c = min(1, max_norm / (N + 1e-6)) in fp64,  out = rnd(g fl32(c)).
  * grads: count host entries (read before the call returns); each tensor has n >= 0 values of its dtype at g and writes n
  * values of the same type to out, which may be g itself; with out NULL in every entry (or in none) only the norm is
- * computed. N is summed in fp64 in a fixed order. norm (nullable): N as one fp32. Where N is Inf or NaN the factor is 1
- * and nonfinite (nullable) is set. max_norm > 0. Tensors at the alignment of their type (those at 16 bytes are
+ * computed. N is summed in fp64 in a fixed order, and is Inf or NaN only where a gradient is: then the factor is 1 and nonfinite
+ * (nullable) is set. norm (nullable): N as one fp32, Inf also where a finite N is beyond fp32; those gradients are scaled, and
+ * nonfinite is not set. max_norm > 0. Tensors at the alignment of their type (those at 16 bytes are
  * read faster); out overlaps no g but its own, so no tensor is given twice. count <= 2^20, n < 2^36.
  * ws: clip_grads_workspace_bytes() bytes, 16-byte aligned, no initialisation. */
 typedef struct qf8_grad {

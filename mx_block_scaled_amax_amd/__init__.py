@@ -985,14 +985,16 @@ def _clip(grads, out, max_norm, norm, nonfinite, ws, stream):
 
 def grad_norm(grads, norm=None, nonfinite=None, ws=None, stream=None):
     """sqrt of the sum of all squares of the tensors grads (BF16 or FP32, any shapes, contiguous), summed in fp64: a
-    float32 tensor of one element."""
+    float32 tensor of one element, Inf where that is beyond float32. nonfinite, an int32 tensor of one element, is set to 1 where
+    a gradient is Inf or NaN."""
     return _clip(list(grads), None, float("inf"), norm, nonfinite, ws, stream)
 
 
 def clip_grads(grads, max_norm, out=None, norm=None, nonfinite=None, ws=None, stream=None):
     """Scales the tensors grads by min(1, max_norm / (N + 1e-6)), N their grad_norm, in place or into the tensors out
-    of the same shapes and types. Where N is not finite they are left as they are (copied to out) and nonfinite,
-    an int32 tensor of one element, is set to 1. Returns N, a float32 tensor of one element; nothing is read back to the host."""
+    of the same shapes and types (out overlaps no gradient but its own). Where a gradient is Inf or NaN they are left as they are
+    (copied to out) and nonfinite, an int32 tensor of one element, is set to 1. Returns N, a float32 tensor of one element, Inf also
+    where finite gradients have a norm beyond float32 (they are scaled, by N in fp64); nothing is read back to the host."""
     grads = list(grads)
     if out is None:
         out = grads

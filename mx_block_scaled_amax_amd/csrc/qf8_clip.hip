@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(const double *p
     for (int64_t i = threadIdx.x; i < n; i += kClipThreads) s += partial[i];
     s = sum_block_f64(s, red);
     if (threadIdx.x == 0) {
-        const double total = sqrt(s);
+        const double total = sqrt(s);                 // beyond fp32 perhaps, beyond fp64 only where a value is
         const bool finite = s < __builtin_inf();
         if (norm) *norm = (float)total;
         const double c = max_norm / (total + 1e-6);
