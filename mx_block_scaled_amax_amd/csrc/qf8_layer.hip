@@ -407,7 +407,7 @@ constexpr int kDownWaves = 8, kDownThreads = 64 * kDownWaves, kDownTiles = 2, kD
 template <int FMT, int CP>
 __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p) {
     constexpr int W = kDownWaves, RT = kDownTiles, COLS = kDownCols;
-    extern __shared__ float sums[];                   // [waves][tokens][COLS], then the list
+    extern __shared__ __align__(16) float sums[];     // [waves][tokens][COLS], then the list
     __shared__ __align__(16) char tile[W][4096];
     __shared__ int arrived;
     const int n = p.tokens * p.top_k, total = p.job_count[0], large = p.job_count[1];
