@@ -510,7 +510,8 @@ qf8_status gated_act_backward(const void *dy, const void *x, qf8_dtype dtype, in
  * id outside [0, experts) adds nothing, one that a token has twice counts with the sum of its weights. The same
  * call gives the same bits. tokens <= 64, tokens * top_k <= 1024, experts <= 1024, top_k <= 64; dim, hidden
  * multiples of 16 and <= 32768. Tensors and ws 16-byte aligned, scales, ids and weights 4-byte; y overlaps no input.
- * ws: expert_layer_tokens_workspace_bytes() bytes, no initialisation. dim and hidden that are multiples of 128 keep the
+ * ws: expert_layer_tokens_workspace_bytes() bytes, no initialisation. More tokens go through the products
+ * (matmul_block_experts), which are faster there than calls of 64 tokens each. dim and hidden that are multiples of 128 keep the
  * weights' rows on whole lines, which reads them faster. */
 size_t expert_layer_tokens_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t dim, int64_t hidden);
 qf8_status expert_layer_tokens(const void *x, int64_t tokens, int64_t dim, const uint8_t *w1, const float *s1,

@@ -914,7 +914,8 @@ def expert_layer_tokens(x, w1, s1, w2, s2, ids, weights, fmt, act=ACT_SILU, y=No
     """A whole expert layer for at most 64 tokens: y[t] = sum_j weights[t][j] W2[e] (act(A x[t]) * (B x[t])) with
     W1[e] = [A; B] and e = ids[t][j] (an id outside the experts adds nothing). x [tokens][dim] bfloat16; w1 codes [experts]
     [2 hidden][dim] and w2 codes [experts][dim][hidden] with their 128x128 scales; ids and weights as route_experts gives
-    them. The activations are not quantized. Returns y [tokens][dim] bfloat16."""
+    them. The activations are not quantized. Returns y [tokens][dim] bfloat16. For more tokens the products
+    (matmul_block_experts) are faster than calls of 64 each."""
     tokens, dim = _need(x, "x", torch.bfloat16, 2)
     device = x.get_device()
     experts, both, d1 = _need(w1, "w1", torch.uint8, 3, device)

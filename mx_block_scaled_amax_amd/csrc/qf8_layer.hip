@@ -249,7 +249,7 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[RT][2], const char *ti
 }
 
 // Weights are read past the caches where rows are whole lines; where they are not, neighbouring rows share lines, and cached
-// loads take them once: 13 tokens of 2064, 40 experts, hidden 720 53 -> 46 us.
+// loads take them once: 13 tokens x 6 of 40 experts, 2064, hidden 720 46.3 -> 44.1 us, 64 x 4 of 16, 4112, hidden 2000 156 -> 144.
 constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64, kUpGroups = 3;      // workgroups to a CU
 
 // A workgroup takes sixteen hidden units of a job, 16 rows of A_e and 16 of B_e; its waves share k, wave w the blocks
@@ -623,8 +623,8 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
 int launched() { return hipGetLastError() == hipSuccess ? QF8_OK : QF8_ERR_HIP; }
 
 // Shares of the second kernel's columns: the fewest that fill three quarters of the CUs in every round of workgroups (or the
-// most of them), with two steps at least for each wave that may have some. us, one share / this: 13 tokens of 2048, hidden 768
-// 19.4 / 14.8 (4 shares), 64 of 4096, hidden 2048 115 / 107 (2), 64 of 4112, hidden 2000 211 / 175 (3).
+// most of them), with two steps at least for each wave that may have some. us of the second kernel, one share / this: 13 tokens x 6
+// of 40 experts, 2048, hidden 768 27.1 / 15.4 (4 shares), 64 x 4 of 16, 4096, hidden 2048 61 / 41 (2), 4112, hidden 2000 74.5 / 67 (3).
 int down_parts(int64_t tokens, int top_k, int experts, int64_t dim, int64_t hidden) {
     const int64_t columns = (dim + kDownCols - 1) / kDownCols, n = tokens * top_k;
     const int64_t steps = (n < experts ? n : experts) * ((hidden + 127) / 128), most = steps / (2 * kDownWaves);
