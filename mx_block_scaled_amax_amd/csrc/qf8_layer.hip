@@ -536,7 +536,9 @@ __global__ __launch_bounds__(kDownThreads, 2) void layer_down_kernel(LayerArgs p
                 const float scale = find_scales(e, g, by);
                 float f[RT];
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {        // the largest value for Inf (a sum of 0 stays 0), NaN stays
+                // The largest value for Inf (a sum of 0 stays 0), NaN stays. Below 2^-126 it has fewer bits, nine where the largest
+                // product of the 128, 2^23 times it, is 2^-117: BF16's own are next to their end there.
+                for (int t = 0; t < RT; ++t) {
                     f[t] = inv[t] * scale;
                     f[t] = f[t] > 3.40282346638528859812e+38f ? 3.40282346638528859812e+38f : f[t];
                 }

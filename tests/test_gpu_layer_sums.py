@@ -91,3 +91,19 @@ def test_activations_of_any_size_side_by_side(fmt, hidden):
     ids, weights = torch.ones(5, 1, dtype=torch.int32, device="cuda"), torch.ones(5, 1, device="cuda")
     y = qf8.expert_layer_tokens(x, w1, s1, w2, s2, ids, weights, fmt).double()
     assert torch.equal(y, 93 * power[None] * x[:, 1:2].double())
+
+
+@pytest.mark.parametrize("fmt", [qf8.E4M3, qf8.E5M2])
+def test_activations_and_scales_of_any_size(fmt):
+    """93 x 2^p under scales 2^s, from small by large to large by small: exact. One call for each s, one token for each p."""
+    eye = torch.zeros(32, 32, dtype=torch.uint8, device="cuda")
+    eye[range(32), range(32)] = 0x38 if fmt == qf8.E4M3 else 0x3C
+    w1, s1, w2, _ = one_unit(fmt, eye)
+    for s in (-100, -70, -30, 0, 30, 70, 100, 120):
+        powers = [p for p in range(-118, 119, 4) if -118 <= p - s <= 118]
+        x = torch.zeros(len(powers), 32, dtype=BF, device="cuda")
+        x[:, 0], x[:, 1] = 93.0, torch.tensor([2.0 ** p for p in powers], dtype=torch.float64).to(BF).cuda()
+        ids, weights = torch.zeros(len(powers), 1, dtype=torch.int32, device="cuda"), torch.ones(len(powers), 1, device="cuda")
+        y = qf8.expert_layer_tokens(x, w1, s1, w2, torch.full((1, 1, 1), 2.0 ** s, device="cuda"), ids, weights, fmt).double()
+        want = torch.tensor([93 * 2.0 ** (p - s) for p in powers], dtype=torch.float64).cuda()[:, None].expand(-1, 32)
+        assert torch.equal(y, want), s
