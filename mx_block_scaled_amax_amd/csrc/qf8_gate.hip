@@ -19,7 +19,7 @@ template <typename TX>
 __device__ __forceinline__ void leave(const GateArgs &p, const float *y, bool ok, int64_t at, int64_t group) {
     const uint32_t amax = group_amax(y);
     const bool first = (threadIdx.x & 15) == 0 && ok;
-    if (p.nonfinite && first && amax >= 0x7F800000u) *p.nonfinite = 1;
+    if (p.nonfinite && first && amax >= (p.y ? kNotFinite<TX> : kNotFinite<float>)) *p.nonfinite = 1;
     if (p.y && ok) {
         Eight<TX> e;
         e.round(y);

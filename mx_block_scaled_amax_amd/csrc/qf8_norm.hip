@@ -137,7 +137,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rms_norm_kernel(NormArgs p)
             for (int i = 0; i < 8; ++i) y[i] = h[v][i] * rstd * w[i];
             const uint32_t amax = group_amax(y, col < cols);       // behind the columns 0 times R, which may be NaN
             const bool first = (threadIdx.x & 15) == 0 && col < cols;
-            if (p.nonfinite && first && amax >= 0x7F800000u) *p.nonfinite = 1;
+            if (p.nonfinite && first && amax >= (p.y ? kNotFinite<TX> : kNotFinite<float>)) *p.nonfinite = 1;
             if (p.y) {
                 Eight<TX> e;
                 e.round(y);

@@ -76,6 +76,8 @@ __device__ __forceinline__ uint32_t group_amax(const float *y, bool there = true
     for (int i = 0; i < 8; ++i) m = umax(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
     return max_row16(there ? m : 0);
 }
+// Bits of the magnitudes that are Inf or NaN once rounded to T: BF16's Inf begins at 255.5 2^120.
+template <typename T> constexpr uint32_t kNotFinite = sizeof(T) == 2 ? 0x7F7F8000u : 0x7F800000u;
 // The group's scale and this lane's eight codes.
 __device__ __forceinline__ float group_scale(uint32_t amax, int fmt, int pow2) {
     if (fmt == kE4M3) return pow2 ? scale_pow2_from_amax_bits<kE4M3>(amax) : scale_from_amax_bits<kE4M3>(amax);
